@@ -1,0 +1,130 @@
+/*
+ * attention.h — C ABI of the attention kernels for MI355X (gfx950): attention
+ * over packed sequences, its backward pass, and the per-head norm of queries
+ * and keys with the position rotation, forward and backward.  They stand
+ * between the query/key/value projection and the output projection of
+ * gemm_fwd.h and take the projection's output in place, as strided views.
+ *
+ * Attention.  `tokens` rows hold sequences one behind the other: sequence b
+ * is rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1, or all rows are one
+ * sequence when cu_seqlens is NULL.  Row i sees row j of its own sequence
+ * when, with causal, j <= i, and, with window > 0, |i - j| < window (every
+ * row sees itself).  Query head h reads key/value head h / (q_heads /
+ * kv_heads).  For every row i and query head:
+ *
+ *   s_ij   = scale q_i . k_j                 over the visible j
+ *   lse_i  = log sum_j exp(s_ij)             (natural logarithm)
+ *   out_i  = sum_j exp(s_ij - lse_i) v_j
+ *
+ * and the backward pass, from dout and the forward's out and lse:
+ *
+ *   p_ij = exp(s_ij - lse_i), delta_i = dout_i . out_i,
+ *   ds_ij = p_ij (dout_i . v_j - delta_i)
+ *   dq_i = scale sum_j ds_ij k_j
+ *   dk_j = scale sum_{heads of the group, i} ds_ij q_i
+ *   dv_j = sum_{heads of the group, i} p_ij dout_i
+ *
+ * Rows in front of cu_seqlens[0] and from cu_seqlens[num_seqs] on belong to
+ * no sequence: they are not read, and their out, dq, dk and dv are zero and
+ * their lse is minus infinity.  Nothing passes between sequences, whatever
+ * the rows of another one or of none hold; inside a sequence a NaN or an
+ * infinity can reach all of its rows.  cu_seqlens must not decrease; entries
+ * outside [0, tokens] are clamped to it and a decreasing entry reads as an
+ * empty sequence (the results are then unspecified, but no access leaves the
+ * arrays).
+ *
+ * Norm and rotation.  For every token t and head, with r = rsqrt(mean_d
+ * x[d]^2 + eps) over the head's head_dim values:
+ *
+ *   n[d] = x[d] r weight[d]
+ *   (y_a, y_b) = (n_a cos - n_b sin, n_b cos + n_a sin),
+ *       angle = positions[t] inv_freq[p]     for pair p < rotated / 2
+ *
+ * where pair p is (p, p + rotated / 2), or (2p, 2p + 1) when interleaved,
+ * and y = n from `rotated` on.  The angle is formed and reduced in 64 bits.
+ * The backward pass gives dx from dy, and the weight's gradient summed over
+ * tokens and heads:
+ *
+ *   dn = the inverse rotation of dy, g = dn weight
+ *   dx[d] = r (g[d] - x[d] r mean(g x r)), dweight[d] = sum dn[d] x[d] r
+ *
+ * Layout: a tensor [tokens, heads, head_dim] of fp32 is given by its first
+ * element and the strides of a token and of a head in elements; a head's
+ * values are contiguous.  Token strides are at least head_dim, base
+ * addresses are 16-byte aligned and strides multiples of 4.  lse is
+ * [q_heads, tokens], dense.  All device pointers are owned by the caller; a
+ * call allocates nothing and only enqueues work on `stream` (a hipStream_t,
+ * NULL for the null stream).  Every sum has a fixed order: results are
+ * bitwise reproducible.
+ *
+ * Errors are returned synchronously, before anything is enqueued (the status
+ * values are those of gemm_fwd.h).
+ */
+#ifndef ATTENTION_H
+#define ATTENTION_H
+
+#include <stdint.h>
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* A [tokens, heads, head_dim] fp32 tensor: strides in elements. */
+typedef struct attn_tensor {
+    void *data;
+    int64_t token_stride;
+    int64_t head_stride;
+} attn_tensor;
+
+/* The sizes and the mask of an attention call. */
+typedef struct attn_problem {
+    const int32_t *cu_seqlens; /* [num_seqs + 1] device array, or NULL: one sequence of all tokens */
+    int64_t num_seqs;          /* ignored when cu_seqlens is NULL */
+    int64_t tokens;
+    int64_t q_heads;
+    int64_t kv_heads;          /* divides q_heads */
+    int64_t head_dim;          /* a multiple of 4, 4 to 128 */
+    int64_t causal;            /* 0 or 1 */
+    int64_t window;            /* 0: none */
+    double scale;              /* positive and finite */
+} attn_problem;
+
+/*
+ * out and lse from q, k, v.  out may be the very same tensor as q; it may
+ * not overlap q otherwise, nor k, v, lse or cu_seqlens.
+ *
+ * GEMM_ERR_NULL for a missing array, GEMM_ERR_SHAPE for sizes outside the
+ * above (tokens < 2^30, heads <= 65535, num_seqs < 2^24) or strides that are
+ * too small, overlap an output's own elements or reach 2^22 elements from one
+ * token to the next, GEMM_ERR_ALIGN, GEMM_ERR_DTYPE for a scale that is not
+ * positive and finite or a causal that is neither 0 nor 1, GEMM_ERR_ALIAS,
+ * and GEMM_ERR_LAUNCH when the runtime rejects the launch.  tokens == 0
+ * enqueues nothing.
+ */
+typedef struct attn_forward_args {
+    attn_problem p;
+    attn_tensor q, k, v, out;
+    float *lse;
+} attn_forward_args;
+int attn_forward(const attn_forward_args *args, void *stream);
+
+/*
+ * dq, dk, dv from dout, q, k, v and the forward's out and lse.  delta is
+ * scratch of q_heads * tokens floats; its contents need not be kept.  No
+ * output may overlap another array of the call (views of one buffer whose
+ * elements do not overlap are fine).
+ */
+typedef struct attn_backward_args {
+    attn_problem p;
+    attn_tensor dout, q, k, v, out;
+    const float *lse;
+    float *delta;
+    attn_tensor dq, dk, dv;
+} attn_backward_args;
+int attn_backward(const attn_backward_args *args, void *stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* ATTENTION_H */

@@ -1,4 +1,4 @@
-"""Python binding over libgemmfwd.so (the C ABI declared in include/gemm_fwd.h).
+"""Python binding over libgemmfwd.so (the C ABI declared in include/*.h).
 
 Argument marshalling only: shapes, dtypes and devices are checked, pointers and
 the current HIP stream are passed through, and every step of the computation
@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -28,8 +29,8 @@ EXPORTED = (
     "gemm_matmul_at_swiglu_a_ex", "gemm_bwd_num_configs", "gemm_bwd_config_name", "gemm_bwd_select_config",
     "gemm_bwd_workspace_bytes", "gemm_matmul_t_swiglu_bwd", "gemm_matmul_t_swiglu_bwd_ex",
     "loss_cross_entropy", "loss_sum_losses", "act_ffn_swiglu_backward", "act_ffn_gelu_backward",
-    "act_gelu_inplace", "gemm_timing_event_create", "gemm_timing_event_record", "gemm_timing_elapsed_ms",
-    "gemm_timing_event_destroy",
+    "act_gelu_inplace", "attn_forward", "attn_backward",
+    "gemm_timing_event_create", "gemm_timing_event_record", "gemm_timing_elapsed_ms", "gemm_timing_event_destroy",
 )
 
 
@@ -129,6 +130,9 @@ def _open(path):
     lib.act_ffn_gelu_backward.restype = c_int
     lib.act_gelu_inplace.argtypes = [p, p, i64, p]
     lib.act_gelu_inplace.restype = c_int
+    for name in ("attn_forward", "attn_backward"):
+        getattr(lib, name).argtypes = [ctypes.c_char_p, p]  # the packed argument struct, the stream
+        getattr(lib, name).restype = c_int
     lib.gemm_timing_event_create.argtypes = [ctypes.POINTER(ctypes.c_void_p)]
     lib.gemm_timing_event_create.restype = c_int
     lib.gemm_timing_event_record.argtypes = [p, p]
@@ -580,3 +584,135 @@ def gelu_inplace(x, pre_gelu=None):
     if st != 0:
         raise GemmError(st, "act_gelu_inplace")
     return x
+
+
+# --- attention (include/attention.h) ---
+#
+# The argument structs of attention.h are packed field by field: every field
+# is 8 bytes wide (pointers, int64_t, double).
+
+_FORWARD_ARGS = struct.Struct("=8qd 12q q")
+_BACKWARD_ARGS = struct.Struct("=8qd 15q 2q 9q")
+
+
+def _call_packed(name, args, device):
+    """Enqueue `name` on `device`'s current stream, with that device current."""
+    fn = getattr(load_library(), name)
+    if device.index == torch.cuda.current_device():
+        st = fn(args, torch.cuda.current_stream(device).cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            st = fn(args, torch.cuda.current_stream(device).cuda_stream)
+    if st != 0:
+        raise GemmError(st, name)
+
+
+def _heads(t, name, shape, device):
+    """(pointer, token stride, head stride) of the [tokens, heads, head_dim] tensor t."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device != device or device.type != "cuda":
+        raise ValueError(f"{name} must live on {device if device.type == 'cuda' else 'a GPU'}, got {t.device}")
+    if t.dtype != torch.float32:
+        raise TypeError(f"{name} must be float32, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    st, sh, sd = t.stride()
+    if sd != 1 and shape[2] > 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+    return t.data_ptr(), st, sh
+
+
+def _row_values(t, name, shape, device):
+    """Pointer of a dense float32 [heads, tokens] tensor."""
+    if not isinstance(t, torch.Tensor) or t.device != device or t.dtype != torch.float32 or t.shape != shape \
+            or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous float32 tensor of shape {tuple(shape)} on {device}")
+    return t.data_ptr()
+
+
+def _attn_problem(q, k, cu_seqlens, causal, window, scale):
+    """The fields of attn_problem, and the shapes of q and of k and v."""
+    for name, t in (("q", q), ("k", k)):
+        if not isinstance(t, torch.Tensor) or t.dim() != 3:
+            raise TypeError(f"{name} must be a 3-D torch.Tensor [tokens, heads, head_dim]")
+    tokens, hq, dim = shape_q = q.shape
+    hkv = k.shape[1]
+    if hq < 1 or hkv < 1 or hq % hkv:
+        raise ValueError(f"{hq} query heads do not share {hkv} key/value heads evenly")
+    cu, nseq = 0, 0
+    if cu_seqlens is not None:
+        if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 or cu_seqlens.device != q.device \
+                or cu_seqlens.shape[0] < 1 or not cu_seqlens.is_contiguous():
+            raise ValueError(f"cu_seqlens must be a contiguous 1-D tensor of at least one entry on {q.device}")
+        if cu_seqlens.dtype != torch.int32:
+            raise TypeError(f"cu_seqlens must be int32, got {cu_seqlens.dtype}")
+        cu, nseq = cu_seqlens.data_ptr(), cu_seqlens.shape[0] - 1
+    if window < 0:
+        raise ValueError(f"window must not be negative, got {window}")
+    if scale is None:
+        scale = dim ** -0.5 if dim else 1.0
+    return (cu, nseq, tokens, hq, hkv, dim, 1 if causal else 0, int(window), float(scale)), shape_q, (tokens, hkv, dim)
+
+
+def attention(q, k, v, cu_seqlens=None, causal=True, window=0, scale=None, out=None, lse=None):
+    """Attention over packed sequences: out = softmax(scale q k^T over the
+    visible keys) v, and lse, the logarithm of each row's sum of exponentials,
+    which attention_backward needs.
+
+    q [tokens, q_heads, head_dim], k and v [tokens, kv_heads, head_dim]
+    float32 (q_heads a multiple of kv_heads, head_dim a multiple of 4 up to
+    128), contiguous along the head with any strides that are multiples of 4,
+    so the projection's output is taken as views.  cu_seqlens, int32
+    [sequences + 1] on the device: sequence b is rows cu_seqlens[b] to
+    cu_seqlens[b + 1] - 1 (None: all rows are one sequence); rows of no
+    sequence get out 0 and lse -inf.  A row sees the rows of its sequence, up
+    to itself with causal, less than `window` away with window > 0.  scale
+    defaults to head_dim ** -0.5.  out may be q itself.
+    Returns (out like q, lse [q_heads, tokens])."""
+    problem, shape_q, shape_k = _attn_problem(q, k, cu_seqlens, causal, window, scale)
+    device = q.device
+    tq = _heads(q, "q", shape_q, device)
+    tk = _heads(k, "k", shape_k, device)
+    tv = _heads(v, "v", shape_k, device)
+    tokens, hq, _ = shape_q
+    if out is None:
+        out = torch.empty(shape_q, dtype=torch.float32, device=device)
+    to = _heads(out, "out", shape_q, device)
+    if lse is None:
+        lse = torch.empty((hq, tokens), dtype=torch.float32, device=device)
+    pl = _row_values(lse, "lse", (hq, tokens), device)
+    _call_packed("attn_forward", _FORWARD_ARGS.pack(*problem, *tq, *tk, *tv, *to, pl), device)
+    return out, lse
+
+
+def attention_backward(dout, q, k, v, out, lse, cu_seqlens=None, causal=True, window=0, scale=None, dq=None, dk=None,
+                       dv=None):
+    """Gradients of attention: dq, dk, dv from dout, its inputs, and the out
+    and lse it returned (the probabilities are formed again from lse).
+    Arguments as for attention; dq, dk and dv may be views of one buffer, but
+    may not overlap an input.  Rows of no sequence get zero gradients.
+    Returns (dq, dk, dv)."""
+    problem, shape_q, shape_k = _attn_problem(q, k, cu_seqlens, causal, window, scale)
+    device = q.device
+    tg = _heads(dout, "dout", shape_q, device)
+    tq = _heads(q, "q", shape_q, device)
+    tk = _heads(k, "k", shape_k, device)
+    tv = _heads(v, "v", shape_k, device)
+    to = _heads(out, "out", shape_q, device)
+    rows = (shape_q[1], shape_q[0])
+    pl = _row_values(lse, "lse", rows, device)
+    if dq is None:
+        dq = torch.empty(shape_q, dtype=torch.float32, device=device)
+    if dk is None:
+        dk = torch.empty(shape_k, dtype=torch.float32, device=device)
+    if dv is None:
+        dv = torch.empty(shape_k, dtype=torch.float32, device=device)
+    tdq = _heads(dq, "dq", shape_q, device)
+    tdk = _heads(dk, "dk", shape_k, device)
+    tdv = _heads(dv, "dv", shape_k, device)
+    # scratch of this call's own: two captured graphs share nothing
+    delta = torch.empty(rows, dtype=torch.float32, device=device)
+    _call_packed("attn_backward", _BACKWARD_ARGS.pack(*problem, *tg, *tq, *tk, *tv, *to, pl, delta.data_ptr(), *tdq,
+                                                      *tdk, *tdv), device)
+    return dq, dk, dv

@@ -13,6 +13,8 @@ ROOT = os.path.dirname(PKG)
 SRC = os.path.join(PKG, "csrc", "gemm_fwd.hip")
 LOSS_SRC = os.path.join(PKG, "csrc", "loss.hip")
 ACT_SRC = os.path.join(PKG, "csrc", "activation.hip")
+ATTN_SRC = os.path.join(PKG, "csrc", "attention.hip")
+SRCS = [SRC, LOSS_SRC, ACT_SRC, ATTN_SRC]
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libgemmfwd.so")
 SYNC_LIB = os.path.join(PKG, "libgemmfwd_sync.so")
@@ -37,16 +39,16 @@ def _hipcc(srcs, lib: str, verbose: bool, defines=()) -> str:
 
 
 def build_library(verbose: bool = False) -> str:
-    """The library: the GEMM family (forward and backward), the fused loss and
-    the FFN activation kernels."""
-    return _hipcc([SRC, LOSS_SRC, ACT_SRC], LIB, verbose)
+    """The library: the GEMM family (forward and backward), the fused loss, the
+    FFN activation kernels and the attention kernels."""
+    return _hipcc(SRCS, LIB, verbose)
 
 
 def build_sync_check_library(verbose: bool = False) -> str:
     """The verification build of the same sources (GEMM_SYNC_CHECK: full
     waits before every barrier, fences around the split-K exchange), which
     the race-check tests compare bit for bit with the shipping library."""
-    return _hipcc([SRC, LOSS_SRC, ACT_SRC], SYNC_LIB, verbose, defines=("GEMM_SYNC_CHECK",))
+    return _hipcc(SRCS, SYNC_LIB, verbose, defines=("GEMM_SYNC_CHECK",))
 
 
 def build_probe(verbose: bool = False) -> str:

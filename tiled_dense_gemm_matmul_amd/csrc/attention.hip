@@ -1,0 +1,898 @@
+// Attention over packed sequences for MI355X (gfx950), forward and backward,
+// in fp32 on v_mfma_f32_16x16x4_f32 (definitions in attention.h).
+//
+// The work is bound by the fp32 matrix instructions: 4 D flops a visible
+// (row, key) pair and head forward, and 14 D backward, where the scores and
+// the products with dout are formed twice, once for dq with the rows held
+// fixed and once for dk and dv with the keys held fixed.  (Forming them once
+// is 10 D flops, but then dq or dk and dv would be summed by atomics, whose
+// order changes results, or kept as [tokens, tokens] arrays.)
+//
+//  * No operand passes through LDS.  A wave holds 16 rows (or keys) in
+//    registers and walks over blocks of 16 of the other side, whose operands
+//    it loads from memory straight into the registers that the MFMA reads;
+//    the four waves of a workgroup walk over the same blocks close together,
+//    so most of these loads hit the CU's L1.
+//  * The probabilities never leave the registers either.  A 16 x 16 product
+//    leaves lane (g, m) = (lane / 16, lane % 16) with its rows 4g .. 4g + 3
+//    of column m.  That is the B operand of the next product when its
+//    contraction step i takes row 4g + i from lane group g, so the scores are
+//    formed with the side that is contracted next as their rows: keys for
+//    out and dq, query rows for dk and dv.
+//  * The other operand of that product is read along the head: lane (g, m)
+//    takes the 4 consecutive values 64c + 4m .. + 3 of row 4g + i with one
+//    16-byte load, which serve as row m of four MFMA tiles.  Result tile
+//    4c + e then holds dimension 64c + 4m + e in its row m, so a lane ends up
+//    with 16 consecutive values of a row's result.
+//  * Loads are buffer loads whose descriptor starts at the block's first row
+//    and ends at its last row in the sequence, so rows past it and head
+//    values past head_dim read as zeros, and offsets stay small however long
+//    the buffer is.
+//
+// A workgroup owns a tile of rows of one sequence and one head.  Where there
+// are enough tiles for the chip its waves own 16 rows each (WS = 1); with
+// fewer, all of them own the same rows, take every WS-th block of the
+// other side and are joined through LDS in wave order (WS = 4).
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "attention.h"
+#include "gemm_fwd.h"
+
+namespace {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned int u32x4v __attribute__((vector_size(16)));
+typedef unsigned int u32x2v __attribute__((vector_size(8)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __amdgpu_buffer_rsrc_t Rsrc;
+
+constexpr int kOOB = (int)0x80000000u;  // past every descriptor's end (they end below 2^31)
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
+// The running maximum of a row that has seen no key yet: low enough that any
+// score replaces it, finite so that differences with it are not NaN.
+constexpr float kNoMax = -3.0e38f;
+
+struct Strided {
+    float *p;
+    int64_t st, sh;
+};
+
+struct Problem {
+    const int *cu;
+    int nseq, tokens, hq, group, d, causal, window, tiles;
+    float scale, c;  // c = scale log2(e): scores go through exp2
+};
+
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// Rows [row, end) of a head, at most N of them, as a buffer.
+template <int N>
+__device__ __forceinline__ Rsrc rows_rsrc(const float *base, int64_t st, int row, int end, int d) {
+    const int n = min(end - row, N);
+    const int bytes = n > 0 ? (int)(((n - 1) * st + d) * 4) : 0;
+    return __builtin_amdgcn_make_buffer_rsrc((void *)(base + row * st), (short)0, bytes, 0x00020000);
+}
+
+__device__ __forceinline__ f32x4 load4(Rsrc r, int off) {
+    return __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+}
+__device__ __forceinline__ f32x2 load2(Rsrc r, int off) {
+    return __builtin_bit_cast(f32x2, __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 0));
+}
+__device__ __forceinline__ void store4(Rsrc r, int off, f32x4 v) {
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4v, v), r, off, 0, 0);
+}
+__device__ __forceinline__ f32x4 mfma(float a, float b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
+}
+
+// 16 rows of a head with lane (g, m) holding values 16j + 4g .. + 3 of row m:
+// the A or B operand of a product contracted along the head.
+template <int DP>
+struct Rows {
+    static constexpr int NJ = DP / 16;
+    f32x4 x[NJ];
+
+    // byte offset of this lane's first value; col(j) past head_dim is out of range
+    template <bool EX>
+    __device__ __forceinline__ void load(Rsrc r, int64_t st, int d) {
+        const int lane = threadIdx.x & 63, g = lane >> 4, m = lane & 15;
+        const int at = m * (int)st * 4 + g * 16;
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) x[j] = load4(r, (EX || 16 * j + 4 * g < d) ? at + 64 * j : kOOB);
+    }
+};
+
+// 16 rows of a head with lane (g, m) holding, of rows 4g + i, the values that
+// are row m of the MFMA tiles: 4 of them for each 64 of the head, 2 for a
+// last 32.  The A operand of a product contracted over the rows.
+template <int DP>
+struct Cols {
+    static constexpr int N4 = DP / 64, N2 = DP % 64 / 32;
+    f32x4 x[4][N4 > 0 ? N4 : 1];
+    f32x2 y[4];
+
+    template <bool EX>
+    __device__ __forceinline__ void load(Rsrc r, int64_t st, int d) {
+        const int lane = threadIdx.x & 63, g = lane >> 4, m = lane & 15;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int row = (4 * g + i) * (int)st * 4;
+#pragma unroll
+            for (int c = 0; c < N4; ++c) x[i][c] = load4(r, (EX || 64 * c + 4 * m < d) ? row + 256 * c + 16 * m : kOOB);
+            if (N2) y[i] = load2(r, (EX || 64 * N4 + 2 * m < d) ? row + 256 * N4 + 8 * m : kOOB);
+        }
+    }
+    // the value of row 4g + i that belongs to MFMA tile t
+    __device__ __forceinline__ float at(int i, int t) const { return t < 4 * N4 ? x[i][t / 4][t % 4] : y[i][t % 2]; }
+};
+
+// The transposed result of 16 rows, [dimension, row], in DP / 16 MFMA tiles.
+template <int DP>
+struct Acc {
+    static constexpr int NT = DP / 16, N4 = DP / 64, N2 = DP % 64 / 32;
+    f32x4 t[NT];
+
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < NT; ++i) t[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+    __device__ __forceinline__ void mul(float f) {
+#pragma unroll
+        for (int i = 0; i < NT; ++i) t[i] *= f;
+    }
+    // += cols^T p, one row of p a register
+    __device__ __forceinline__ void add(const Cols<DP> &a, f32x4 p) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < NT; ++j) t[j] = mfma(a.at(i, j), p[i], t[j]);
+    }
+    // Calls f(first dimension, 4 consecutive values) for all of the lane's
+    // values of row m.
+    template <class F>
+    __device__ __forceinline__ void each4(F f) const {
+        const int g = (threadIdx.x & 63) >> 4;
+#pragma unroll
+        for (int c = 0; c < N4; ++c)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                f(64 * c + 16 * g + 4 * i, f32x4{t[4 * c][i], t[4 * c + 1][i], t[4 * c + 2][i], t[4 * c + 3][i]});
+        if (N2) {
+#pragma unroll
+            for (int i = 0; i < 4; i += 2)
+                f(64 * N4 + 8 * g + 2 * i, f32x4{t[NT - 2][i], t[NT - 1][i], t[NT - 2][i + 1], t[NT - 1][i + 1]});
+        }
+    }
+};
+
+// [rows of a, rows of b] scores: += a b^T.
+template <int DP>
+__device__ __forceinline__ f32x4 dots(const Rows<DP> &a, const Rows<DP> &b) {
+    f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int j = 0; j < DP / 16; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s = mfma(a.x[j][e], b.x[j][e], s);
+    return s;
+}
+
+// Sum over the four lane groups (lanes of one m).
+__device__ __forceinline__ float group_sum(float v) {
+    v += __shfl_xor(v, 16, 64);
+    return v + __shfl_xor(v, 32, 64);
+}
+__device__ __forceinline__ float group_max(float v) {
+    v = fmaxf(v, __shfl_xor(v, 16, 64));
+    return fmaxf(v, __shfl_xor(v, 32, 64));
+}
+
+// The sequence [s0, s1) and the first row of tile x of TILE rows, each
+// sequence cut into tiles by itself.  Sequence bounds are clamped to the
+// buffer.  Returns false when there is no such tile.  With `back`, a
+// sequence's tiles are taken from its end, where a causal row sees most.
+template <int TILE>
+__device__ __forceinline__ bool find_tile(const Problem &p, int x, bool back, int &s0, int &s1, int &r0) {
+    auto clamp = [&](int v) { return max(0, min(v, p.tokens)); };
+    int n = 0;
+    if (p.nseq <= 1) {
+        s0 = p.cu ? uniform(p.nseq ? clamp(p.cu[0]) : 0) : 0;
+        s1 = p.cu ? uniform(p.nseq ? max(s0, clamp(p.cu[1])) : 0) : p.tokens;
+        n = (s1 - s0 + TILE - 1) / TILE;
+        if (x >= n) return false;
+    } else {
+        const int lane = threadIdx.x & 63;
+        int b = 0;
+        for (;; b += 64) {
+            if (b >= p.nseq) return false;
+            const bool in = b + lane < p.nseq;
+            const int lo = in ? clamp(p.cu[b + lane]) : 0;
+            const int hi = in ? max(lo, clamp(p.cu[b + lane + 1])) : 0;
+            const int mine = (hi - lo + TILE - 1) / TILE;
+            int upto = mine;  // tiles of the sequences up to this lane's
+#pragma unroll
+            for (int o = 1; o < 64; o <<= 1) {
+                const int v = __shfl_up(upto, o, 64);
+                if (lane >= o) upto += v;
+            }
+            const uint64_t past = __ballot(upto > x);
+            if (past) {
+                const int at = __builtin_ctzll(past);
+                s0 = __builtin_amdgcn_readlane(lo, at);
+                s1 = __builtin_amdgcn_readlane(hi, at);
+                n = __builtin_amdgcn_readlane(mine, at);
+                x -= __builtin_amdgcn_readlane(upto, at) - n;
+                break;
+            }
+            x -= __builtin_amdgcn_readlane(upto, 63);
+        }
+    }
+    r0 = s0 + (back ? n - 1 - x : x) * TILE;
+    return true;
+}
+
+// Workgroups reach the 8 XCDs in turn; renumbered so that each XCD, with its
+// own L2, gets neighbouring tiles of neighbouring heads.
+__device__ __forceinline__ int xcd_order(int id, int total) {
+    const int xcd = id & 7, per = total >> 3, rest = total & 7;
+    return xcd * per + min(xcd, rest) + (id >> 3);
+}
+
+// Zeroes this workgroup's share of the rows that belong to no sequence: rows
+// [x TILE, x TILE + TILE) in front of the first sequence or behind the last.
+template <int TILE, class F>
+__device__ __forceinline__ void outside_rows(const Problem &p, int x, F f) {
+    if (!p.cu) return;
+    const int first = uniform(max(0, min(p.cu[0], p.tokens)));
+    const int last = uniform(max(first, min(p.cu[p.nseq], p.tokens)));
+    const int64_t a = (int64_t)x * TILE;
+    if (a >= p.tokens) return;
+    const int b = (int)min(a + TILE, (int64_t)p.tokens);
+    if (a >= first && b <= last) return;
+    for (int r = (int)a + (int)(threadIdx.x >> 6); r < b; r += blockDim.x >> 6)
+        if (r < first || r >= last) f(r);
+}
+__device__ __forceinline__ void zero_row(float *row, int d) {
+    for (int i = threadIdx.x & 63; i < d; i += 64) row[i] = 0.0f;
+}
+
+// Which keys a block of rows may see.
+struct Range {
+    int lo, hi;
+};
+__device__ __forceinline__ Range keys_of(const Problem &p, int s0, int s1, int r0, int n) {
+    const int last = min(r0 + n, s1) - 1;
+    Range k = {s0, s1};
+    if (p.window) k.lo = max(s0, r0 - p.window + 1);
+    if (p.causal) k.hi = last + 1;
+    else if (p.window) k.hi = (int)min((int64_t)s1, (int64_t)last + p.window);
+    return k;
+}
+// Which rows may see a block of keys.
+__device__ __forceinline__ Range rows_of(const Problem &p, int s0, int s1, int k0, int n) {
+    const int last = min(k0 + n, s1) - 1;
+    Range r = {s0, s1};
+    if (p.causal) r.lo = k0;
+    else if (p.window) r.lo = max(s0, k0 - p.window + 1);
+    if (p.window) r.hi = (int)min((int64_t)s1, (int64_t)last + p.window);
+    return r;
+}
+__device__ __forceinline__ bool sees(const Problem &p, int i, int j) {
+    return (!p.causal || j <= i) && (!p.window || (i - j < p.window && j - i < p.window));
+}
+// Whether rows [r, r + n) of the sequence all see keys [k, k + m), both whole inside it.
+__device__ __forceinline__ bool all_see(const Problem &p, int s1, int r, int n, int k, int m) {
+    if (r + n > s1 || k + m > s1) return false;
+    if (p.causal && k + m - 1 > r) return false;
+    return !p.window || ((int64_t)r + n - 1 - k < p.window && (int64_t)k + m - 1 - r < p.window);
+}
+
+// --- forward ---
+//
+// Online softmax over blocks of 16 keys.  The reference value of a row is
+// moved, and the sums rescaled, only when a score exceeds it by 2^8: the
+// probabilities then stay below 2^8 of the reference, which fp32 holds
+// without loss, and most blocks need neither the maximum across lanes nor
+// the rescaling.
+template <int DP, bool EX, int RB, int WS>
+__global__ __launch_bounds__(256, 2) void attention_fwd(Problem p, Strided q, Strided k, Strided v, Strided o,
+                                                        float *lse) {
+    constexpr int WROWS = 16 * RB, TILE = WS == 1 ? 4 * WROWS : WROWS;
+    const int lane = threadIdx.x & 63, g = lane >> 4, m = lane & 15;
+    const int wave = uniform(threadIdx.x >> 6);
+    const int id = xcd_order(blockIdx.x, gridDim.x);
+    const int h = id / p.tiles, x = id - h * p.tiles;
+    outside_rows<TILE>(p, x, [&](int r) {
+        zero_row(o.p + r * o.st + h * o.sh, p.d);
+        if (lane == 0) lse[(int64_t)h * p.tokens + r] = -INFINITY;
+    });
+    int s0, s1, t0;
+    if (!find_tile<TILE>(p, x, p.causal, s0, s1, t0)) return;
+    const int r0 = t0 + (WS == 1 ? wave * WROWS : 0);
+    if (WS == 1 && r0 >= s1) return;
+    const float *kp = k.p + (h / p.group) * k.sh, *vp = v.p + (h / p.group) * v.sh;
+
+    Rows<DP> Q[RB];
+    Acc<DP> O[RB];
+    float top[RB], sum[RB];
+#pragma unroll
+    for (int b = 0; b < RB; ++b) {
+        Q[b].template load<EX>(rows_rsrc<16>(q.p + h * q.sh, q.st, r0 + 16 * b, s1, p.d), q.st, p.d);
+        O[b].clear();
+        top[b] = kNoMax;
+        sum[b] = 0.0f;
+    }
+    const Range kr = keys_of(p, s0, s1, r0, WROWS);
+    const int step = WS == 1 ? 16 : 16 * WS;
+    int kb = kr.lo + (WS == 1 ? 0 : 16 * wave);
+    Rows<DP> K;
+    Cols<DP> V;
+    K.template load<EX>(rows_rsrc<16>(kp, k.st, kb, s1, p.d), k.st, p.d);
+    V.template load<EX>(rows_rsrc<16>(vp, v.st, kb, s1, p.d), v.st, p.d);
+    for (; kb < kr.hi; kb += step) {
+        f32x4 s[RB];
+#pragma unroll
+        for (int b = 0; b < RB; ++b) s[b] = dots<DP>(K, Q[b]);
+        K.template load<EX>(rows_rsrc<16>(kp, k.st, kb + step, s1, p.d), k.st, p.d);
+        __builtin_amdgcn_sched_barrier(0);
+        if (!all_see(p, s1, r0, WROWS, kb, 16)) {
+#pragma unroll
+            for (int b = 0; b < RB; ++b)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int key = kb + 4 * g + i;
+                    if (key >= s1 || !sees(p, r0 + 16 * b + m, key)) s[b][i] = -INFINITY;
+                }
+        }
+#pragma unroll
+        for (int b = 0; b < RB; ++b) {
+            const float most = fmaxf(fmaxf(s[b][0], s[b][1]), fmaxf(s[b][2], s[b][3])) * p.c;
+            if (__any(most > top[b] + 8.0f)) {
+                const float to = fmaxf(top[b], group_max(most));
+                const float f = __builtin_amdgcn_exp2f(top[b] - to);
+                top[b] = to;
+                sum[b] *= f;
+                O[b].mul(f);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                s[b][i] = __builtin_amdgcn_exp2f(fmaf(s[b][i], p.c, -top[b]));
+                sum[b] += s[b][i];
+            }
+            O[b].add(V, s[b]);
+        }
+        V.template load<EX>(rows_rsrc<16>(vp, v.st, kb + step, s1, p.d), v.st, p.d);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int b = 0; b < RB; ++b) sum[b] = group_sum(sum[b]);
+
+    if (WS == 1) {
+#pragma unroll
+        for (int b = 0; b < RB; ++b) {
+            const int r = r0 + 16 * b;
+            if (r >= s1) break;
+            const Rsrc ro = rows_rsrc<16>(o.p + h * o.sh, o.st, r, s1, p.d);
+            const float inv = 1.0f / sum[b];
+            O[b].each4([&](int d0, f32x4 y) {
+                store4(ro, (EX || d0 < p.d) ? m * (int)o.st * 4 + d0 * 4 : kOOB, y * inv);
+            });
+            if (g == 0 && r + m < s1)
+                lse[(int64_t)h * p.tokens + r + m] = (top[b] + __builtin_amdgcn_logf(sum[b])) * kLn2;
+        }
+    } else {
+        // join the waves, in wave order
+        static_assert(RB == 1 || WS == 1, "joined waves hold 16 rows");
+        constexpr int LD = DP + 4;
+        __shared__ __align__(16) float part[WS == 1 ? 1 : WS][WS == 1 ? 1 : 16 * LD];
+        __shared__ float ptop[WS][16], psum[WS][16];
+        O[0].each4([&](int d0, f32x4 y) { *(f32x4 *)&part[wave][m * LD + d0] = y; });
+        if (g == 0) {
+            ptop[wave][m] = top[0];
+            psum[wave][m] = sum[0];
+        }
+        __syncthreads();
+        const int row = threadIdx.x >> 4, e = threadIdx.x & 15;
+        if (r0 + row >= s1) return;
+        float to = ptop[0][row], total = 0.0f, f[WS];
+#pragma unroll
+        for (int w = 1; w < WS; ++w) to = fmaxf(to, ptop[w][row]);
+#pragma unroll
+        for (int w = 0; w < WS; ++w) {
+            f[w] = __builtin_amdgcn_exp2f(ptop[w][row] - to);
+            total += f[w] * psum[w][row];
+        }
+        const float inv = 1.0f / total;
+        float *dst = o.p + (int64_t)(r0 + row) * o.st + h * o.sh;
+#pragma unroll
+        for (int c = 0; c < (DP + 63) / 64; ++c) {
+            const int d0 = 64 * c + 4 * e;
+            if (d0 < p.d) {
+                f32x4 y = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int w = 0; w < WS; ++w) y += f[w] * *(const f32x4 *)&part[w][row * LD + d0];
+                *(f32x4 *)(dst + d0) = y * inv;
+            }
+        }
+        if (e == 0) lse[(int64_t)h * p.tokens + r0 + row] = (to + __builtin_amdgcn_logf(total)) * kLn2;
+    }
+}
+
+// --- backward: dq, and delta for the other kernel ---
+template <int DP, bool EX, int RB, int WS>
+__global__ __launch_bounds__(256, 2) void attention_bwd_dq(Problem p, Strided dout, Strided q, Strided k, Strided v,
+                                                           Strided o, const float *lse, float *delta, Strided dq) {
+    constexpr int WROWS = 16 * RB, TILE = WS == 1 ? 4 * WROWS : WROWS;
+    const int lane = threadIdx.x & 63, g = lane >> 4, m = lane & 15;
+    const int wave = uniform(threadIdx.x >> 6);
+    const int id = xcd_order(blockIdx.x, gridDim.x);
+    const int h = id / p.tiles, x = id - h * p.tiles;
+    outside_rows<TILE>(p, x, [&](int r) { zero_row(dq.p + r * dq.st + h * dq.sh, p.d); });
+    int s0, s1, t0;
+    if (!find_tile<TILE>(p, x, p.causal, s0, s1, t0)) return;
+    const int r0 = t0 + (WS == 1 ? wave * WROWS : 0);
+    if (WS == 1 && r0 >= s1) return;
+    const float *kp = k.p + (h / p.group) * k.sh, *vp = v.p + (h / p.group) * v.sh;
+
+    Rows<DP> Q[RB], G[RB];
+    Acc<DP> A[RB];
+    float l2[RB], del[RB];
+#pragma unroll
+    for (int b = 0; b < RB; ++b) {
+        const int r = r0 + 16 * b;
+        Q[b].template load<EX>(rows_rsrc<16>(q.p + h * q.sh, q.st, r, s1, p.d), q.st, p.d);
+        G[b].template load<EX>(rows_rsrc<16>(dout.p + h * dout.sh, dout.st, r, s1, p.d), dout.st, p.d);
+        Rows<DP> out;
+        out.template load<EX>(rows_rsrc<16>(o.p + h * o.sh, o.st, r, s1, p.d), o.st, p.d);
+        f32x4 dot = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int j = 0; j < DP / 16; ++j) dot += G[b].x[j] * out.x[j];
+        del[b] = group_sum((dot[0] + dot[1]) + (dot[2] + dot[3]));
+        const int64_t at = (int64_t)h * p.tokens + r + m;
+        l2[b] = r + m < s1 ? lse[at] * kLog2e : 0.0f;
+        if (g == 0 && r + m < s1 && (WS == 1 || wave == 0)) delta[at] = del[b];
+        A[b].clear();
+    }
+    const Range kr = keys_of(p, s0, s1, r0, WROWS);
+    const int step = WS == 1 ? 16 : 16 * WS;
+    int kb = kr.lo + (WS == 1 ? 0 : 16 * wave);
+    Rows<DP> K, V;
+    Cols<DP> T;
+    K.template load<EX>(rows_rsrc<16>(kp, k.st, kb, s1, p.d), k.st, p.d);
+    V.template load<EX>(rows_rsrc<16>(vp, v.st, kb, s1, p.d), v.st, p.d);
+    T.template load<EX>(rows_rsrc<16>(kp, k.st, kb, s1, p.d), k.st, p.d);
+    for (; kb < kr.hi; kb += step) {
+        f32x4 s[RB], dp[RB];
+#pragma unroll
+        for (int b = 0; b < RB; ++b) s[b] = dots<DP>(K, Q[b]);
+        K.template load<EX>(rows_rsrc<16>(kp, k.st, kb + step, s1, p.d), k.st, p.d);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int b = 0; b < RB; ++b) dp[b] = dots<DP>(V, G[b]);
+        V.template load<EX>(rows_rsrc<16>(vp, v.st, kb + step, s1, p.d), v.st, p.d);
+        __builtin_amdgcn_sched_barrier(0);
+        const bool whole = all_see(p, s1, r0, WROWS, kb, 16);
+#pragma unroll
+        for (int b = 0; b < RB; ++b) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                s[b][i] = __builtin_amdgcn_exp2f(fmaf(s[b][i], p.c, -l2[b])) * (dp[b][i] - del[b]);
+            if (!whole) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int key = kb + 4 * g + i;
+                    if (key >= s1 || !sees(p, r0 + 16 * b + m, key)) s[b][i] = 0.0f;
+                }
+            }
+            A[b].add(T, s[b]);
+        }
+        T.template load<EX>(rows_rsrc<16>(kp, k.st, kb + step, s1, p.d), k.st, p.d);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+
+    if (WS == 1) {
+#pragma unroll
+        for (int b = 0; b < RB; ++b) {
+            const int r = r0 + 16 * b;
+            if (r >= s1) break;
+            const Rsrc ro = rows_rsrc<16>(dq.p + h * dq.sh, dq.st, r, s1, p.d);
+            A[b].each4([&](int d0, f32x4 y) {
+                store4(ro, (EX || d0 < p.d) ? m * (int)dq.st * 4 + d0 * 4 : kOOB, y * p.scale);
+            });
+        }
+    } else {
+        static_assert(RB == 1 || WS == 1, "joined waves hold 16 rows");
+        constexpr int LD = DP + 4;
+        __shared__ __align__(16) float part[WS == 1 ? 1 : WS][WS == 1 ? 1 : 16 * LD];
+        A[0].each4([&](int d0, f32x4 y) { *(f32x4 *)&part[wave][m * LD + d0] = y; });
+        __syncthreads();
+        const int row = threadIdx.x >> 4, e = threadIdx.x & 15;
+        if (r0 + row >= s1) return;
+        float *dst = dq.p + (int64_t)(r0 + row) * dq.st + h * dq.sh;
+#pragma unroll
+        for (int c = 0; c < (DP + 63) / 64; ++c) {
+            const int d0 = 64 * c + 4 * e;
+            if (d0 < p.d) {
+                f32x4 y = *(const f32x4 *)&part[0][row * LD + d0];
+#pragma unroll
+                for (int w = 1; w < WS; ++w) y += *(const f32x4 *)&part[w][row * LD + d0];
+                *(f32x4 *)(dst + d0) = y * p.scale;
+            }
+        }
+    }
+}
+
+// --- backward: dk and dv ---
+//
+// The keys are held fixed and the blocks of 16 rows of every query head of
+// the group are walked over, in the order of the heads.
+template <int DP, bool EX, int RB, int WS>
+__global__ __launch_bounds__(256, 2) void attention_bwd_dkv(Problem p, Strided dout, Strided q, Strided k, Strided v,
+                                                            const float *lse, const float *delta, Strided dk,
+                                                            Strided dv) {
+    constexpr int WROWS = 16 * RB, TILE = WS == 1 ? 4 * WROWS : WROWS;
+    const int lane = threadIdx.x & 63, g = lane >> 4, m = lane & 15;
+    const int wave = uniform(threadIdx.x >> 6);
+    const int id = xcd_order(blockIdx.x, gridDim.x);
+    const int h = id / p.tiles, x = id - h * p.tiles;
+    outside_rows<TILE>(p, x, [&](int r) {
+        zero_row(dk.p + r * dk.st + h * dk.sh, p.d);
+        zero_row(dv.p + r * dv.st + h * dv.sh, p.d);
+    });
+    int s0, s1, t0;
+    if (!find_tile<TILE>(p, x, false, s0, s1, t0)) return;
+    const int k0 = t0 + (WS == 1 ? wave * WROWS : 0);
+    if (WS == 1 && k0 >= s1) return;
+
+    Rows<DP> K[RB], V[RB];
+    Acc<DP> DK[RB], DV[RB];
+#pragma unroll
+    for (int b = 0; b < RB; ++b) {
+        K[b].template load<EX>(rows_rsrc<16>(k.p + h * k.sh, k.st, k0 + 16 * b, s1, p.d), k.st, p.d);
+        V[b].template load<EX>(rows_rsrc<16>(v.p + h * v.sh, v.st, k0 + 16 * b, s1, p.d), v.st, p.d);
+        DK[b].clear();
+        DV[b].clear();
+    }
+    const Range rr = rows_of(p, s0, s1, k0, WROWS);
+    const int blocks = (rr.hi - rr.lo + 15) / 16, total = blocks * p.group;
+    // block n of the walk: head n / blocks of the group, rows from rr.lo + 16 (n % blocks)
+    int n = WS == 1 ? 0 : wave, qh = 0, qb = n;
+    const int step = WS == 1 ? 1 : WS;
+    while (blocks > 0 && qb >= blocks) {
+        qb -= blocks;
+        ++qh;
+    }
+    Rows<DP> Q, G;
+    Cols<DP> QT, GT;
+    f32x4 l4, d4;
+    const float *qp, *gp;
+    int r;
+    auto at = [&]() {
+        const int head = h * p.group + qh;
+        const bool in = n < total;
+        qp = q.p + head * q.sh;
+        gp = dout.p + head * dout.sh;
+        r = in ? rr.lo + 16 * qb : s1;
+    };
+    auto stats = [&](const float *from) {
+        const int left = r < s1 ? s1 - r : 0;
+        return load4(__builtin_amdgcn_make_buffer_rsrc((void *)(from + (int64_t)(h * p.group + qh) * p.tokens + r),
+                                                       (short)0, min(left, 16) * 4, 0x00020000),
+                     16 * g);
+    };
+    at();
+    Q.template load<EX>(rows_rsrc<16>(qp, q.st, r, s1, p.d), q.st, p.d);
+    G.template load<EX>(rows_rsrc<16>(gp, dout.st, r, s1, p.d), dout.st, p.d);
+    l4 = stats(lse);
+    d4 = stats(delta);
+    GT.template load<EX>(rows_rsrc<16>(gp, dout.st, r, s1, p.d), dout.st, p.d);
+    QT.template load<EX>(rows_rsrc<16>(qp, q.st, r, s1, p.d), q.st, p.d);
+    while (n < total) {
+        const int row = r;
+        n += step;
+        qb += step;
+        while (qb >= blocks) {
+            qb -= blocks;
+            ++qh;
+        }
+        at();
+        f32x4 s[RB], dp[RB];
+#pragma unroll
+        for (int b = 0; b < RB; ++b) s[b] = dots<DP>(Q, K[b]);
+        Q.template load<EX>(rows_rsrc<16>(qp, q.st, r, s1, p.d), q.st, p.d);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int b = 0; b < RB; ++b) dp[b] = dots<DP>(G, V[b]);
+        G.template load<EX>(rows_rsrc<16>(gp, dout.st, r, s1, p.d), dout.st, p.d);
+        __builtin_amdgcn_sched_barrier(0);
+        const bool whole = all_see(p, s1, row, 16, k0, WROWS);
+        const f32x4 l2 = l4 * kLog2e;
+#pragma unroll
+        for (int b = 0; b < RB; ++b) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                s[b][i] = __builtin_amdgcn_exp2f(fmaf(s[b][i], p.c, -l2[i]));
+                dp[b][i] = s[b][i] * (dp[b][i] - d4[i]);
+            }
+            if (!whole) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int qi = row + 4 * g + i;
+                    if (qi >= s1 || !sees(p, qi, k0 + 16 * b + m)) s[b][i] = dp[b][i] = 0.0f;
+                }
+            }
+        }
+        l4 = stats(lse);
+        d4 = stats(delta);
+#pragma unroll
+        for (int b = 0; b < RB; ++b) DV[b].add(GT, s[b]);
+        GT.template load<EX>(rows_rsrc<16>(gp, dout.st, r, s1, p.d), dout.st, p.d);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int b = 0; b < RB; ++b) DK[b].add(QT, dp[b]);
+        QT.template load<EX>(rows_rsrc<16>(qp, q.st, r, s1, p.d), q.st, p.d);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+
+    if (WS == 1) {
+#pragma unroll
+        for (int b = 0; b < RB; ++b) {
+            const int r1 = k0 + 16 * b;
+            if (r1 >= s1) break;
+            const Rsrc rk = rows_rsrc<16>(dk.p + h * dk.sh, dk.st, r1, s1, p.d);
+            const Rsrc rv = rows_rsrc<16>(dv.p + h * dv.sh, dv.st, r1, s1, p.d);
+            DK[b].each4([&](int d0, f32x4 y) {
+                store4(rk, (EX || d0 < p.d) ? m * (int)dk.st * 4 + d0 * 4 : kOOB, y * p.scale);
+            });
+            DV[b].each4([&](int d0, f32x4 y) {
+                store4(rv, (EX || d0 < p.d) ? m * (int)dv.st * 4 + d0 * 4 : kOOB, y);
+            });
+        }
+    } else {
+        static_assert(RB == 1 || WS == 1, "joined waves hold 16 keys");
+        constexpr int LD = DP + 4;
+        __shared__ __align__(16) float part[2][WS == 1 ? 1 : WS][WS == 1 ? 1 : 16 * LD];
+        DK[0].each4([&](int d0, f32x4 y) { *(f32x4 *)&part[0][wave][m * LD + d0] = y; });
+        DV[0].each4([&](int d0, f32x4 y) { *(f32x4 *)&part[1][wave][m * LD + d0] = y; });
+        __syncthreads();
+        const int row = threadIdx.x >> 4, e = threadIdx.x & 15;
+        if (k0 + row >= s1) return;
+        float *dst[2] = {dk.p + (int64_t)(k0 + row) * dk.st + h * dk.sh, dv.p + (int64_t)(k0 + row) * dv.st + h * dv.sh};
+        const float f[2] = {p.scale, 1.0f};
+#pragma unroll
+        for (int a = 0; a < 2; ++a)
+#pragma unroll
+            for (int c = 0; c < (DP + 63) / 64; ++c) {
+                const int d0 = 64 * c + 4 * e;
+                if (d0 < p.d) {
+                    f32x4 y = *(const f32x4 *)&part[a][0][row * LD + d0];
+#pragma unroll
+                    for (int w = 1; w < WS; ++w) y += *(const f32x4 *)&part[a][w][row * LD + d0];
+                    *(f32x4 *)(dst[a] + d0) = y * f[a];
+                }
+            }
+    }
+}
+
+// --- host ---
+
+bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+struct View {
+    const attn_tensor *t;
+    int64_t heads;
+    bool output;
+};
+
+// Bytes from the first to behind the last element.
+int64_t extent(const View &v, int64_t tokens, int64_t d) {
+    return ((tokens - 1) * v.t->token_stride + (v.heads - 1) * v.t->head_stride + d) * 4;
+}
+
+// Whether two tensors may share an element.  Tensors in separate ranges do
+// not; nor do views of one buffer with the same token stride whose spans
+// within a token's row lie apart.
+bool overlap(const View &a, const View &b, int64_t tokens, int64_t d) {
+    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.t->data), b0 = reinterpret_cast<uintptr_t>(b.t->data);
+    if (a0 >= b0 + (uintptr_t)extent(b, tokens, d) || b0 >= a0 + (uintptr_t)extent(a, tokens, d)) return false;
+    const int64_t st = a.t->token_stride * 4;
+    const int64_t sa = ((a.heads - 1) * a.t->head_stride + d) * 4, sb = ((b.heads - 1) * b.t->head_stride + d) * 4;
+    if (a.t->token_stride != b.t->token_stride || sa > st || sb > st) return true;
+    const int64_t from_a = (int64_t)(((int64_t)(b0 - a0) % st + st) % st);
+    return from_a < sa || from_a + sb > st;
+}
+
+bool in_range(const View &v, const void *p, int64_t bytes, int64_t tokens, int64_t d) {
+    const uintptr_t a0 = reinterpret_cast<uintptr_t>(v.t->data), b0 = reinterpret_cast<uintptr_t>(p);
+    return p != nullptr && a0 < b0 + (uintptr_t)bytes && b0 < a0 + (uintptr_t)extent(v, tokens, d);
+}
+
+constexpr int64_t kMaxTokens = (int64_t)1 << 30, kMaxStride = (int64_t)1 << 22, kMaxHeadStride = (int64_t)1 << 40;
+
+int check_tensor(const View &v, int64_t tokens, int64_t d) {
+    if (v.t->data == nullptr) return GEMM_ERR_NULL;
+    const int64_t st = v.t->token_stride, sh = v.t->head_stride;
+    if (st < 0 || sh < 0 || sh > kMaxHeadStride) return GEMM_ERR_SHAPE;
+    if (tokens > 1 && (st < d || st >= kMaxStride)) return GEMM_ERR_SHAPE;
+    if (v.output && v.heads > 1) {
+        // an output's rows may not overlap: heads inside a token's row, or tokens inside a head
+        const bool inside = sh >= d && (tokens == 1 || st >= (v.heads - 1) * sh + d);
+        if (!inside && sh < (tokens - 1) * st + d) return GEMM_ERR_SHAPE;
+    }
+    if (!aligned(v.t->data, 16) || (tokens > 1 && st % 4) || (v.heads > 1 && sh % 4)) return GEMM_ERR_ALIGN;
+    return GEMM_OK;
+}
+
+int check_problem(const attn_problem &p) {
+    if (p.tokens < 0 || p.tokens >= kMaxTokens || p.q_heads < 1 || p.q_heads > 65535 || p.kv_heads < 1 ||
+        p.kv_heads > p.q_heads || p.q_heads % p.kv_heads || p.head_dim < 4 || p.head_dim > 128 || p.head_dim % 4 ||
+        p.window < 0)
+        return GEMM_ERR_SHAPE;
+    if (p.cu_seqlens && (p.num_seqs < 0 || p.num_seqs >= ((int64_t)1 << 24))) return GEMM_ERR_SHAPE;
+    if (!(p.scale > 0.0) || !std::isfinite((float)p.scale) || !((float)p.scale > 0.0f) ||
+        (p.causal != 0 && p.causal != 1))
+        return GEMM_ERR_DTYPE;
+    if (!aligned(p.cu_seqlens, 4)) return GEMM_ERR_ALIGN;
+    return GEMM_OK;
+}
+
+Problem device_problem(const attn_problem &a) {
+    Problem p;
+    p.cu = a.cu_seqlens;
+    p.nseq = a.cu_seqlens ? (int)a.num_seqs : 1;
+    p.tokens = (int)a.tokens;
+    p.hq = (int)a.q_heads;
+    p.group = (int)(a.q_heads / a.kv_heads);
+    p.d = (int)a.head_dim;
+    p.causal = (int)a.causal;
+    p.window = a.window < a.tokens ? (int)a.window : 0;  // a wider window hides nothing
+    p.scale = (float)a.scale;
+    p.c = (float)(a.scale * 1.44269504088896340736);
+    p.tiles = 0;
+    return p;
+}
+
+Strided strided(const attn_tensor &t, int64_t tokens, int64_t heads) {
+    // the stride of an axis of one element is never stepped over
+    return {static_cast<float *>(t.data), tokens > 1 ? t.token_stride : 0, heads > 1 ? t.head_stride : 0};
+}
+
+// Tiles of `tile` rows a head: every sequence's own, and enough for the rows of none.
+int64_t tiles_of(const attn_problem &p, int64_t tile) {
+    const int64_t whole = (p.tokens + tile - 1) / tile;
+    return p.cu_seqlens ? std::max(whole, p.tokens / tile + p.num_seqs) : whole;
+}
+
+// Waves that own 64 rows a workgroup when that gives every CU two workgroups,
+// else joined waves on 16.
+bool joined(const attn_problem &p, int64_t heads) { return (p.tokens / 64) * heads < 512; }
+
+#define ATTN_BY_DIM(LAUNCH)                                                     \
+    do {                                                                        \
+        const int64_t d_ = a.p.head_dim;                                        \
+        if (d_ == 32) LAUNCH(32, true);                                         \
+        else if (d_ < 32) LAUNCH(32, false);                                    \
+        else if (d_ == 64) LAUNCH(64, true);                                    \
+        else if (d_ < 64) LAUNCH(64, false);                                    \
+        else if (d_ == 96) LAUNCH(96, true);                                    \
+        else if (d_ < 96) LAUNCH(96, false);                                    \
+        else if (d_ == 128) LAUNCH(128, true);                                  \
+        else LAUNCH(128, false);                                                \
+    } while (0)
+
+}  // namespace
+
+extern "C" {
+
+int attn_forward(const attn_forward_args *args, void *stream) {
+    if (args == nullptr) return GEMM_ERR_NULL;
+    const attn_forward_args &a = *args;
+    const int64_t T = a.p.tokens, D = a.p.head_dim;
+    int st = check_problem(a.p);
+    if (st != GEMM_OK) return st;
+    if (T == 0) return GEMM_OK;
+    const View q = {&a.q, a.p.q_heads, false}, k = {&a.k, a.p.kv_heads, false}, v = {&a.v, a.p.kv_heads, false},
+               o = {&a.out, a.p.q_heads, true};
+    for (const View *x : {&q, &k, &v, &o})
+        if ((st = check_tensor(*x, T, D)) != GEMM_OK) return st;
+    if (a.lse == nullptr) return GEMM_ERR_NULL;
+    if (!aligned(a.lse, 4)) return GEMM_ERR_ALIGN;
+    const bool in_place = a.out.data == a.q.data && a.out.token_stride == a.q.token_stride &&
+                          a.out.head_stride == a.q.head_stride;
+    const int64_t lse_bytes = a.p.q_heads * T * 4, cu_bytes = (a.p.num_seqs + 1) * 4;
+    if ((!in_place && overlap(o, q, T, D)) || overlap(o, k, T, D) || overlap(o, v, T, D) ||
+        in_range(o, a.lse, lse_bytes, T, D) || in_range(q, a.lse, lse_bytes, T, D) ||
+        in_range(k, a.lse, lse_bytes, T, D) || in_range(v, a.lse, lse_bytes, T, D) ||
+        in_range(o, a.p.cu_seqlens, cu_bytes, T, D))
+        return GEMM_ERR_ALIAS;
+    Problem p = device_problem(a.p);
+    const bool join = joined(a.p, a.p.q_heads);
+    p.tiles = (int)tiles_of(a.p, join ? 16 : 64);
+    const int64_t grid = (int64_t)p.tiles * a.p.q_heads;
+    if (grid >= ((int64_t)1 << 31)) return GEMM_ERR_SHAPE;
+    const Strided sq = strided(a.q, T, a.p.q_heads), sk = strided(a.k, T, a.p.kv_heads),
+                  sv = strided(a.v, T, a.p.kv_heads), so = strided(a.out, T, a.p.q_heads);
+    hipStream_t hs = static_cast<hipStream_t>(stream);
+#define FWD(DP, EX)                                                                                              \
+    do {                                                                                                          \
+        if (join)                                                                                                 \
+            hipLaunchKernelGGL((attention_fwd<DP, EX, 1, 4>), dim3((unsigned)grid), dim3(256), 0, hs, p, sq, sk, \
+                               sv, so, a.lse);                                                                    \
+        else                                                                                                      \
+            hipLaunchKernelGGL((attention_fwd<DP, EX, 1, 1>), dim3((unsigned)grid), dim3(256), 0, hs, p, sq, sk, \
+                               sv, so, a.lse);                                                                    \
+    } while (0)
+    ATTN_BY_DIM(FWD);
+#undef FWD
+    return hipGetLastError() == hipSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
+}
+
+int attn_backward(const attn_backward_args *args, void *stream) {
+    if (args == nullptr) return GEMM_ERR_NULL;
+    const attn_backward_args &a = *args;
+    const int64_t T = a.p.tokens, D = a.p.head_dim, HQ = a.p.q_heads, HK = a.p.kv_heads;
+    int st = check_problem(a.p);
+    if (st != GEMM_OK) return st;
+    if (T == 0) return GEMM_OK;
+    const View in[5] = {{&a.dout, HQ, false}, {&a.q, HQ, false}, {&a.k, HK, false}, {&a.v, HK, false}, {&a.out, HQ, false}};
+    const View res[3] = {{&a.dq, HQ, true}, {&a.dk, HK, true}, {&a.dv, HK, true}};
+    for (const View &x : in)
+        if ((st = check_tensor(x, T, D)) != GEMM_OK) return st;
+    for (const View &x : res)
+        if ((st = check_tensor(x, T, D)) != GEMM_OK) return st;
+    if (a.lse == nullptr || a.delta == nullptr) return GEMM_ERR_NULL;
+    if (!aligned(a.lse, 4) || !aligned(a.delta, 4)) return GEMM_ERR_ALIGN;
+    const int64_t row_bytes = HQ * T * 4, cu_bytes = (a.p.num_seqs + 1) * 4;
+    for (int i = 0; i < 3; ++i) {
+        for (const View &x : in)
+            if (overlap(res[i], x, T, D)) return GEMM_ERR_ALIAS;
+        for (int j = 0; j < i; ++j)
+            if (overlap(res[i], res[j], T, D)) return GEMM_ERR_ALIAS;
+        if (in_range(res[i], a.lse, row_bytes, T, D) || in_range(res[i], a.delta, row_bytes, T, D) ||
+            in_range(res[i], a.p.cu_seqlens, cu_bytes, T, D))
+            return GEMM_ERR_ALIAS;
+    }
+    for (const View &x : in)
+        if (in_range(x, a.delta, row_bytes, T, D)) return GEMM_ERR_ALIAS;
+    const uintptr_t l0 = reinterpret_cast<uintptr_t>(a.lse), e0 = reinterpret_cast<uintptr_t>(a.delta);
+    if (l0 < e0 + (uintptr_t)row_bytes && e0 < l0 + (uintptr_t)row_bytes) return GEMM_ERR_ALIAS;
+
+    Problem p = device_problem(a.p), pk;
+    pk = p;
+    const bool join = joined(a.p, HQ), joink = joined(a.p, HK);
+    p.tiles = (int)tiles_of(a.p, join ? 16 : 64);
+    pk.tiles = (int)tiles_of(a.p, joink ? 16 : 64);
+    const int64_t grid = (int64_t)p.tiles * HQ, gridk = (int64_t)pk.tiles * HK;
+    if (grid >= ((int64_t)1 << 31) || gridk >= ((int64_t)1 << 31)) return GEMM_ERR_SHAPE;
+    const Strided sg = strided(a.dout, T, HQ), sq = strided(a.q, T, HQ), sk = strided(a.k, T, HK),
+                  sv = strided(a.v, T, HK), so = strided(a.out, T, HQ), dq = strided(a.dq, T, HQ),
+                  dk = strided(a.dk, T, HK), dv = strided(a.dv, T, HK);
+    hipStream_t hs = static_cast<hipStream_t>(stream);
+#define BWD(DP, EX)                                                                                                 \
+    do {                                                                                                             \
+        if (join)                                                                                                    \
+            hipLaunchKernelGGL((attention_bwd_dq<DP, EX, 1, 4>), dim3((unsigned)grid), dim3(256), 0, hs, p, sg, sq, \
+                               sk, sv, so, a.lse, a.delta, dq);                                                      \
+        else                                                                                                         \
+            hipLaunchKernelGGL((attention_bwd_dq<DP, EX, 1, 1>), dim3((unsigned)grid), dim3(256), 0, hs, p, sg, sq, \
+                               sk, sv, so, a.lse, a.delta, dq);                                                      \
+        if (joink)                                                                                                   \
+            hipLaunchKernelGGL((attention_bwd_dkv<DP, EX, 1, 4>), dim3((unsigned)gridk), dim3(256), 0, hs, pk, sg,  \
+                               sq, sk, sv, a.lse, a.delta, dk, dv);                                                  \
+        else                                                                                                         \
+            hipLaunchKernelGGL((attention_bwd_dkv<DP, EX, 1, 1>), dim3((unsigned)gridk), dim3(256), 0, hs, pk, sg,  \
+                               sq, sk, sv, a.lse, a.delta, dk, dv);                                                  \
+    } while (0)
+    ATTN_BY_DIM(BWD);
+#undef BWD
+    return hipGetLastError() == hipSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
+}
+
+}  // extern "C"
