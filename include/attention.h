@@ -123,6 +123,59 @@ typedef struct attn_backward_args {
 } attn_backward_args;
 int attn_backward(const attn_backward_args *args, void *stream);
 
+/* The sizes of a norm and rotation and what all rows share. */
+typedef struct attn_norm {
+    const void *positions;     /* [tokens] int32 or int64, any values */
+    int64_t positions64;       /* 0: int32, 1: int64 */
+    const float *inv_freq;     /* [rotated / 2] */
+    const float *q_weight;     /* [head_dim] */
+    const float *k_weight;     /* [head_dim] */
+    int64_t tokens;
+    int64_t q_heads;
+    int64_t k_heads;
+    int64_t head_dim;          /* even, 2 to 256 */
+    int64_t rotated;           /* even, 0 to head_dim */
+    int64_t interleaved;       /* 0 or 1 */
+    double eps;                /* finite, not negative */
+} attn_norm;
+
+/*
+ * q_out and k_out from q and k; each may be the very same tensor as its
+ * input, and may not overlap anything else of the call.  Any strides and
+ * 4-byte alignment; 16-byte accesses where bases and strides are multiples
+ * of 16 bytes, head_dim is a multiple of 8 and, unless interleaved,
+ * rotated / 2 and (head_dim - rotated) / 2 are multiples of 4.  tokens == 0
+ * enqueues nothing.
+ *
+ * GEMM_ERR_SHAPE for sizes outside the above (tokens < 2^30, heads <= 65535)
+ * or an output whose rows overlap, GEMM_ERR_DTYPE for a flag that is neither
+ * 0 nor 1 or a bad eps, GEMM_ERR_NULL, GEMM_ERR_ALIGN, GEMM_ERR_ALIAS and
+ * GEMM_ERR_LAUNCH as above.
+ */
+typedef struct attn_qk_norm_rope_args {
+    attn_norm n;
+    attn_tensor q, k, q_out, k_out;
+} attn_qk_norm_rope_args;
+int attn_qk_norm_rope(const attn_qk_norm_rope_args *args, void *stream);
+
+/*
+ * dq, dk and the weights' gradients [head_dim] from dq_out, dk_out, q and k.
+ * dq may be the very same tensor as dq_out or q, dk as dk_out or k.  The
+ * workspace holds at least attn_qk_norm_rope_workspace_bytes bytes (-1 for
+ * sizes the call refuses), 8-byte aligned, of any contents; calls that may
+ * run at the same time need one each (GEMM_ERR_WORKSPACE when it is too
+ * small).  With tokens == 0 the weights' gradients are zero.
+ */
+typedef struct attn_qk_norm_rope_backward_args {
+    attn_norm n;
+    attn_tensor dq_out, dk_out, q, k, dq, dk;
+    float *dq_weight, *dk_weight;
+    void *workspace;
+    int64_t workspace_bytes;
+} attn_qk_norm_rope_backward_args;
+int attn_qk_norm_rope_backward(const attn_qk_norm_rope_backward_args *args, void *stream);
+int64_t attn_qk_norm_rope_workspace_bytes(int64_t tokens, int64_t head_dim);
+
 #ifdef __cplusplus
 }
 #endif

@@ -28,8 +28,9 @@ EXPORTED = (
     "gemm_matmul_t", "gemm_matmul_at", "gemm_matmul_at_swiglu_a", "gemm_matmul_t_ex", "gemm_matmul_at_ex",
     "gemm_matmul_at_swiglu_a_ex", "gemm_bwd_num_configs", "gemm_bwd_config_name", "gemm_bwd_select_config",
     "gemm_bwd_workspace_bytes", "gemm_matmul_t_swiglu_bwd", "gemm_matmul_t_swiglu_bwd_ex",
-    "loss_cross_entropy", "loss_sum_losses", "act_ffn_swiglu_backward", "act_ffn_gelu_backward",
-    "act_gelu_inplace", "attn_forward", "attn_backward",
+    "loss_cross_entropy", "loss_sum_losses", "loss_distill_cross_entropy", "act_ffn_swiglu_backward",
+    "act_ffn_gelu_backward", "act_gelu_inplace", "attn_forward", "attn_backward", "attn_qk_norm_rope",
+    "attn_qk_norm_rope_backward", "attn_qk_norm_rope_workspace_bytes",
     "gemm_timing_event_create", "gemm_timing_event_record", "gemm_timing_elapsed_ms", "gemm_timing_event_destroy",
 )
 
@@ -130,9 +131,12 @@ def _open(path):
     lib.act_ffn_gelu_backward.restype = c_int
     lib.act_gelu_inplace.argtypes = [p, p, i64, p]
     lib.act_gelu_inplace.restype = c_int
-    for name in ("attn_forward", "attn_backward"):
+    for name in ("attn_forward", "attn_backward", "attn_qk_norm_rope", "attn_qk_norm_rope_backward",
+                 "loss_distill_cross_entropy"):
         getattr(lib, name).argtypes = [ctypes.c_char_p, p]  # the packed argument struct, the stream
         getattr(lib, name).restype = c_int
+    lib.attn_qk_norm_rope_workspace_bytes.argtypes = [i64, i64]
+    lib.attn_qk_norm_rope_workspace_bytes.restype = i64
     lib.gemm_timing_event_create.argtypes = [ctypes.POINTER(ctypes.c_void_p)]
     lib.gemm_timing_event_create.restype = c_int
     lib.gemm_timing_event_record.argtypes = [p, p]
@@ -533,6 +537,85 @@ def sum_losses(losses, out=None):
     return out
 
 
+_DISTILL_ARGS = struct.Struct("=6q 3q 3q 5d")
+
+
+def _call_packed(name, args, device):
+    """Enqueue `name` on `device`'s current stream, with that device current.
+    `args` is the entry point's argument struct, packed field by field (every
+    field is 8 bytes wide: pointers, int64_t, double)."""
+    fn = getattr(load_library(), name)
+    if device.index == torch.cuda.current_device():
+        st = fn(args, torch.cuda.current_stream(device).cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            st = fn(args, torch.cuda.current_stream(device).cuda_stream)
+    if st != 0:
+        raise GemmError(st, name)
+
+
+def _indices(t, name, shape, device):
+    """(pointer, 1 if int64) of a dense index tensor."""
+    if not isinstance(t, torch.Tensor) or t.shape != shape or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {list(shape)} tensor on {device}")
+    if t.dtype not in (torch.int32, torch.int64):
+        raise TypeError(f"{name} must be int32 or int64, got {t.dtype}")
+    return t.data_ptr(), 1 if t.dtype == torch.int64 else 0
+
+
+def distill_cross_entropy(logits, targets, teacher_ids, teacher_logits, temperature=1.0, mix=0.5, alpha=0.0, beta=0.0,
+                          inv_norm=None, dlogits=None, losses=None):
+    """cross_entropy mixed with distillation from a teacher's best logits: the
+    losses of every row, and the gradient of inv_norm * sum over rows of
+    (1 - mix) * cross-entropy + mix * distillation.
+
+    logits [S, V] f32; targets [S] int32/int64 (a value outside [0, V) marks a
+    padding row; None only with mix 1); teacher_ids [S, K] int32/int64 and
+    teacher_logits [S, K] f32/f16, K up to 1024, the teacher's columns and its
+    logits there (an id outside [0, V) marks an unused entry).  The
+    distillation loss is temperature^2 * KL(teacher over its entries ||
+    student over the vocabulary), both at the temperature; alpha and beta are
+    cross_entropy's label smoothing and z-loss.  inv_norm defaults to 1 /
+    (number of rows that are not padding), which reads that count back to the
+    host when there are targets.  The gradient is written to dlogits, or over
+    `logits` when that is None.  Returns the losses [2, S]: cross-entropy and
+    distillation."""
+    if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
+        raise TypeError("logits must be a 2-D torch.Tensor [S, V]")
+    S, V = logits.shape
+    device = logits.device
+    _check_act(logits, "logits", (S, V), device)
+    if not isinstance(teacher_ids, torch.Tensor) or teacher_ids.dim() != 2:
+        raise TypeError("teacher_ids must be a 2-D torch.Tensor [S, K]")
+    K = teacher_ids.shape[1]
+    pi, ids64 = _indices(teacher_ids, "teacher_ids", (S, K), device)
+    if not isinstance(teacher_logits, torch.Tensor) or teacher_logits.shape != (S, K) \
+            or teacher_logits.device != device or not teacher_logits.is_contiguous():
+        raise ValueError(f"teacher_logits must be a contiguous [{S}, {K}] tensor on {device}")
+    if teacher_logits.dtype not in (torch.float32, torch.float16):
+        raise TypeError(f"teacher_logits must be float32 or float16, got {teacher_logits.dtype}")
+    pt, targets64 = (0, 0) if targets is None else _indices(targets, "targets", (S,), device)
+    if targets is None and mix != 1:
+        raise ValueError("targets may be None only with mix 1")
+    if inv_norm is None:
+        valid = S if targets is None else int(((targets >= 0) & (targets < V)).sum().item())
+        inv_norm = 1.0 / valid if valid else 0.0
+    if dlogits is None:
+        dlogits = logits
+    else:
+        _check_act(dlogits, "dlogits", (S, V), device)
+    if losses is None:
+        losses = torch.empty((2, S), dtype=torch.float32, device=device)
+    else:
+        _check_act(losses, "losses", (2, S), device)
+    _call_packed("loss_distill_cross_entropy",
+                 _DISTILL_ARGS.pack(logits.data_ptr(), dlogits.data_ptr(), pt, pi, teacher_logits.data_ptr(),
+                                    losses.data_ptr(), targets64, ids64,
+                                    1 if teacher_logits.dtype == torch.float16 else 0, S, V, K, float(temperature),
+                                    float(mix), float(alpha), float(beta), float(inv_norm)), device)
+    return losses
+
+
 # --- FFN activation kernels (include/activation.h) ---
 
 def _same_shape(name, t, ref):
@@ -587,24 +670,11 @@ def gelu_inplace(x, pre_gelu=None):
 
 
 # --- attention (include/attention.h) ---
-#
-# The argument structs of attention.h are packed field by field: every field
-# is 8 bytes wide (pointers, int64_t, double).
 
 _FORWARD_ARGS = struct.Struct("=8qd 12q q")
 _BACKWARD_ARGS = struct.Struct("=8qd 15q 2q 9q")
-
-
-def _call_packed(name, args, device):
-    """Enqueue `name` on `device`'s current stream, with that device current."""
-    fn = getattr(load_library(), name)
-    if device.index == torch.cuda.current_device():
-        st = fn(args, torch.cuda.current_stream(device).cuda_stream)
-    else:
-        with torch.cuda.device(device):
-            st = fn(args, torch.cuda.current_stream(device).cuda_stream)
-    if st != 0:
-        raise GemmError(st, name)
+_NORM_ARGS = struct.Struct("=11qd 12q")
+_NORM_BACKWARD_ARGS = struct.Struct("=11qd 18q 4q")
 
 
 def _heads(t, name, shape, device):
@@ -716,3 +786,95 @@ def attention_backward(dout, q, k, v, out, lse, cu_seqlens=None, causal=True, wi
     _call_packed("attn_backward", _BACKWARD_ARGS.pack(*problem, *tg, *tq, *tk, *tv, *to, pl, delta.data_ptr(), *tdq,
                                                       *tdk, *tdv), device)
     return dq, dk, dv
+
+
+def _vector(t, name, device, n=None):
+    """Pointer of a dense float32 vector (of n values)."""
+    if not isinstance(t, torch.Tensor) or t.device != device or t.dtype != torch.float32 or t.dim() != 1 \
+            or not t.is_contiguous() or (n is not None and t.shape[0] != n):
+        raise ValueError(f"{name} must be a contiguous float32 vector{'' if n is None else f' of {n}'} on {device}")
+    return t.data_ptr()
+
+
+def _attn_norm(q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved):
+    """The fields of attn_norm, and the shapes of q and of k."""
+    for name, t in (("q", q), ("k", k)):
+        if not isinstance(t, torch.Tensor) or t.dim() != 3:
+            raise TypeError(f"{name} must be a 3-D torch.Tensor [tokens, heads, head_dim]")
+    device = q.device
+    tokens, hq, dim = q.shape
+    hk = k.shape[1]
+    if not isinstance(positions, torch.Tensor) or positions.shape != (tokens,) or positions.device != device \
+            or not positions.is_contiguous():
+        raise ValueError(f"positions must be a contiguous [{tokens}] tensor on {device}")
+    if positions.dtype not in (torch.int32, torch.int64):
+        raise TypeError(f"positions must be int32 or int64, got {positions.dtype}")
+    pf = _vector(inv_freq, "inv_freq", device)
+    rotated = 2 * inv_freq.shape[0]
+    if rotated > dim:
+        raise ValueError(f"inv_freq has {rotated // 2} entries, a head only {dim} dimensions")
+    fields = (positions.data_ptr(), 1 if positions.dtype == torch.int64 else 0, pf,
+              _vector(q_weight, "q_weight", device, dim), _vector(k_weight, "k_weight", device, dim), tokens, hq, hk,
+              dim, rotated, 1 if interleaved else 0, float(eps))
+    return fields, q.shape, (tokens, hk, dim)
+
+
+def qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, eps=1e-6, interleaved=False, q_out=None, k_out=None):
+    """Root-mean-square norm of every query and key head, times a weight, then
+    the rotation by the token's position, in one pass over both.
+
+    q [tokens, q_heads, head_dim] and k [tokens, k_heads, head_dim] float32,
+    contiguous along the head with any other strides (head_dim even, up to
+    256); q_weight, k_weight [head_dim]; positions int32 or int64 [tokens];
+    inv_freq float32 [rotated / 2]: pair p of the first `rotated` dimensions
+    turns by positions * inv_freq[p].  Pair p is dimensions p and p + rotated
+    / 2, or with interleaved 2p and 2p + 1.  q_out and k_out may be q and k.
+    Returns (q_out, k_out)."""
+    fields, shape_q, shape_k = _attn_norm(q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved)
+    device = q.device
+    tq = _heads(q, "q", shape_q, device)
+    tk = _heads(k, "k", shape_k, device)
+    if q_out is None:
+        q_out = torch.empty(shape_q, dtype=torch.float32, device=device)
+    if k_out is None:
+        k_out = torch.empty(shape_k, dtype=torch.float32, device=device)
+    toq = _heads(q_out, "q_out", shape_q, device)
+    tok = _heads(k_out, "k_out", shape_k, device)
+    _call_packed("attn_qk_norm_rope", _NORM_ARGS.pack(*fields, *tq, *tk, *toq, *tok), device)
+    return q_out, k_out
+
+
+def qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, positions, inv_freq, eps=1e-6, interleaved=False,
+                          dq=None, dk=None, dq_weight=None, dk_weight=None):
+    """Gradients of qk_norm_rope, from those of its results and its inputs.
+    dq may be dq_out or q, dk may be dk_out or k (which are overwritten).
+    Returns (dq, dk, dq_weight, dk_weight); the weights' gradients are sums
+    over all tokens and heads."""
+    fields, shape_q, shape_k = _attn_norm(q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved)
+    device = q.device
+    tgq = _heads(dq_out, "dq_out", shape_q, device)
+    tgk = _heads(dk_out, "dk_out", shape_k, device)
+    tq = _heads(q, "q", shape_q, device)
+    tk = _heads(k, "k", shape_k, device)
+    if dq is None:
+        dq = torch.empty(shape_q, dtype=torch.float32, device=device)
+    if dk is None:
+        dk = torch.empty(shape_k, dtype=torch.float32, device=device)
+    tdq = _heads(dq, "dq", shape_q, device)
+    tdk = _heads(dk, "dk", shape_k, device)
+    tokens, _, dim = shape_q
+    if dq_weight is None:
+        dq_weight = torch.empty((dim,), dtype=torch.float32, device=device)
+    if dk_weight is None:
+        dk_weight = torch.empty((dim,), dtype=torch.float32, device=device)
+    pqw = _vector(dq_weight, "dq_weight", device, dim)
+    pkw = _vector(dk_weight, "dk_weight", device, dim)
+    nbytes = load_library().attn_qk_norm_rope_workspace_bytes(tokens, dim)
+    if nbytes < 0:
+        raise GemmError(-2, "attn_qk_norm_rope_workspace_bytes")
+    # scratch of this call's own: two captured graphs share nothing
+    scratch = torch.empty((nbytes,), dtype=torch.uint8, device=device)
+    _call_packed("attn_qk_norm_rope_backward",
+                 _NORM_BACKWARD_ARGS.pack(*fields, *tgq, *tgk, *tq, *tk, *tdq, *tdk, pqw, pkw, scratch.data_ptr(),
+                                          nbytes), device)
+    return dq, dk, dq_weight, dk_weight

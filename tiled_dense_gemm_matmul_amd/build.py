@@ -14,7 +14,8 @@ SRC = os.path.join(PKG, "csrc", "gemm_fwd.hip")
 LOSS_SRC = os.path.join(PKG, "csrc", "loss.hip")
 ACT_SRC = os.path.join(PKG, "csrc", "activation.hip")
 ATTN_SRC = os.path.join(PKG, "csrc", "attention.hip")
-SRCS = [SRC, LOSS_SRC, ACT_SRC, ATTN_SRC]
+NORM_SRC = os.path.join(PKG, "csrc", "qk_norm_rope.hip")
+SRCS = [SRC, LOSS_SRC, ACT_SRC, ATTN_SRC, NORM_SRC]
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libgemmfwd.so")
 SYNC_LIB = os.path.join(PKG, "libgemmfwd_sync.so")
@@ -40,7 +41,8 @@ def _hipcc(srcs, lib: str, verbose: bool, defines=()) -> str:
 
 def build_library(verbose: bool = False) -> str:
     """The library: the GEMM family (forward and backward), the fused loss, the
-    FFN activation kernels and the attention kernels."""
+    FFN activation kernels, the attention kernels and the norm and
+    rotation of queries and keys."""
     return _hipcc(SRCS, LIB, verbose)
 
 

@@ -43,6 +43,7 @@
 
 #include "attention.h"
 #include "gemm_fwd.h"
+#include "strided.h"
 
 namespace {
 
@@ -58,11 +59,6 @@ constexpr float kLn2 = 0.69314718055994530942f;
 // The running maximum of a row that has seen no key yet: low enough that any
 // score replaces it, finite so that differences with it are not NaN.
 constexpr float kNoMax = -3.0e38f;
-
-struct Strided {
-    float *p;
-    int64_t st, sh;
-};
 
 struct Problem {
     const int *cu;
@@ -683,37 +679,6 @@ __global__ __launch_bounds__(256, 2) void attention_bwd_dkv(Problem p, Strided d
 
 // --- host ---
 
-bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-struct View {
-    const attn_tensor *t;
-    int64_t heads;
-    bool output;
-};
-
-// Bytes from the first to behind the last element.
-int64_t extent(const View &v, int64_t tokens, int64_t d) {
-    return ((tokens - 1) * v.t->token_stride + (v.heads - 1) * v.t->head_stride + d) * 4;
-}
-
-// Whether two tensors may share an element.  Tensors in separate ranges do
-// not; nor do views of one buffer with the same token stride whose spans
-// within a token's row lie apart.
-bool overlap(const View &a, const View &b, int64_t tokens, int64_t d) {
-    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.t->data), b0 = reinterpret_cast<uintptr_t>(b.t->data);
-    if (a0 >= b0 + (uintptr_t)extent(b, tokens, d) || b0 >= a0 + (uintptr_t)extent(a, tokens, d)) return false;
-    const int64_t st = a.t->token_stride * 4;
-    const int64_t sa = ((a.heads - 1) * a.t->head_stride + d) * 4, sb = ((b.heads - 1) * b.t->head_stride + d) * 4;
-    if (a.t->token_stride != b.t->token_stride || sa > st || sb > st) return true;
-    const int64_t from_a = (int64_t)(((int64_t)(b0 - a0) % st + st) % st);
-    return from_a < sa || from_a + sb > st;
-}
-
-bool in_range(const View &v, const void *p, int64_t bytes, int64_t tokens, int64_t d) {
-    const uintptr_t a0 = reinterpret_cast<uintptr_t>(v.t->data), b0 = reinterpret_cast<uintptr_t>(p);
-    return p != nullptr && a0 < b0 + (uintptr_t)bytes && b0 < a0 + (uintptr_t)extent(v, tokens, d);
-}
-
 constexpr int64_t kMaxTokens = (int64_t)1 << 30, kMaxStride = (int64_t)1 << 22, kMaxHeadStride = (int64_t)1 << 40;
 
 int check_tensor(const View &v, int64_t tokens, int64_t d) {
@@ -721,11 +686,7 @@ int check_tensor(const View &v, int64_t tokens, int64_t d) {
     const int64_t st = v.t->token_stride, sh = v.t->head_stride;
     if (st < 0 || sh < 0 || sh > kMaxHeadStride) return GEMM_ERR_SHAPE;
     if (tokens > 1 && (st < d || st >= kMaxStride)) return GEMM_ERR_SHAPE;
-    if (v.output && v.heads > 1) {
-        // an output's rows may not overlap: heads inside a token's row, or tokens inside a head
-        const bool inside = sh >= d && (tokens == 1 || st >= (v.heads - 1) * sh + d);
-        if (!inside && sh < (tokens - 1) * st + d) return GEMM_ERR_SHAPE;
-    }
+    if (v.output && !rows_apart(v, tokens, d)) return GEMM_ERR_SHAPE;
     if (!aligned(v.t->data, 16) || (tokens > 1 && st % 4) || (v.heads > 1 && sh % 4)) return GEMM_ERR_ALIGN;
     return GEMM_OK;
 }
@@ -757,11 +718,6 @@ Problem device_problem(const attn_problem &a) {
     p.c = (float)(a.scale * 1.44269504088896340736);
     p.tiles = 0;
     return p;
-}
-
-Strided strided(const attn_tensor &t, int64_t tokens, int64_t heads) {
-    // the stride of an axis of one element is never stepped over
-    return {static_cast<float *>(t.data), tokens > 1 ? t.token_stride : 0, heads > 1 ? t.head_stride : 0};
 }
 
 // Tiles of `tile` rows a head: every sequence's own, and enough for the rows of none.
@@ -804,8 +760,7 @@ int attn_forward(const attn_forward_args *args, void *stream) {
         if ((st = check_tensor(*x, T, D)) != GEMM_OK) return st;
     if (a.lse == nullptr) return GEMM_ERR_NULL;
     if (!aligned(a.lse, 4)) return GEMM_ERR_ALIGN;
-    const bool in_place = a.out.data == a.q.data && a.out.token_stride == a.q.token_stride &&
-                          a.out.head_stride == a.q.head_stride;
+    const bool in_place = same_tensor(a.out, a.q);
     const int64_t lse_bytes = a.p.q_heads * T * 4, cu_bytes = (a.p.num_seqs + 1) * 4;
     if ((!in_place && overlap(o, q, T, D)) || overlap(o, k, T, D) || overlap(o, v, T, D) ||
         in_range(o, a.lse, lse_bytes, T, D) || in_range(q, a.lse, lse_bytes, T, D) ||

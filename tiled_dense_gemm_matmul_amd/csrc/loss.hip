@@ -32,6 +32,8 @@
 #include <stdint.h>
 
 #include <cmath>
+#include <initializer_list>
+#include <utility>
 
 #include "gemm_fwd.h"
 #include "loss.h"
@@ -237,6 +239,300 @@ __global__ __launch_bounds__(NT) void sum_losses_kernel(const float *losses, flo
     if (threadIdx.x == 0) out[0] = total;
 }
 
+// --- distillation ---
+//
+// One workgroup per row again.  The gradient of both terms is a function of
+// the logit and the column alone, A e^(l - max) + B e^((l - max) / tau) + C,
+// but for the target's column and the teacher's: those few are written once
+// more, with their subtractions, after the row.  Bound by memory like
+// cross_entropy: each logit is read once and its gradient written once while
+// the row fits in the registers (65536 logits); longer rows are read twice,
+// the maximum and the sums being formed in one pass over the row.
+//
+// 16-byte accesses start at the row's first 16-byte boundary, so rows of any
+// length and any 4-byte alignment take them; the up to three logits in front
+// of the boundary and behind the last whole group go to one thread each.
+constexpr int kMaxTop = 1024;  // teacher entries a row
+
+struct Distill {
+    const float *logits;
+    float *grad;
+    const void *targets, *ids, *teacher;
+    float *losses;
+    int S, V, K;
+    int targets64, ids64, half;
+    float inv_tau, tau, mix, alpha, beta, inv_norm;
+};
+
+// A column of a 32- or 64-bit index array, -1 for one outside [0, V).
+__device__ __forceinline__ int column(const void *p, int wide, int64_t i, int V) {
+    const int64_t v = wide ? ((const int64_t *)p)[i] : (int64_t)((const int *)p)[i];
+    return v >= 0 && v < V ? (int)v : -1;
+}
+
+// The sums of a row that its losses and its gradient are made of.
+struct RowSums {
+    float top, inv_hard, lse, inv_soft, log_soft, sum_l;
+};
+
+// The teacher's distribution over a row's used entries, with the student's
+// logits there, in LDS.
+struct Teacher {
+    int id[kMaxTop];
+    float mass[kMaxTop], l[kMaxTop];
+};
+
+// Loads and normalises it: thread t takes entries t, t + NT, ...  Returns
+// whether any entry has mass.  All threads call it; the student's row is not
+// written before the next barrier.
+template <int NT>
+__device__ __forceinline__ bool load_teacher(const Distill &a, int s, const float *row, Teacher &t, float *logt_sum,
+                                             float *slots) {
+    constexpr int NW = NT / 64;
+    const int64_t base = (int64_t)s * a.K;
+    float m = -INFINITY;
+    for (int j = threadIdx.x; j < a.K; j += NT) {
+        const int id = column(a.ids, a.ids64, base + j, a.V);
+        float z = a.half ? (float)((const _Float16 *)a.teacher)[base + j] : ((const float *)a.teacher)[base + j];
+        z *= a.inv_tau;
+        t.id[j] = id;
+        t.mass[j] = z;
+        t.l[j] = id >= 0 ? row[id] : 0.0f;
+        // a NaN stays in the sum below; the maximum passes over it
+        if (id >= 0) m = fmaxf(m, z);
+    }
+    m = block_reduce<NW, true>(m, slots);
+    const float ref = m == -INFINITY ? 0.0f : m;
+    float se = 0.0f;
+    for (int j = threadIdx.x; j < a.K; j += NT) {
+        const float e = t.id[j] >= 0 ? expf(t.mass[j] - ref) : 0.0f;
+        se += e;
+    }
+    se = block_reduce<NW, false>(se, slots + NW);
+    const bool has = se != 0.0f;  // NaN counts: it is passed on
+    const float inv = has ? 1.0f / se : 0.0f, ln = has ? logf(se) : 0.0f;
+    // sum of mass * log(mass), and the masses in place of the logits
+    float h = 0.0f;
+    for (int j = threadIdx.x; j < a.K; j += NT) {
+        const float z = t.mass[j] - ref;
+        const float e = t.id[j] >= 0 && has ? expf(z) * inv : 0.0f;
+        if (e != 0.0f) h += e * (z - ln);
+        t.mass[j] = e;
+    }
+    *logt_sum = h;
+    return has;
+}
+
+// Losses of the row, and the columns whose gradient differs from the rest.
+// Called after the row's gradient has been written and a barrier.
+template <int NT>
+__device__ __forceinline__ void finish_row(const Distill &a, int s, int tgt, float l_t, const RowSums &r, bool has,
+                                           float logt_sum, const Teacher &t, float *grad, float A, float B, float C,
+                                           float *slots) {
+    constexpr int NW = NT / 64;
+    float kd = logt_sum;
+    for (int j = threadIdx.x; j < a.K; j += NT) {
+        const float mass = t.mass[j];
+        if (mass != 0.0f) kd -= mass * ((t.l[j] - r.top) * a.inv_tau - r.log_soft);
+    }
+    kd = block_reduce<NW, false>(kd, slots);
+    const float hit = (1.0f - a.mix) * (1.0f - a.alpha) * a.inv_norm, soft = a.mix * a.tau * a.inv_norm;
+    if (threadIdx.x == 0) {
+        a.losses[s] = tgt >= 0 ? row_loss(r.lse, l_t, r.sum_l / (float)a.V, a.alpha, a.beta) : 0.0f;
+        a.losses[a.S + s] = has ? a.tau * a.tau * kd : 0.0f;
+    }
+    auto value = [&](float l) {
+        const float d = l - r.top;
+        return A * __expf(d) + B * __expf(d * a.inv_tau) + C;
+    };
+    // The first entry of a column writes it, with the masses of all of that
+    // column's entries in their order.
+    bool target_taken = false;
+    for (int j = threadIdx.x; j < a.K; j += NT) {
+        const int id = t.id[j];
+        if (id < 0) continue;
+        bool first = true;
+        float mass = 0.0f;
+        for (int i = 0; i < a.K; ++i) {
+            if (t.id[i] != id) continue;
+            first = first && i >= j;
+            mass += t.mass[i];
+        }
+        if (first) grad[id] = value(t.l[j]) - soft * mass - (id == tgt ? hit : 0.0f);
+        target_taken = target_taken || id == tgt;
+    }
+    if (!__syncthreads_or(target_taken) && threadIdx.x == 0 && tgt >= 0) grad[tgt] = value(l_t) - hit;
+}
+
+// The factors of the row's gradient from its sums.
+__device__ __forceinline__ void factors(const Distill &a, int tgt, const RowSums &r, bool has, float &A, float &B,
+                                        float &C) {
+    const float hard = tgt >= 0 ? (1.0f - a.mix) * a.inv_norm : 0.0f;
+    A = hard * (1.0f + 2.0f * a.beta * r.lse) * r.inv_hard;
+    B = has ? a.mix * a.tau * a.inv_norm * r.inv_soft : 0.0f;
+    C = -hard * (a.alpha / (float)a.V);
+}
+
+__device__ __forceinline__ RowSums row_sums(const Distill &a, float top, float hard, float soft, float sum_l) {
+    RowSums r;
+    r.top = top;
+    r.inv_hard = 1.0f / hard;
+    r.lse = top + logf(hard);
+    r.inv_soft = 1.0f / soft;
+    r.log_soft = logf(soft);
+    r.sum_l = sum_l;
+    return r;
+}
+
+// The row's layout for 16-byte accesses: `head` logits in front of the first
+// boundary, `groups` whole groups, `tail` logits behind them.
+struct RowShape {
+    int head, groups, tail;
+};
+__device__ __forceinline__ RowShape row_shape(const float *row, int V) {
+    RowShape r;
+    r.head = min((int)((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) / 4, V);
+    r.groups = (V - r.head) / 4;
+    r.tail = V - r.head - 4 * r.groups;
+    return r;
+}
+// The column of the edge logit that this thread holds, or -1.
+__device__ __forceinline__ int edge_column(const RowShape &r) {
+    const int t = threadIdx.x;
+    if (t < r.head) return t;
+    if (t < r.head + r.tail) return t + 4 * r.groups;
+    return -1;
+}
+
+template <int NT, int CAP, bool STREAM>
+__global__ __launch_bounds__(NT) void distill_resident(Distill a) {
+    constexpr int NW = NT / 64, G = CAP / 4, POL = STREAM ? kNonTemporal : 0;
+    __shared__ float red[8][NW];
+    __shared__ Teacher teacher;
+    const int tid = threadIdx.x, s = blockIdx.x;
+    const float *row = a.logits + (size_t)s * a.V;
+    float *grad = a.grad + (size_t)s * a.V;
+    const RowShape shape = row_shape(row, a.V);
+    const int edge = edge_column(shape);
+    const Rsrc rr = row_rsrc(row + shape.head, shape.groups * 16), rg = row_rsrc(grad + shape.head, shape.groups * 16);
+    auto off = [&](int j) { return (j * NT + tid) * 16; };
+    const int tgt = a.targets ? column(a.targets, a.targets64, s, a.V) : -1;
+    if (a.targets && tgt < 0) {
+        // padding: zero losses, zero gradient
+        if (tid < 2) a.losses[(size_t)tid * a.S + s] = 0.0f;
+#pragma unroll
+        for (int j = 0; j < G; ++j) __builtin_amdgcn_raw_buffer_store_b128(u32x4v{0u, 0u, 0u, 0u}, rg, off(j), 0, POL);
+        if (edge >= 0) grad[edge] = 0.0f;
+        return;
+    }
+    f32x4 x[G];
+#pragma unroll
+    for (int j = 0; j < G; ++j)
+        x[j] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rr, off(j), 0, POL));
+    const float xe = edge >= 0 ? row[edge] : -INFINITY;
+    const float l_t = tgt >= 0 ? row[tgt] : 0.0f;
+    const int nv = shape.groups > tid ? min(G, (shape.groups - tid + NT - 1) / NT) : 0;  // this thread's groups
+    float logt_sum;
+    const bool has = load_teacher<NT>(a, s, row, teacher, &logt_sum, red[0]);
+    float m = xe, sl = edge >= 0 ? xe : 0.0f;
+#pragma unroll
+    for (int j = 0; j < G; ++j) {
+        if (j < nv) {
+            m = fmaxf(m, fmaxf(fmaxf(x[j][0], x[j][1]), fmaxf(x[j][2], x[j][3])));
+            sl += (x[j][0] + x[j][1]) + (x[j][2] + x[j][3]);
+        }
+    }
+    const float top = block_reduce<NW, true>(m, red[2]);
+    float hard = 0.0f, soft = 0.0f;
+    if (edge >= 0) {
+        hard = __expf(xe - top);
+        soft = __expf((xe - top) * a.inv_tau);
+    }
+#pragma unroll
+    for (int j = 0; j < G; ++j) {
+        if (j < nv) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const float d = x[j][c] - top;
+                hard += __expf(d);
+                soft += __expf(d * a.inv_tau);
+            }
+        }
+    }
+    hard = block_reduce<NW, false>(hard, red[3]);
+    soft = block_reduce<NW, false>(soft, red[4]);
+    const float sum_l = a.alpha > 0.0f ? block_reduce<NW, false>(sl, red[5]) : 0.0f;
+    const RowSums r = row_sums(a, top, hard, soft, sum_l);
+    float A, B, C;
+    factors(a, tgt, r, has, A, B, C);
+    // All reads of the row lie before the barriers above.
+#pragma unroll
+    for (int j = 0; j < G; ++j) {
+        f32x4 g;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const float d = x[j][c] - top;
+            g[c] = A * __expf(d) + B * __expf(d * a.inv_tau) + C;
+        }
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4v, g), rg, off(j), 0, POL);
+    }
+    if (edge >= 0) grad[edge] = A * __expf(xe - top) + B * __expf((xe - top) * a.inv_tau) + C;
+    // the stores above have to be complete before other waves write the same columns
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();
+    finish_row<NT>(a, s, tgt, l_t, r, has, logt_sum, teacher, grad, A, B, C, red[6]);
+}
+
+// Rows too long for the registers, or whose gradient lies at another
+// alignment than the row: one pass for the maximum and the sums, each thread
+// moving its own reference when it meets a larger logit, one for the gradient.
+template <int NT>
+__global__ __launch_bounds__(NT) void distill_stream(Distill a) {
+    constexpr int NW = NT / 64;
+    __shared__ float red[8][NW];
+    __shared__ Teacher teacher;
+    const int tid = threadIdx.x, s = blockIdx.x;
+    const float *row = a.logits + (size_t)s * a.V;
+    float *grad = a.grad + (size_t)s * a.V;
+    const int tgt = a.targets ? column(a.targets, a.targets64, s, a.V) : -1;
+    if (a.targets && tgt < 0) {
+        if (tid < 2) a.losses[(size_t)tid * a.S + s] = 0.0f;
+        for (int v = tid; v < a.V; v += NT) grad[v] = 0.0f;
+        return;
+    }
+    const float l_t = tgt >= 0 ? row[tgt] : 0.0f;
+    float logt_sum;
+    const bool has = load_teacher<NT>(a, s, row, teacher, &logt_sum, red[0]);
+    float m = -INFINITY, hard = 0.0f, soft = 0.0f, sl = 0.0f;
+    for (int v = tid; v < a.V; v += NT) {
+        const float l = row[v];
+        sl += l;
+        if (l > m) {
+            hard *= __expf(m - l);
+            soft *= __expf((m - l) * a.inv_tau);
+            m = l;
+        }
+        const float d = l == m ? 0.0f : l - m;  // also where both are minus infinity
+        hard += __expf(d);
+        soft += __expf(d * a.inv_tau);
+    }
+    const float top = block_reduce<NW, true>(m, red[2]);
+    const float d0 = m == -INFINITY ? -INFINITY : m - top;
+    hard = block_reduce<NW, false>(m == -INFINITY ? 0.0f : hard * __expf(d0), red[3]);
+    soft = block_reduce<NW, false>(m == -INFINITY ? 0.0f : soft * __expf(d0 * a.inv_tau), red[4]);
+    const float sum_l = a.alpha > 0.0f ? block_reduce<NW, false>(sl, red[5]) : 0.0f;
+    const RowSums r = row_sums(a, top, hard, soft, sum_l);
+    float A, B, C;
+    factors(a, tgt, r, has, A, B, C);
+    for (int v = tid; v < a.V; v += NT) {
+        const float d = row[v] - top;
+        grad[v] = A * __expf(d) + B * __expf(d * a.inv_tau) + C;
+    }
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();
+    finish_row<NT>(a, s, tgt, l_t, r, has, logt_sum, teacher, grad, A, B, C, red[6]);
+}
+
 bool overlaps(const void *a, size_t abytes, const void *b, size_t bbytes) {
     if (a == nullptr || b == nullptr || abytes == 0 || bbytes == 0) return false;
     const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
@@ -300,6 +596,74 @@ int loss_sum_losses(const float *losses, float *out, int64_t S, void *stream) {
     if (overlaps(out, 4, losses, (size_t)S * 4)) return GEMM_ERR_ALIAS;
     hipLaunchKernelGGL((sum_losses_kernel<1024>), dim3(1), dim3(1024), 0, static_cast<hipStream_t>(stream), losses, out,
                        (int)S);
+    return hipGetLastError() == hipSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
+}
+
+int loss_distill_cross_entropy(const loss_distill_args *args, void *stream) {
+    if (args == nullptr) return GEMM_ERR_NULL;
+    const loss_distill_args &p = *args;
+    const int64_t S = p.S, V = p.V, K = p.K;
+    if (S < 0 || V < 0 || K < 0 || S >= ((int64_t)1 << 31) || V >= ((int64_t)1 << 29) || K > kMaxTop)
+        return GEMM_ERR_SHAPE;
+    if (S > 0 && (p.losses == nullptr || (V > 0 && (p.logits == nullptr || p.dlogits == nullptr)) ||
+                  (K > 0 && (p.teacher_ids == nullptr || p.teacher_logits == nullptr))))
+        return GEMM_ERR_NULL;
+    const float tau = (float)p.temperature, mix = (float)p.mix, alpha = (float)p.alpha, beta = (float)p.beta;
+    if ((p.targets64 != 0 && p.targets64 != 1) || (p.ids64 != 0 && p.ids64 != 1) ||
+        (p.teacher_f16 != 0 && p.teacher_f16 != 1) || !(tau > 0.0f) || !std::isfinite(tau) ||
+        !std::isfinite(1.0f / tau) || !std::isfinite(tau * tau) || !(mix >= 0.0f && mix <= 1.0f) ||
+        !(alpha >= 0.0f && alpha <= 1.0f) || !(beta >= 0.0f) || !std::isfinite(beta) ||
+        !std::isfinite((float)p.inv_norm))
+        return GEMM_ERR_DTYPE;
+    if (p.targets == nullptr && mix != 1.0f && S > 0) return GEMM_ERR_NULL;  // the hard term needs targets
+    if (!aligned(p.logits, 4) || !aligned(p.dlogits, 4) || !aligned(p.losses, 4) ||
+        !aligned(p.targets, p.targets64 ? 8 : 4) || !aligned(p.teacher_ids, p.ids64 ? 8 : 4) ||
+        !aligned(p.teacher_logits, p.teacher_f16 ? 2 : 4))
+        return GEMM_ERR_ALIGN;
+    const size_t rows = (size_t)S * V * 4, lb = (size_t)S * 8, tb = (size_t)S * (p.targets64 ? 8 : 4),
+                 ib = (size_t)S * K * (p.ids64 ? 8 : 4), zb = (size_t)S * K * (p.teacher_f16 ? 2 : 4);
+    if ((p.dlogits != p.logits && overlaps(p.dlogits, rows, p.logits, rows)) ||
+        overlaps(p.dlogits, rows, p.losses, lb) || overlaps(p.logits, rows, p.losses, lb))
+        return GEMM_ERR_ALIAS;
+    for (const auto &out : {std::make_pair((const void *)p.dlogits, rows), std::make_pair((const void *)p.losses, lb)})
+        if (overlaps(out.first, out.second, p.targets, tb) || overlaps(out.first, out.second, p.teacher_ids, ib) ||
+            overlaps(out.first, out.second, p.teacher_logits, zb))
+            return GEMM_ERR_ALIAS;
+    if (S == 0) return GEMM_OK;
+    Distill a;
+    a.logits = p.logits;
+    a.grad = p.dlogits;
+    a.targets = p.targets;
+    a.ids = p.teacher_ids;
+    a.teacher = p.teacher_logits;
+    a.losses = p.losses;
+    a.S = (int)S;
+    a.V = (int)V;
+    a.K = (int)K;
+    a.targets64 = (int)p.targets64;
+    a.ids64 = (int)p.ids64;
+    a.half = (int)p.teacher_f16;
+    a.tau = tau;
+    a.inv_tau = 1.0f / tau;
+    a.mix = mix;
+    a.alpha = alpha;
+    a.beta = beta;
+    a.inv_norm = (float)p.inv_norm;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    const bool nt = S * V * 4 >= kStreamBytes;
+    const bool same_phase = ((reinterpret_cast<uintptr_t>(p.logits) ^ reinterpret_cast<uintptr_t>(p.dlogits)) & 15) == 0;
+#define DISTILL(NT, CAP)                                                                                     \
+    do {                                                                                                     \
+        if (nt) hipLaunchKernelGGL((distill_resident<NT, CAP, true>), dim3(a.S), dim3(NT), 0, st, a);        \
+        else hipLaunchKernelGGL((distill_resident<NT, CAP, false>), dim3(a.S), dim3(NT), 0, st, a);          \
+    } while (0)
+    if (!same_phase || V > 1024 * 64) hipLaunchKernelGGL((distill_stream<1024>), dim3(a.S), dim3(1024), 0, st, a);
+    else if (V <= 256 * 16) DISTILL(256, 16);
+    else if (V <= 512 * 16) DISTILL(512, 16);
+    else if (V <= 512 * 32) DISTILL(512, 32);
+    else if (V <= 1024 * 32) DISTILL(1024, 32);
+    else DISTILL(1024, 64);
+#undef DISTILL
     return hipGetLastError() == hipSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
 }
 
