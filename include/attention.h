@@ -41,7 +41,8 @@
  *       angle = positions[t] inv_freq[p]     for pair p < rotated / 2
  *
  * where pair p is (p, p + rotated / 2), or (2p, 2p + 1) when interleaved,
- * and y = n from `rotated` on.  The angle is formed and reduced in 64 bits.
+ * and y = n from `rotated` on.  The angle is reduced to a part of a
+ * turn without loss for positions up to 2^53 in magnitude.
  * The backward pass gives dx from dy, and the weight's gradient summed over
  * tokens and heads:
  *

@@ -74,3 +74,48 @@ def sum_losses(losses):
 # (a few 1e-6 relative), a V-term sum (log2 V roundings), one division.
 TOL_LOSS = (1e-5, 1e-6)
 TOL_DLOGITS = (1e-5, 1e-9)
+
+
+def distill(logits, targets, ids, teacher, temperature=1.0, mix=0.5, alpha=0.0, beta=0.0, inv_norm=1.0):
+    """Losses and dLogits of distill_cross_entropy (include/loss.h):
+
+        t    = softmax of the teacher's used logits / tau
+        kd   = tau^2 sum_j t[j] (log t[j] - log softmax(l / tau)[id[j]])
+        dl   = (1 - mix) * cross_entropy's + mix tau (softmax(l / tau) - t at its columns), times inv_norm
+
+    logits [S, V]; targets [S] or None (mix 1); ids, teacher [S, K]; an id
+    outside [0, V) is not used.  Returns (losses [2, S], dlogits [S, V],
+    scale dict of the magnitudes the bounds TOL_LOSS and TOL_DLOGITS are
+    relative to).
+    """
+    logits = np.asarray(logits)
+    S, V = logits.shape
+    tau = temperature
+    losses, dl = np.zeros((2, S)), np.zeros((S, V))
+    loss_mag, dl_mag = np.zeros((2, S)), np.zeros((S, V))
+    for s in range(S):
+        if targets is not None:
+            tgt = int(targets[s])
+            if not 0 <= tgt < V:
+                continue
+            one, grad, mag = cross_entropy(logits[s:s + 1], [tgt], alpha, beta, 1.0)
+            losses[0, s], loss_mag[0, s] = one[0], mag["loss"][0]
+            dl[s], dl_mag[s] = (1 - mix) * grad[0], (1 - mix) * mag["dlogits"][0]
+        use = [j for j in range(len(ids[s])) if 0 <= int(ids[s][j]) < V and float(teacher[s][j]) > -math.inf]
+        if use:
+            z = np.array([float(teacher[s][j]) for j in use]) / tau
+            log_t = z - z.max()
+            log_t -= math.log(float(np.exp(log_t).sum()))
+            t = np.exp(log_t)
+            l = logits[s].astype(np.float64) / tau
+            log_p = l - l.max()
+            norm = math.log(float(np.exp(log_p).sum()))
+            at = np.array([int(ids[s][j]) for j in use])
+            losses[1, s] = tau * tau * float((t * (log_t - (log_p[at] - norm))).sum())
+            loss_mag[1, s] = tau * tau * float((t * (np.abs(log_t) + np.abs(log_p[at]) + norm + 1)).sum())
+            p = np.exp(log_p - norm)
+            given = np.zeros(V)
+            np.add.at(given, at, t)
+            dl[s] += mix * tau * (p - given)
+            dl_mag[s] += mix * tau * (p + given)
+    return losses, dl * inv_norm, {"loss": loss_mag, "dlogits": dl_mag * abs(inv_norm)}

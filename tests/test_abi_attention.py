@@ -1,0 +1,286 @@
+"""The C boundary of the attention, norm-and-rotation and distillation entry
+points, on the CPU: the argument structs have the layout that the binding
+packs, every declared function is exported, and bad arguments are refused
+synchronously with the documented status (fake host addresses; nothing
+reaches a device)."""
+import os
+import re
+import struct
+import subprocess
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+OK, NULL, SHAPE, ALIGN, DTYPE, ALIAS, WORKSPACE = 0, -1, -2, -3, -4, -5, -8
+
+
+@pytest.fixture(scope="module")
+def binding():
+    from tiled_dense_gemm_matmul_amd import binding
+    return binding
+
+
+def _header(name):
+    with open(os.path.join(ROOT, "include", name)) as f:
+        return f.read()
+
+
+def test_statuses():
+    text = _header("gemm_fwd.h")
+    for name, code in (("NULL", NULL), ("SHAPE", SHAPE), ("ALIGN", ALIGN), ("DTYPE", DTYPE), ("ALIAS", ALIAS),
+                       ("WORKSPACE", WORKSPACE)):
+        assert int(re.search(rf"#define\s+GEMM_ERR_{name}\s+\(?(-?\d+)\)?", text).group(1)) == code
+
+
+def test_exports(binding):
+    lib = binding.load_library()
+    for name in ("attention.h", "loss.h"):
+        text = re.sub(r"/\*.*?\*/", "", _header(name), flags=re.S)
+        for fn in re.findall(r"\b((?:attn|loss)_[a-z_0-9]+)\s*\(", text):
+            assert hasattr(lib, fn) and fn in binding.EXPORTED, fn
+
+
+def test_struct_sizes(binding, tmp_path):
+    src = tmp_path / "sizes.c"
+    src.write_text('#include <stdio.h>\n#include "attention.h"\n#include "loss.h"\nint main(void) {\n'
+                   'printf("%zu %zu %zu %zu %zu", sizeof(attn_forward_args), sizeof(attn_backward_args),\n'
+                   'sizeof(attn_qk_norm_rope_args), sizeof(attn_qk_norm_rope_backward_args),\n'
+                   'sizeof(loss_distill_args));\nreturn 0; }\n')
+    exe = tmp_path / "sizes"
+    subprocess.run(["gcc", "-I", os.path.join(ROOT, "include"), str(src), "-o", str(exe)], check=True)
+    sizes = [int(x) for x in subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout.split()]
+    assert sizes == [binding._FORWARD_ARGS.size, binding._BACKWARD_ARGS.size, binding._NORM_ARGS.size,
+                     binding._NORM_BACKWARD_ARGS.size, binding._DISTILL_ARGS.size]
+
+
+BASE = 0x10000000
+STEP = 0x1000000
+
+
+class Args:
+    """The fields of an argument struct by name, in order."""
+
+    def __init__(self, fmt, names, values):
+        self.fmt, self.names, self.values = fmt, names, values
+
+    def pack(self, changes):
+        v = dict(zip(self.names, self.values))
+        for k, x in changes.items():
+            assert k in v, k
+            v[k] = x
+        return self.fmt.pack(*[v[n] for n in self.names])
+
+
+def _problem(**kw):
+    p = {"cu": 0, "nseq": 0, "tokens": 100, "hq": 4, "hk": 2, "d": 64, "causal": 1, "window": 0, "scale": 0.125}
+    return {**p, **kw}
+
+
+def _tensor(i, heads, d=64):
+    return [BASE + i * STEP, heads * d, d]
+
+
+def _named(prefixes):
+    return [f"{p}.{f}" for p in prefixes for f in ("p", "st", "sh")]
+
+
+@pytest.fixture(scope="module")
+def forward(binding):
+    names = list(_problem()) + _named(["q", "k", "v", "o"]) + ["lse"]
+    values = list(_problem().values()) + _tensor(0, 4) + _tensor(1, 2) + _tensor(2, 2) + _tensor(3, 4) + [BASE + 9 * STEP]
+    a = Args(binding._FORWARD_ARGS, names, values)
+    return lambda **kw: binding.load_library().attn_forward(a.pack({k.replace("_", "."): v for k, v in kw.items()}), None)
+
+
+@pytest.fixture(scope="module")
+def backward(binding):
+    names = list(_problem()) + _named(["g", "q", "k", "v", "o"]) + ["lse", "delta"] + _named(["dq", "dk", "dv"])
+    heads = [4, 4, 2, 2, 4]
+    values = list(_problem().values()) + sum([_tensor(i, h) for i, h in enumerate(heads)], []) + \
+        [BASE + 9 * STEP, BASE + 10 * STEP] + _tensor(5, 4) + _tensor(6, 2) + _tensor(7, 2)
+    a = Args(binding._BACKWARD_ARGS, names, values)
+    return lambda **kw: binding.load_library().attn_backward(a.pack({k.replace("_", "."): v for k, v in kw.items()}), None)
+
+
+BAD_PROBLEMS = [({"tokens": -1}, SHAPE), ({"tokens": 1 << 30}, SHAPE), ({"hq": 0}, SHAPE), ({"hk": 0}, SHAPE),
+                ({"hq": 3}, SHAPE), ({"hk": 8}, SHAPE), ({"hq": 65536}, SHAPE), ({"d": 0}, SHAPE), ({"d": 66}, SHAPE),
+                ({"d": 132}, SHAPE), ({"window": -1}, SHAPE), ({"scale": 0.0}, DTYPE), ({"scale": -1.0}, DTYPE),
+                ({"scale": float("nan")}, DTYPE), ({"scale": float("inf")}, DTYPE), ({"scale": 1e300}, DTYPE),
+                ({"causal": 2}, DTYPE), ({"cu": 0x20002}, ALIGN), ({"cu": 0x20000, "nseq": -1}, SHAPE),
+                ({"cu": 0x20000, "nseq": 1 << 24}, SHAPE)]
+
+
+@pytest.mark.parametrize("bad,status", BAD_PROBLEMS)
+def test_problem_refusals(forward, backward, bad, status):
+    assert forward(**bad) == status and backward(**bad) == status
+
+
+def test_forward_refusals(binding, forward):
+    assert binding.load_library().attn_forward(None, None) == NULL
+    for t in "qkvo":
+        assert forward(**{f"{t}_p": 0}) == NULL
+        assert forward(**{f"{t}_p": BASE + 12 * STEP + 4}) == ALIGN
+        assert forward(**{f"{t}_st": 60}) == SHAPE          # tokens closer than a head is wide
+        assert forward(**{f"{t}_st": 1 << 22}) == SHAPE
+        assert forward(**{f"{t}_st": -256}) == SHAPE
+        assert forward(**{f"{t}_sh": -64}) == SHAPE
+        assert forward(**{f"{t}_st": 322}) == ALIGN
+    assert forward(o_sh=60) == SHAPE                        # heads of an output overlap
+    assert forward(o_st=128) == SHAPE
+    assert forward(lse=0) == NULL and forward(lse=BASE + 9 * STEP + 2) == ALIGN
+    for t in "kv":
+        assert forward(o_p=BASE + (1 if t == "k" else 2) * STEP + 512) == ALIAS
+    assert forward(o_p=BASE + 256) == ALIAS                 # over q, but not q itself
+    assert forward(lse=BASE + 3 * STEP + 64) == ALIAS and forward(lse=BASE + 64) == ALIAS
+    assert forward(cu=BASE + 3 * STEP, nseq=1) == ALIAS
+    assert forward(tokens=0, q_p=0, k_p=0, v_p=0, o_p=0, lse=0) == OK
+
+
+def test_backward_refusals(binding, backward):
+    assert binding.load_library().attn_backward(None, None) == NULL
+    for t in ("g", "q", "k", "v", "o", "dq", "dk", "dv"):
+        assert backward(**{f"{t}_p": 0}) == NULL
+        assert backward(**{f"{t}_p": BASE + 12 * STEP + 8}) == ALIGN
+        assert backward(**{f"{t}_st": 60}) == SHAPE
+    assert backward(lse=0) == NULL and backward(delta=0) == NULL
+    for i, t in enumerate(("dq", "dk", "dv")):
+        for j in range(5):                                  # over each input
+            assert backward(**{f"{t}_p": BASE + j * STEP}) == ALIAS
+        assert backward(**{f"{t}_p": BASE + 9 * STEP}) == ALIAS      # lse
+        assert backward(**{f"{t}_p": BASE + 10 * STEP}) == ALIAS     # delta
+        assert backward(**{f"{t}_sh": 32}) == SHAPE
+    assert backward(dk_p=BASE + 5 * STEP) == ALIAS and backward(dv_p=BASE + 6 * STEP) == ALIAS
+    assert backward(delta=BASE + 9 * STEP + 16) == ALIAS and backward(delta=BASE + 64) == ALIAS
+    # interleaved columns of one buffer whose elements overlap
+    assert backward(dq_st=512, dk_st=512, dv_st=512, dk_p=BASE + 5 * STEP + 4 * 255 + 4 - 16,
+                    dv_p=BASE + 5 * STEP + 4 * 384) == ALIAS
+    assert backward(tokens=0) == OK
+
+
+def _norm(**kw):
+    n = {"pos": BASE + 20 * STEP, "wide": 0, "freq": BASE + 21 * STEP, "qw": BASE + 22 * STEP, "kw": BASE + 23 * STEP,
+         "tokens": 100, "hq": 4, "hk": 2, "d": 64, "rotated": 64, "il": 0, "eps": 1e-6}
+    return {**n, **kw}
+
+
+@pytest.fixture(scope="module")
+def norm(binding):
+    names = list(_norm()) + _named(["q", "k", "oq", "ok"])
+    values = list(_norm().values()) + _tensor(0, 4) + _tensor(1, 2) + _tensor(2, 4) + _tensor(3, 2)
+    a = Args(binding._NORM_ARGS, names, values)
+    return lambda **kw: binding.load_library().attn_qk_norm_rope(a.pack({k.replace("_", "."): v for k, v in kw.items()}),
+                                                                 None)
+
+
+@pytest.fixture(scope="module")
+def norm_backward(binding):
+    names = list(_norm()) + _named(["gq", "gk", "q", "k", "dq", "dk"]) + ["dqw", "dkw", "ws", "wsb"]
+    values = list(_norm().values()) + sum([_tensor(i, 4 - 2 * (i % 2)) for i in range(6)], []) + \
+        [BASE + 24 * STEP, BASE + 25 * STEP, BASE + 26 * STEP, 1 << 20]
+    a = Args(binding._NORM_BACKWARD_ARGS, names, values)
+    return lambda **kw: binding.load_library().attn_qk_norm_rope_backward(
+        a.pack({k.replace("_", "."): v for k, v in kw.items()}), None)
+
+
+@pytest.mark.parametrize("bad,status", [({"tokens": -1}, SHAPE), ({"tokens": 1 << 30}, SHAPE), ({"hq": 0}, SHAPE),
+                                        ({"hk": 0}, SHAPE), ({"d": 63}, SHAPE), ({"d": 258}, SHAPE), ({"d": 0}, SHAPE),
+                                        ({"rotated": -2}, SHAPE), ({"rotated": 3}, SHAPE), ({"rotated": 66}, SHAPE),
+                                        ({"wide": 2}, DTYPE), ({"il": 2}, DTYPE), ({"eps": -1e-6}, DTYPE),
+                                        ({"eps": float("nan")}, DTYPE), ({"eps": float("inf")}, DTYPE),
+                                        ({"qw": 0}, NULL), ({"kw": 0}, NULL), ({"freq": 0}, NULL), ({"pos": 0}, NULL),
+                                        ({"qw": 0x20002}, ALIGN), ({"freq": 0x20001}, ALIGN),
+                                        ({"pos": 0x20004, "wide": 1}, ALIGN)])
+def test_norm_refusals(norm, norm_backward, bad, status):
+    assert norm(**bad) == status and norm_backward(**bad) == status
+
+
+def test_norm_tensor_refusals(binding, norm, norm_backward):
+    lib = binding.load_library()
+    assert lib.attn_qk_norm_rope(None, None) == NULL and lib.attn_qk_norm_rope_backward(None, None) == NULL
+    for t in ("q", "k", "oq", "ok"):
+        assert norm(**{f"{t}_p": 0}) == NULL and norm(**{f"{t}_p": BASE + 30 * STEP + 2}) == ALIGN
+        assert norm(**{f"{t}_st": -64}) == SHAPE
+    assert norm(oq_st=128) == SHAPE and norm(ok_sh=32) == SHAPE
+    assert norm(oq_p=BASE + 4) == ALIAS and norm(ok_p=BASE) == ALIAS and norm(oq_p=BASE + STEP) == ALIAS
+    assert norm(ok_p=BASE + 2 * STEP) == ALIAS
+    for shared in ("pos", "freq", "qw", "kw"):
+        assert norm(**{shared: BASE + 2 * STEP}) == ALIAS and norm_backward(**{shared: BASE + 5 * STEP}) == ALIAS
+    for t in ("gq", "gk", "q", "k", "dq", "dk"):
+        assert norm_backward(**{f"{t}_p": 0}) == NULL
+    assert norm_backward(dqw=0) == NULL and norm_backward(dkw=0) == NULL and norm_backward(ws=0) == NULL
+    assert norm_backward(ws=BASE + 26 * STEP + 4) == ALIGN
+    need = lib.attn_qk_norm_rope_workspace_bytes(100, 64)
+    assert need > 0 and norm_backward(wsb=need - 1) == WORKSPACE
+    assert lib.attn_qk_norm_rope_workspace_bytes(-1, 64) == -1 and lib.attn_qk_norm_rope_workspace_bytes(4, 300) == -1
+    # dq over dk_out or k, dk over dq_out or q, either over the other or the scratch
+    assert norm_backward(dq_p=BASE + STEP) == ALIAS and norm_backward(dq_p=BASE + 3 * STEP) == ALIAS
+    assert norm_backward(dk_p=BASE) == ALIAS and norm_backward(dk_p=BASE + 2 * STEP) == ALIAS
+    assert norm_backward(dk_p=BASE + 4 * STEP) == ALIAS
+    assert norm_backward(ws=BASE + 4 * STEP) == ALIAS and norm_backward(ws=BASE) == ALIAS
+    assert norm_backward(dqw=BASE + 5 * STEP) == ALIAS
+    assert norm_backward(dkw=BASE + 24 * STEP) == ALIAS and norm_backward(dqw=BASE + 26 * STEP) == ALIAS
+    assert norm_backward(dqw=BASE) == ALIAS                  # a weight's gradient over an input
+    assert norm(tokens=0, q_p=0, k_p=0, oq_p=0, ok_p=0, pos=0) == OK
+
+
+DISTILL = {"l": BASE, "dl": BASE + STEP, "t": BASE + 2 * STEP, "ids": BASE + 3 * STEP, "z": BASE + 4 * STEP,
+           "losses": BASE + 5 * STEP, "t64": 0, "ids64": 0, "half": 0, "S": 10, "V": 1000, "K": 8, "tau": 2.0, "mix": 0.5,
+           "alpha": 0.1, "beta": 1e-4, "norm": 0.1}
+
+
+@pytest.mark.parametrize("bad,status", [({"S": -1}, SHAPE), ({"V": -1}, SHAPE), ({"K": -1}, SHAPE), ({"K": 1025}, SHAPE),
+                                        ({"V": 1 << 29}, SHAPE), ({"S": 1 << 31}, SHAPE), ({"l": 0}, NULL),
+                                        ({"dl": 0}, NULL), ({"t": 0}, NULL), ({"ids": 0}, NULL), ({"z": 0}, NULL),
+                                        ({"losses": 0}, NULL), ({"t64": 2}, DTYPE), ({"ids64": -1}, DTYPE),
+                                        ({"half": 2}, DTYPE), ({"tau": 0.0}, DTYPE), ({"tau": -1.0}, DTYPE),
+                                        ({"tau": float("nan")}, DTYPE), ({"tau": 1e-39}, DTYPE), ({"tau": 1e30}, DTYPE),
+                                        ({"mix": 1.5}, DTYPE), ({"mix": -0.1}, DTYPE), ({"mix": float("nan")}, DTYPE),
+                                        ({"alpha": 1.1}, DTYPE), ({"beta": -1.0}, DTYPE),
+                                        ({"beta": float("inf")}, DTYPE), ({"norm": float("nan")}, DTYPE),
+                                        ({"l": BASE + 2}, ALIGN), ({"dl": BASE + STEP + 1}, ALIGN),
+                                        ({"t": BASE + 2 * STEP + 4, "t64": 1}, ALIGN),
+                                        ({"ids": BASE + 3 * STEP + 4, "ids64": 1}, ALIGN),
+                                        ({"z": BASE + 4 * STEP + 1, "half": 1}, ALIGN), ({"dl": BASE + 4}, ALIAS),
+                                        ({"losses": BASE}, ALIAS), ({"losses": BASE + STEP + 400}, ALIAS),
+                                        ({"ids": BASE + STEP}, ALIAS), ({"z": BASE + 5 * STEP + 4}, ALIAS),
+                                        ({"t": BASE + STEP + 40}, ALIAS)])
+def test_distill_refusals(binding, bad, status):
+    fmt = binding._DISTILL_ARGS
+    assert isinstance(fmt, struct.Struct)
+    assert binding.load_library().loss_distill_cross_entropy(Args(fmt, list(DISTILL), list(DISTILL.values())).pack(bad),
+                                                             None) == status
+
+
+def test_distill_nothing_to_do(binding):
+    a = Args(binding._DISTILL_ARGS, list(DISTILL), list(DISTILL.values()))
+    lib = binding.load_library()
+    assert lib.loss_distill_cross_entropy(a.pack({"S": 0, "l": 0, "t": 0, "losses": 0}), None) == OK
+    assert lib.loss_distill_cross_entropy(None, None) == NULL
+
+
+def test_binding_refuses(binding):
+    """Tensors of the wrong kind are refused before the library is called."""
+    torch = pytest.importorskip("torch")
+    q = torch.zeros(4, 2, 32)
+    with pytest.raises(ValueError):
+        binding.attention(q, q, q)                          # not on a GPU
+    with pytest.raises(TypeError):
+        binding.attention(q[0], q, q)
+    with pytest.raises(ValueError):
+        binding.attention(q, torch.zeros(4, 3, 32), q)      # 2 heads do not share 3
+    with pytest.raises(ValueError):
+        binding.attention(q, q, q, window=-1)
+    with pytest.raises(TypeError):
+        binding.attention(q, q, q, cu_seqlens=torch.zeros(2, dtype=torch.int64))
+    with pytest.raises(ValueError):
+        binding.attention(q, q, q, cu_seqlens=torch.zeros(0, dtype=torch.int32))
+    w, pos = torch.ones(32), torch.zeros(4, dtype=torch.int32)
+    with pytest.raises(ValueError):
+        binding.qk_norm_rope(q, q, w, w, pos, torch.ones(16))
+    with pytest.raises(ValueError):
+        binding.qk_norm_rope(q, q, w, w, pos, torch.ones(17))   # more pairs than the head has
+    with pytest.raises(TypeError):
+        binding.qk_norm_rope(q, q, w, w, pos.float(), torch.ones(16))
+    l, ids = torch.zeros(3, 8), torch.zeros(3, 2, dtype=torch.int32)
+    with pytest.raises(ValueError):
+        binding.distill_cross_entropy(l, pos[:3], ids, torch.zeros(3, 2))

@@ -1,0 +1,297 @@
+"""attention and attention_backward on the GPU against the oracle
+(oracle/attention.py): every head width of the kernels and widths between
+them, shared heads, causal and sliding-window masks, packed sequences of one
+token, of none, and ending anywhere in a tile, strided views, rows of no
+sequence, poisoned neighbours, offsets past 32 bits, other streams and graph
+replays.  The bounds are the oracle's, counted per element."""
+import numpy as np
+import pytest
+
+from oracle import attention as OA
+
+from _gpu import device, say, to_dev
+
+pytestmark = pytest.mark.gpu
+
+SENTINEL = -777.0
+
+
+def cu_of(lengths, first=0):
+    return np.cumsum([first] + list(lengths)).astype(np.int32)
+
+
+class Case:
+    """Device tensors of an attention call: q, k, v as views in `layout`,
+    everything around them NaN, rows of no sequence NaN as well."""
+
+    def __init__(self, seed, lengths, first=0, tail=0, hq=2, hk=1, d=64, layout="qkv", causal=True, window=0,
+                 scale=None, gain=1.0):
+        import torch
+        r = np.random.default_rng(seed)
+        self.T = T = first + sum(lengths) + tail
+        self.kw = {"causal": causal, "window": window, "scale": scale}
+        self.cu = None if lengths == [T] else cu_of(lengths, first)
+        self.shapes = ((T, hq, d), (T, hk, d), (T, hk, d))
+        self.host = [(r.standard_normal(s) * gain).astype(np.float32) for s in self.shapes]
+        self.g = r.standard_normal(self.shapes[0]).astype(np.float32)
+        self.used = np.zeros(T, bool)
+        for a, b in OA.sequences(self.cu, T):
+            self.used[a:b] = True
+        self.layout = layout
+        self.q, self.k, self.v = self.fill(self.views(float("nan")), self.host)
+        self.dcu = None if self.cu is None else to_dev(self.cu)
+        (self.dout,) = self.fill([torch.full(self.shapes[0], float("nan"), device=device())], [self.g])
+
+    def views(self, value):
+        """Three tensors of the q, k, v shapes in this case's layout, filled with `value`."""
+        import torch
+        T = self.T
+        if self.layout == "qkv":      # one projection's columns, 4 unused ones behind
+            w = [s[1] * s[2] for s in self.shapes]
+            buf = torch.full((T, sum(w) + 4), value, device=device())
+            self.buffer = buf
+            at = np.cumsum([0] + w)
+            return [buf[:, at[i]:at[i + 1]].unflatten(1, self.shapes[i][1:]) for i in range(3)]
+        if self.layout == "heads":    # [heads, tokens, head_dim], 8 unused rows a head
+            return [torch.full((s[1], T + 8, s[2]), value, device=device())[:, :T].transpose(0, 1)
+                    for s in self.shapes]
+        return [torch.full(s, value, device=device()) for s in self.shapes]
+
+    def fill(self, views, arrays):
+        for t, a in zip(views, arrays):
+            rows = to_dev(np.flatnonzero(self.used))
+            t[rows] = to_dev(a[self.used])
+        return views
+
+    def clean(self, a):
+        return np.where(self.used[:, None, None], a, 0.0)
+
+    def oracle_args(self):
+        kw = dict(self.kw)
+        return [self.clean(x) for x in self.host], {"cu": self.cu, **kw}
+
+
+def call(c, **kw):
+    from tiled_dense_gemm_matmul_amd import binding
+    return binding.attention(c.q, c.k, c.v, cu_seqlens=c.dcu, **c.kw, **kw)
+
+
+def call_backward(c, out, lse, **kw):
+    from tiled_dense_gemm_matmul_amd import binding
+    return binding.attention_backward(c.dout, c.q, c.k, c.v, out, lse, cu_seqlens=c.dcu, **c.kw, **kw)
+
+
+def check(c, label):
+    import torch
+    out, lse = call(c)
+    torch.cuda.synchronize()
+    args, kw = c.oracle_args()
+    ro, rl, eo, el = OA.attention(*args, **kw)
+    for name, y, ref, err in (("out", out, ro, eo), ("lse", lse, rl, el)):
+        res = OA.compare(y.cpu().numpy(), ref, err)
+        say(f"  {label} {name}: max err/bound {res['max_ratio']:.3g}, fails {res['fails']} of {res['n']}")
+        assert res["fails"] == 0, (label, name, res)
+    got = call_backward(c, out, lse)
+    torch.cuda.synchronize()
+    # from the out and lse that the call was given
+    want = OA.attention_backward(c.clean(c.g), *args, out.cpu().numpy(), lse.cpu().numpy(), **kw)
+    for name, y, ref, err in zip(("dq", "dk", "dv"), got, want[:3], want[3:]):
+        res = OA.compare(y.cpu().numpy(), ref, err)
+        say(f"  {label} {name}: max err/bound {res['max_ratio']:.3g}, fails {res['fails']} of {res['n']}")
+        assert res["fails"] == 0, (label, name, res)
+
+
+@pytest.mark.parametrize("d", [4, 12, 20, 32, 36, 48, 64, 72, 80, 96, 100, 128])
+def test_head_widths(d):
+    say(f"attention head_dim {d}")
+    check(Case(d, [70, 33], hq=2, hk=1, d=d), f"D={d}")
+
+
+@pytest.mark.parametrize("d", [32, 64, 96, 128])
+@pytest.mark.parametrize("causal,window", [(True, 0), (False, 0), (True, 1), (True, 37), (False, 1), (False, 37)])
+def test_masks_on_many_rows(d, causal, window):
+    """Enough heads and rows that a workgroup's waves hold their own rows."""
+    say(f"attention D={d} causal={causal} window={window}")
+    check(Case(d + window, [300, 1, 0, 131, 80], first=3, tail=7, hq=96, hk=96, d=d, causal=causal, window=window,
+               layout="dense"), f"D={d} {causal} {window}")
+
+
+@pytest.mark.parametrize("lengths", [[1], [2], [15], [16], [17], [63], [64], [65], [1] * 40, [0, 5, 0, 0, 3, 0],
+                                     [127, 129], [513], list(range(1, 24))])
+@pytest.mark.parametrize("causal", [True, False])
+def test_lengths(lengths, causal):
+    say(f"attention lengths {lengths} causal={causal}")
+    check(Case(len(lengths), lengths, hq=3, hk=3, d=32, causal=causal), str(lengths)[:30])
+
+
+@pytest.mark.parametrize("hq,hk", [(1, 1), (4, 1), (6, 2), (5, 5), (16, 2), (200, 50)])
+@pytest.mark.parametrize("layout", ["qkv", "heads", "dense"])
+def test_shared_heads_and_layouts(hq, hk, layout):
+    say(f"attention heads {hq}/{hk} {layout}")
+    check(Case(hq, [200, 57], first=1, tail=5, hq=hq, hk=hk, d=64, layout=layout, window=90), f"{hq}/{hk} {layout}")
+
+
+def test_many_sequences():
+    """More sequences than one look of 64 finds, some empty."""
+    r = np.random.default_rng(3)
+    lengths = [int(x) for x in r.integers(0, 9, 300)]
+    check(Case(4, lengths, tail=3, hq=2, hk=1, d=32), "300 sequences")
+
+
+@pytest.mark.parametrize("gain,scale", [(6.0, None), (1.0, 2.5), (0.01, 1e-4)])
+def test_scales(gain, scale):
+    """Scores from nearly equal to ones whose exponentials underflow."""
+    check(Case(9, [150], hq=2, hk=2, d=64, gain=gain, scale=scale), f"gain {gain} scale {scale}")
+
+
+def test_empty():
+    import torch
+    from tiled_dense_gemm_matmul_amd import binding
+    dev = device()
+    q = torch.empty((0, 2, 32), device=dev)
+    out, lse = binding.attention(q, q, q)
+    assert out.shape == (0, 2, 32) and lse.shape == (2, 0)
+    assert [x.shape for x in binding.attention_backward(q, q, q, q, out, lse)] == [(0, 2, 32)] * 3
+    # no sequence at all: every row is outside
+    q = torch.full((37, 2, 32), float("nan"), device=dev)
+    cu = torch.zeros(1, dtype=torch.int32, device=dev)
+    out, lse = binding.attention(q, q, q, cu_seqlens=cu)
+    grads = binding.attention_backward(q, q, q, q, q, lse, cu_seqlens=cu)
+    torch.cuda.synchronize()
+    assert not out.any() and bool((lse == -float("inf")).all()) and not any(bool(x.any()) for x in grads)
+
+
+def test_bounds_of_sequences_are_clamped():
+    """Entries outside [0, tokens] read as the nearest bound."""
+    import torch
+    from tiled_dense_gemm_matmul_amd import binding
+    c = Case(5, [50], hq=2, hk=1, d=32, layout="dense")
+    far = torch.tensor([-9, 20, 1000], dtype=torch.int32, device=device())
+    near = torch.tensor([0, 20, 50], dtype=torch.int32, device=device())
+    got = binding.attention(c.q, c.k, c.v, cu_seqlens=far)
+    want = binding.attention(c.q, c.k, c.v, cu_seqlens=near)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    got = binding.attention_backward(c.dout, c.q, c.k, c.v, *want, cu_seqlens=far)
+    want = binding.attention_backward(c.dout, c.q, c.k, c.v, *want, cu_seqlens=near)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("heads", [2, 64])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_nothing_passes_between_sequences(heads, bad):
+    """A sequence's results do not depend on another's values, finite or not."""
+    import torch
+    c = Case(6, [90, 70, 101], hq=heads, hk=heads, d=64, layout="dense")
+    out, lse = call(c)
+    grads = call_backward(c, out, lse)
+    for t in (c.q, c.k, c.v, c.dout):
+        t[90:160] = bad
+    out2, lse2 = call(c)
+    grads2 = call_backward(c, out2, lse2)
+    for a, b in zip((out, *grads), (out2, *grads2)):
+        assert torch.equal(a[:90], b[:90]) and torch.equal(a[160:], b[160:])
+    assert torch.equal(lse[:, :90], lse2[:, :90]) and torch.equal(lse[:, 160:], lse2[:, 160:])
+
+
+@pytest.mark.parametrize("heads", [2, 64])
+def test_writes_stay_inside(heads):
+    """Outputs in the layout of the inputs, with everything around them kept."""
+    import torch
+    c = Case(7, [77, 100], first=2, tail=3, hq=heads, hk=heads // 2, d=48)
+    plain = call(c)
+    grads = call_backward(c, *plain)
+    dq, dk, dv = c.views(SENTINEL)
+    buf = c.buffer
+    call_backward(c, *plain, dq=dq, dk=dk, dv=dv)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(grads, (dq, dk, dv)))
+    assert bool((buf[:, -4:] == SENTINEL).all())
+    wide = torch.full((c.T + 2, heads + 1, 52), SENTINEL, device=device())
+    out = wide[1:-1, :heads, :48]
+    call(c, out=out)
+    torch.cuda.synchronize()
+    assert torch.equal(out, plain[0])
+    wide[1:-1, :heads, :48] = SENTINEL
+    assert bool((wide == SENTINEL).all())
+    # out over q
+    q = c.q.clone()
+    c.q = q
+    got, _ = call(c, out=q)
+    assert got is q and torch.equal(q, plain[0])
+
+
+def test_offsets_past_32_bits():
+    """Rows 16 K values apart, past 8 GiB into the buffer: sampled tiles of a windowed sequence."""
+    import torch
+    from tiled_dense_gemm_matmul_amd import binding
+    T, st, d, w = 140000, 16384, 32, 8
+    buf = torch.empty((T, st), device=device())
+    g = torch.Generator(device=device())
+    g.manual_seed(1)
+    small = torch.randn((T, 4 * d), generator=g, device=device())
+    buf[:, 64:64 + 4 * d] = small
+    q, k, v, do = (buf[:, 64 + i * d:64 + (i + 1) * d].unflatten(1, (1, d)) for i in range(4))
+    out, lse = binding.attention(q, k, v, window=w)
+    dense = [x.contiguous() for x in (q, k, v, do)]
+    out2, lse2 = binding.attention(*dense[:3], window=w)
+    assert torch.equal(out, out2) and torch.equal(lse, lse2)
+    a = binding.attention_backward(do, q, k, v, out, lse, window=w)
+    b = binding.attention_backward(dense[3], *dense[:3], out, lse, window=w)
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+    rows = slice(T - 200, T)
+    ro, _, eo, _ = OA.attention(*[x[rows].cpu().numpy() for x in dense[:3]], window=w)
+    res = OA.compare(out[rows][w:].cpu().numpy(), ro[w:], eo[w:])
+    assert res["fails"] == 0, res
+    del buf, a, b, q, k, v, do
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("heads", [2, 64])
+def test_repeated_calls_give_the_same_bits(heads):
+    import torch
+    c = Case(8, [211, 90], hq=heads, hk=heads // 2, d=64)
+    out, lse = call(c)
+    grads = call_backward(c, out, lse)
+    for _ in range(3):
+        o2, l2 = call(c)
+        g2 = call_backward(c, out, lse)
+        assert torch.equal(out, o2) and torch.equal(lse, l2) and all(torch.equal(a, b) for a, b in zip(grads, g2))
+
+
+def test_streams_and_graphs():
+    """Calls queued on two streams at once, and two captured graphs replayed
+    in turn with eager calls between, give the eager bits."""
+    import torch
+    cases = [Case(10 + i, [200, 50 + i], hq=4, hk=2, d=64) for i in range(2)]
+
+    def step(c):
+        out, lse = call(c)
+        return (out, lse, *call_backward(c, out, lse))
+
+    want = [step(c) for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    got = []
+    for _ in range(4):
+        got = []
+        for c, s in zip(cases, streams):
+            with torch.cuda.stream(s):
+                got.append(step(c))
+    torch.cuda.synchronize()
+    for a, b in zip(want, got):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+    graphs, held = [], []
+    for c in cases:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            held.append(step(c))
+        graphs.append(g)
+    for turn in range(3):
+        for c in cases:
+            c.q.mul_(1.25)
+        fresh = [step(c) for c in cases]
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(fresh, held):
+            assert all(torch.equal(x, y) for x, y in zip(a, b)), turn

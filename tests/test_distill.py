@@ -1,0 +1,199 @@
+"""distill_cross_entropy on the GPU against the oracle (oracle/loss.py): each
+launch shape and its edges, rows of any length and alignment, the streaming
+path, teachers of one entry to 1024, unused, repeated and infinite entries,
+padding rows, the gradient in place and apart, index and logit types, and
+graph replays.  The bounds are cross_entropy's: the same exponentials and
+sums of the same length make up both losses."""
+import numpy as np
+import pytest
+
+from oracle import loss as OL
+from tiled_dense_gemm_matmul_amd import inputs
+
+from _gpu import device, say, to_dev
+
+pytestmark = pytest.mark.gpu
+
+PARAMS = [(1.0, 0.5, 0.0, 0.0), (2.0, 0.7, 0.1, 1e-4), (0.5, 0.25, 0.0, 0.01), (3.0, 1.0, 0.0, 0.0)]
+
+
+def case(seed, S, V, K, scale=2.0, half=False, ids64=False, targets64=False, ignore_every=5):
+    r = np.random.default_rng(seed)
+    c = inputs.loss_case(seed, S, V, scale=scale)
+    t = c["targets"].astype(np.int64 if targets64 else np.int32)
+    if ignore_every:
+        t[ignore_every - 1::ignore_every] = -1
+    ids = r.integers(0, max(V, 1), (S, K)).astype(np.int64 if ids64 else np.int32)
+    z = (r.standard_normal((S, K)) * 2 + 5).astype(np.float16 if half else np.float32)
+    if K > 2 and S > 1:
+        ids[0, K - 1] = ids[0, 0]        # one column twice
+        ids[1, ::3] = -1                 # unused entries, whatever their logit
+        z[1, 0] = np.nan
+        ids[1, 1] = t[1] if t[1] >= 0 else 0
+    if S > 2 and K:
+        ids[2] = V                       # no used entry
+        z[2, 0] = np.inf
+    if S > 3 and K:
+        z[3] = -np.inf                   # no mass
+        z[3, K // 2] = 1.0
+    return {"logits": c["logits"], "targets": t, "ids": ids, "teacher": z}
+
+
+def run(c, tau, mix, alpha, beta, inv_norm, apart=False, logits=None):
+    import torch
+    from tiled_dense_gemm_matmul_amd import binding
+    logits = to_dev(c["logits"]) if logits is None else logits
+    dl = torch.full_like(logits, float("nan")) if apart else None
+    losses = binding.distill_cross_entropy(logits, None if c["targets"] is None else to_dev(c["targets"]),
+                                           to_dev(c["ids"]), to_dev(c["teacher"]), tau, mix, alpha, beta, inv_norm,
+                                           dlogits=dl)
+    torch.cuda.synchronize()
+    return losses, dl if apart else logits
+
+
+def check(c, losses, grad, params, inv_norm, label):
+    import oracle
+    rl, rg, mag = OL.distill(c["logits"], c["targets"], c["ids"], c["teacher"], *params, inv_norm=inv_norm)
+    a = oracle.compare(losses.cpu().numpy(), rl, mag["loss"], OL.TOL_LOSS)
+    b = oracle.compare(grad.cpu().numpy(), rg, mag["dlogits"], OL.TOL_DLOGITS)
+    say(f"  {label}: losses max err/tol {a['max_ratio']:.3g} fails {a['fails']}; "
+        f"dlogits max err/tol {b['max_ratio']:.3g} fails {b['fails']} of {b['n']}")
+    assert a["fails"] == 0 and b["fails"] == 0, (a, b)
+
+
+@pytest.mark.parametrize("V", [1, 2, 3, 5, 100, 1001, 4093, 4096, 4097, 8191, 8192, 8193, 16384, 16385, 32767, 32768,
+                               32771, 50257, 50304, 65535, 65536, 65537, 70001])
+def test_row_lengths(V):
+    say(f"distill V={V}")
+    c = case(V, 7, V, 9)
+    for i, params in enumerate(PARAMS[:2]):
+        losses, grad = run(c, *params, 0.125, apart=bool(i))
+        check(c, losses, grad, params, 0.125, f"V={V} {params}")
+
+
+@pytest.mark.parametrize("K", [0, 1, 2, 63, 64, 65, 255, 256, 257, 700, 1024])
+@pytest.mark.parametrize("params", PARAMS)
+def test_teachers(K, params):
+    say(f"distill K={K} {params}")
+    c = case(K, 6, 3001, K, half=K % 2 == 0, ids64=K % 3 == 0, targets64=K % 2 == 1)
+    losses, grad = run(c, *params, 0.5)
+    check(c, losses, grad, params, 0.5, f"K={K}")
+
+
+@pytest.mark.parametrize("off,apart_off", [(1, None), (2, None), (3, None), (0, 0), (1, 1), (0, 1), (3, 2)])
+def test_alignment(off, apart_off):
+    """Logits at every offset from a 16-byte boundary, the gradient over them,
+    at the same offset and at another; nothing beside either is touched."""
+    import torch
+    from tiled_dense_gemm_matmul_amd import binding
+    S, V, params = 5, 5003, PARAMS[1]
+    c = case(off, S, V, 20)
+
+    def at(o, fill):
+        buf = torch.full((S * V + 64,), fill, device=device())
+        return buf, buf[16 + o:16 + o + S * V].view(S, V)
+    lbuf, l = at(off, float("nan"))
+    l.copy_(to_dev(c["logits"]))
+    gbuf, g = (lbuf, l) if apart_off is None else at(apart_off, float("nan"))
+    losses = binding.distill_cross_entropy(l, to_dev(c["targets"]), to_dev(c["ids"]), to_dev(c["teacher"]), *params,
+                                           0.5, dlogits=None if apart_off is None else g)
+    torch.cuda.synchronize()
+    check(c, losses, g, params, 0.5, f"offsets {off} {apart_off}")
+    o = off if apart_off is None else apart_off
+    assert bool(gbuf[:16 + o].isnan().all()) and bool(gbuf[16 + o + S * V:].isnan().all())
+    if apart_off is not None:
+        assert np.array_equal(l.cpu().numpy(), c["logits"])
+
+
+def test_one_column_everywhere():
+    """All entries of a row on one column, which is also the target."""
+    c = case(1, 4, 500, 300, ignore_every=0)
+    c["ids"][:] = c["targets"][:, None]
+    c["teacher"] = np.zeros_like(c["teacher"])
+    losses, grad = run(c, *PARAMS[1], 1.0)
+    check(c, losses, grad, PARAMS[1], 1.0, "one column")
+
+
+def test_without_targets():
+    c = case(2, 6, 2000, 30)
+    c["targets"] = None
+    losses, grad = run(c, 2.0, 1.0, 0.0, 0.0, 0.5)
+    check(c, losses, grad, (2.0, 1.0, 0.0, 0.0), 0.5, "no targets")
+
+
+def test_masked_vocabulary():
+    """Logits of minus infinity take no part; a teacher entry on one without
+    mass adds nothing."""
+    import torch
+    c = case(3, 4, 3000, 12, ignore_every=0)
+    c["logits"][:, 100:900] = -np.inf
+    c["targets"][:] = 5
+    c["ids"][:] = np.arange(1000, 1012)
+    c["teacher"][:] = 1.0
+    c["ids"][0, 3], c["teacher"][0, 3] = 200, -np.inf
+    losses, grad = run(c, 2.0, 0.5, 0.0, 0.0, 1.0)
+    assert bool(torch.isfinite(losses).all()) and bool(torch.isfinite(grad).all()) and not grad[:, 100:900].any()
+    keep = np.r_[0:100, 900:3000]
+    d = {**c, "logits": c["logits"][:, keep], "ids": np.where(c["ids"] >= 900, c["ids"] - 800, -1)}
+    check(d, losses, grad[:, to_dev(keep)], (2.0, 0.5, 0.0, 0.0), 1.0, "masked")
+
+
+def test_no_teacher_is_cross_entropy():
+    """mix 0 gives cross_entropy's loss and gradient."""
+    from tiled_dense_gemm_matmul_amd import binding
+    import oracle
+    c = case(4, 20, 5000, 8)
+    losses, grad = run(c, 2.0, 0.0, 0.1, 1e-3, 0.25)
+    l = to_dev(c["logits"])
+    plain = binding.cross_entropy(l, to_dev(c["targets"]), alpha=0.1, beta=1e-3, inv_norm=0.25)
+    rl, rg, mag = OL.cross_entropy(c["logits"], np.where(c["targets"] < 0, 5000, c["targets"]), 0.1, 1e-3, 0.25)
+    for y in (losses[0], plain):
+        assert oracle.compare(y.cpu().numpy(), rl, mag["loss"], OL.TOL_LOSS)["fails"] == 0
+    for y in (grad, l):
+        assert oracle.compare(y.cpu().numpy(), rg, mag["dlogits"], OL.TOL_DLOGITS)["fails"] == 0
+
+
+def test_degenerate_and_default_norm():
+    import torch
+    from tiled_dense_gemm_matmul_amd import binding
+    dev = device()
+    ids, z = torch.empty((0, 4), dtype=torch.int32, device=dev), torch.empty((0, 4), device=dev)
+    none = torch.empty(0, dtype=torch.int32, device=dev)
+    assert binding.distill_cross_entropy(torch.empty((0, 8), device=dev), none, ids, z).shape == (2, 0)
+    ids, z = torch.zeros((3, 4), dtype=torch.int32, device=dev), torch.zeros((3, 4), device=dev)
+    out = binding.distill_cross_entropy(torch.empty((3, 0), device=dev),
+                                        torch.zeros(3, dtype=torch.int32, device=dev), ids, z)
+    assert out.shape == (2, 3) and not out.any()
+    c = case(5, 10, 600, 5)
+    kept = int((c["targets"] >= 0).sum())
+    a = run(c, 1.0, 0.5, 0.0, 0.0, None)
+    b = run(c, 1.0, 0.5, 0.0, 0.0, 1.0 / kept)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    big = c["targets"].astype(np.int64)
+    big[0] = 1 << 32           # no 32-bit reading of it is a column
+    losses, grad = run({**c, "targets": big}, 1.0, 0.5, 0.0, 0.0, 1.0)
+    assert not losses[:, 0].any() and not grad[0].any()
+
+
+def test_repeats_and_graphs():
+    import torch
+    from tiled_dense_gemm_matmul_amd import binding
+    c = case(6, 40, 20000, 64)
+    l, t, ids, z = (to_dev(c[x]) for x in ("logits", "targets", "ids", "teacher"))
+    dl = torch.empty_like(l)
+
+    def step():
+        return binding.distill_cross_entropy(l, t, ids, z, 2.0, 0.5, 0.1, 1e-4, 0.1, dlogits=dl)
+    want, grad = step().clone(), dl.clone()
+    for _ in range(3):
+        assert torch.equal(step(), want) and torch.equal(dl, grad)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        held = step()
+    for _ in range(3):
+        l.mul_(1.1)
+        want, grad = step().clone(), dl.clone()
+        dl.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(held, want) and torch.equal(dl, grad)

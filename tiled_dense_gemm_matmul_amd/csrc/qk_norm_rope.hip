@@ -12,8 +12,9 @@
 //    alignment allow it, else W = 1.
 //  * The dimensions that are not rotated are paired in the same way and turned by
 //    the angle zero, so a head is one kind of pair throughout.
-//  * The angle pos * inv_freq is formed in 64 bits and reduced there to a
-//    part of a turn, which fp32 then holds to 2^-25 of a turn at any position.
+//  * The angle pos * inv_freq is formed and reduced to a part of a turn in 64
+//    bits, with the rounding errors of both products carried along, so the
+//    part of a turn is good to fp32 at any position up to 2^53.
 //  * The weight's gradient sums over all tokens and heads: fp32 over a token's
 //    heads in a lane, then 64 bits over tokens, lanes, waves and workgroups,
 //    each in a fixed order; a second small kernel adds the workgroups' parts.
@@ -96,11 +97,17 @@ __device__ __forceinline__ void write_pairs(const Norm &n, float *head, Place at
 
 // Cosine and sine of the angle of pair p at a token (1 and 0 past the rotated pairs).
 __device__ __forceinline__ void turn(const Norm &n, double pos, int p, float &c, float &s) {
+#pragma clang fp contract(off)  // the products' roundings are taken as they are
     c = 1.0f;
     s = 0.0f;
     if (p < n.half) {
-        const double turns = pos * (double)n.inv_freq[p] * 0.15915494309189533577;
-        sincospif(2.0f * (float)(turns - rint(turns)), &s, &c);
+        // 1 / (2 pi) as the sum of two doubles
+        constexpr double kTurn = 0x1.45f306dc9c883p-3, kTurnLow = -0x1.6b01ec5417056p-57;
+        const double f = (double)n.inv_freq[p];
+        const double angle = pos * f, angle_low = fma(pos, f, -angle);
+        const double turns = angle * kTurn;
+        const double low = fma(angle, kTurn, -turns) + (angle * kTurnLow + angle_low * kTurn);
+        sincospif(2.0f * (float)((turns - rint(turns)) + low), &s, &c);
     }
 }
 __device__ __forceinline__ double position(const Norm &n, int t) {
@@ -453,13 +460,21 @@ int attn_qk_norm_rope_backward(const attn_qk_norm_rope_backward_args *args, void
                                  ((o == &dq) == (x == &gq || x == &q));
                 if (!own && overlap(*o, *x, T, D)) return GEMM_ERR_ALIAS;
             }
-            if (covers_shared(*o, a.n) || in_range(*o, a.workspace, need, T, D) ||
-                in_range(*o, a.dq_weight, D * 4, T, D) || in_range(*o, a.dk_weight, D * 4, T, D))
-                return GEMM_ERR_ALIAS;
+            if (covers_shared(*o, a.n)) return GEMM_ERR_ALIAS;
         }
         if (overlap(dq, dk, T, D)) return GEMM_ERR_ALIAS;
-        for (const View *x : {&gq, &gk, &q, &k})
-            if (in_range(*x, a.workspace, need, T, D)) return GEMM_ERR_ALIAS;
+    }
+    // the weights' gradients and the scratch apart from everything else
+    const Span small[3] = {{a.dq_weight, D * 4}, {a.dk_weight, D * 4}, {a.workspace, need}};
+    const Span shared[4] = {{a.n.q_weight, D * 4}, {a.n.k_weight, D * 4}, {a.n.inv_freq, a.n.rotated * 2},
+                            {a.n.positions, T * (a.n.positions64 ? 8 : 4)}};
+    for (int i = 0; i < 3; ++i) {
+        for (int j = 0; j < i; ++j)
+            if (spans_overlap(small[i], small[j])) return GEMM_ERR_ALIAS;
+        for (const Span &x : shared)
+            if (spans_overlap(small[i], x)) return GEMM_ERR_ALIAS;
+        for (const View *x : {&gq, &gk, &q, &k, &dq, &dk})
+            if (T > 0 && in_range(*x, small[i].p, small[i].bytes, T, D)) return GEMM_ERR_ALIAS;
     }
     const attn_tensor *all[6] = {&a.dq_out, &a.dk_out, &a.q, &a.k, &a.dq, &a.dk};
     const bool vec = vector_access(a.n, all, 6, HQ);

@@ -51,6 +51,15 @@ bool in_range(const View &v, const void *p, int64_t bytes, int64_t tokens, int64
     return p != nullptr && a0 < b0 + (uintptr_t)bytes && b0 < a0 + (uintptr_t)extent(v, tokens, d);
 }
 
+struct Span {
+    const void *p;
+    int64_t bytes;
+};
+bool spans_overlap(const Span &a, const Span &b) {
+    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
+    return a.p && b.p && a.bytes > 0 && b.bytes > 0 && a0 < b0 + (uintptr_t)b.bytes && b0 < a0 + (uintptr_t)a.bytes;
+}
+
 // The strides of an output keep its rows apart: heads inside a token's row, or
 // tokens inside a head.
 bool rows_apart(const View &v, int64_t tokens, int64_t d) {
