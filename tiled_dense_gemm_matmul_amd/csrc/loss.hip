@@ -33,6 +33,7 @@
 
 #include <cmath>
 #include <initializer_list>
+#include <type_traits>
 #include <utility>
 
 #include "gemm_fwd.h"
@@ -242,16 +243,32 @@ __global__ __launch_bounds__(NT) void sum_losses_kernel(const float *losses, flo
 // --- distillation ---
 //
 // One workgroup per row again.  The gradient of both terms is a function of
-// the logit and the column alone, A e^(l - max) + B e^((l - max) / tau) + C,
-// but for the target's column and the teacher's: those few are written once
-// more, with their subtractions, after the row.  Bound by memory like
-// cross_entropy: each logit is read once and its gradient written once while
-// the row fits in the registers (65536 logits); longer rows are read twice,
-// the maximum and the sums being formed in one pass over the row.
+// the logit alone, A e^(l - max) + B e^((l - max) / tau) + C, but for the
+// target's column and the teacher's: those few are written once more, with
+// their subtractions, after the row.  Bound by memory like cross_entropy:
+// each logit is read once and its gradient written once while the row fits in
+// the registers (65536 logits); longer rows are read twice, the maximum and
+// the sums being formed in one pass over the row.
 //
-// 16-byte accesses start at the row's first 16-byte boundary, so rows of any
-// length and any 4-byte alignment take them; the up to three logits in front
-// of the boundary and behind the last whole group go to one thread each.
+//  * 16-byte accesses start at the row's first 16-byte boundary, so rows of
+//    any length and any 4-byte alignment take them; the up to three logits in
+//    front of the boundary and behind the last whole group go to one thread
+//    each.
+//  * Between its loads and its stores a row meets two barriers: one for the
+//    maximum (and the teacher's entries, in LDS), one for all sums together.
+//    The last wave, whose share of the row is the smallest, forms the
+//    teacher's statistics between the two, and all threads together look for
+//    columns that several entries name: K^2 comparisons by K threads alone
+//    took as long as half of a 4096-logit row.
+//  * Rows of 16385 to 51200 logits take 512 threads with 64 or 100 logits
+//    each, so that two rows share a CU and one's loads run under the other's
+//    reductions and stores: 4096 x 32000 in 184 us (5.7 TB/s) against 230
+//    with 1024 threads of 32, 4093 x 50257 in 322 us (5.1 TB/s) against 343
+//    with 1024 of 64.  The bound of four waves a SIMD that this needs costs the
+//    100-logit kernel 20 to 68 bytes of spilled registers a thread; without
+//    it one row would have the CU to itself (354 us).
+//  * tau = 1 (T1) makes both exponentials one, which is then kept in place of
+//    the logit, as in cross_entropy.
 constexpr int kMaxTop = 1024;  // teacher entries a row
 
 struct Distill {
@@ -269,119 +286,207 @@ __device__ __forceinline__ int column(const void *p, int wide, int64_t i, int V)
     const int64_t v = wide ? ((const int64_t *)p)[i] : (int64_t)((const int *)p)[i];
     return v >= 0 && v < V ? (int)v : -1;
 }
-
-// The sums of a row that its losses and its gradient are made of.
-struct RowSums {
-    float top, inv_hard, lse, inv_soft, log_soft, sum_l;
-};
-
-// The teacher's distribution over a row's used entries, with the student's
-// logits there, in LDS.
-struct Teacher {
-    int id[kMaxTop];
-    float mass[kMaxTop], l[kMaxTop];
-};
-
-// Loads and normalises it: thread t takes entries t, t + NT, ...  Returns
-// whether any entry has mass.  All threads call it; the student's row is not
-// written before the next barrier.
-template <int NT>
-__device__ __forceinline__ bool load_teacher(const Distill &a, int s, const float *row, Teacher &t, float *logt_sum,
-                                             float *slots) {
-    constexpr int NW = NT / 64;
-    const int64_t base = (int64_t)s * a.K;
-    float m = -INFINITY;
-    for (int j = threadIdx.x; j < a.K; j += NT) {
-        const int id = column(a.ids, a.ids64, base + j, a.V);
-        float z = a.half ? (float)((const _Float16 *)a.teacher)[base + j] : ((const float *)a.teacher)[base + j];
-        z *= a.inv_tau;
-        t.id[j] = id;
-        t.mass[j] = z;
-        t.l[j] = id >= 0 ? row[id] : 0.0f;
-        // a NaN stays in the sum below; the maximum passes over it
-        if (id >= 0) m = fmaxf(m, z);
-    }
-    m = block_reduce<NW, true>(m, slots);
-    const float ref = m == -INFINITY ? 0.0f : m;
-    float se = 0.0f;
-    for (int j = threadIdx.x; j < a.K; j += NT) {
-        const float e = t.id[j] >= 0 ? expf(t.mass[j] - ref) : 0.0f;
-        se += e;
-    }
-    se = block_reduce<NW, false>(se, slots + NW);
-    const bool has = se != 0.0f;  // NaN counts: it is passed on
-    const float inv = has ? 1.0f / se : 0.0f, ln = has ? logf(se) : 0.0f;
-    // sum of mass * log(mass), and the masses in place of the logits
-    float h = 0.0f;
-    for (int j = threadIdx.x; j < a.K; j += NT) {
-        const float z = t.mass[j] - ref;
-        const float e = t.id[j] >= 0 && has ? expf(z) * inv : 0.0f;
-        if (e != 0.0f) h += e * (z - ln);
-        t.mass[j] = e;
-    }
-    *logt_sum = h;
-    return has;
+__device__ __forceinline__ float teacher_logit(const Distill &a, int64_t i) {
+    return a.half ? (float)((const _Float16 *)a.teacher)[i] : ((const float *)a.teacher)[i];
 }
 
-// Losses of the row, and the columns whose gradient differs from the rest.
-// Called after the row's gradient has been written and a barrier.
-template <int NT>
-__device__ __forceinline__ void finish_row(const Distill &a, int s, int tgt, float l_t, const RowSums &r, bool has,
-                                           float logt_sum, const Teacher &t, float *grad, float A, float B, float C,
-                                           float *slots) {
-    constexpr int NW = NT / 64;
-    float kd = logt_sum;
-    for (int j = threadIdx.x; j < a.K; j += NT) {
-        const float mass = t.mass[j];
-        if (mass != 0.0f) kd -= mass * ((t.l[j] - r.top) * a.inv_tau - r.log_soft);
-    }
-    kd = block_reduce<NW, false>(kd, slots);
-    const float hit = (1.0f - a.mix) * (1.0f - a.alpha) * a.inv_norm, soft = a.mix * a.tau * a.inv_norm;
-    if (threadIdx.x == 0) {
-        a.losses[s] = tgt >= 0 ? row_loss(r.lse, l_t, r.sum_l / (float)a.V, a.alpha, a.beta) : 0.0f;
-        a.losses[a.S + s] = has ? a.tau * a.tau * kd : 0.0f;
-    }
-    auto value = [&](float l) {
-        const float d = l - r.top;
-        return A * __expf(d) + B * __expf(d * a.inv_tau) + C;
+// Sum or maximum over the wave's lanes, the same in every lane: shifts within
+// rows of 16 lanes, then broadcasts into the next rows (a butterfly through
+// LDS takes several times as long).
+template <bool MAX>
+__device__ __forceinline__ float lanes_reduce(float v) {
+    const int none = MAX ? __builtin_bit_cast(int, -INFINITY) : 0;
+    auto step = [&](auto ctrl, auto rows) {
+        const float u = __builtin_bit_cast(
+            float, __builtin_amdgcn_update_dpp(none, __builtin_bit_cast(int, v), ctrl.value, rows.value, 0xf, false));
+        v = MAX ? fmaxf(v, u) : v + u;
     };
-    // The first entry of a column writes it, with the masses of all of that
-    // column's entries in their order.
-    bool target_taken = false;
-    for (int j = threadIdx.x; j < a.K; j += NT) {
+    using std::integral_constant;
+    step(integral_constant<int, 0x111>(), integral_constant<int, 0xf>());  // row_shr:1
+    step(integral_constant<int, 0x112>(), integral_constant<int, 0xf>());  // row_shr:2
+    step(integral_constant<int, 0x114>(), integral_constant<int, 0xf>());  // row_shr:4
+    step(integral_constant<int, 0x118>(), integral_constant<int, 0xf>());  // row_shr:8
+    step(integral_constant<int, 0x142>(), integral_constant<int, 0xa>());  // row_bcast:15
+    step(integral_constant<int, 0x143>(), integral_constant<int, 0xc>());  // row_bcast:31
+    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
+}
+
+// The teacher's distribution over a row's used entries: mass j =
+// exp(z[j] - ref) inv, its logarithm z[j] - ref - log_sum.
+struct Masses {
+    float ref, inv, log_sum;
+    int any;  // some entry has mass (or is NaN, which is passed on)
+};
+
+// A row's teacher entries in LDS: columns (-1: not used), the teacher's
+// logits over tau, the student's logits there, and whether another entry
+// names the same column.
+struct Teacher {
+    __align__(16) int id[kMaxTop];
+    float z[kMaxTop], l[kMaxTop];
+    unsigned char twice[kMaxTop];
+    Masses mass;
+};
+
+__device__ __forceinline__ Masses masses(const Teacher &t, int K) {
+    const int lane = threadIdx.x & 63;
+    float m = -INFINITY, se = 0.0f;
+    for (int j = lane; j < K; j += 64)
+        if (t.id[j] >= 0) m = fmaxf(m, t.z[j]);
+    m = lanes_reduce<true>(m);
+    Masses r;
+    r.ref = m == -INFINITY ? 0.0f : m;
+    for (int j = lane; j < K; j += 64)
+        if (t.id[j] >= 0) se += expf(t.z[j] - r.ref);
+    se = lanes_reduce<false>(se);
+    r.any = se != 0.0f;
+    r.inv = r.any ? 1.0f / se : 0.0f;
+    r.log_sum = r.any ? logf(se) : 0.0f;
+    return r;
+}
+__device__ __forceinline__ float mass_of(const Teacher &t, const Masses &r, int j) {
+    return r.any && t.id[j] >= 0 ? expf(t.z[j] - r.ref) * r.inv : 0.0f;
+}
+
+// Marks the entries whose column another entry names too.  Entries are dealt
+// to the threads, and with fewer entries than threads so are the entries that
+// each is compared with, four at a time.
+template <int NT>
+__device__ __forceinline__ void mark_repeats(Teacher &t, int K) {
+    int span = 64;  // threads for one entry each: a power of two
+    while (span < K && span < NT) span *= 2;
+    const int parts = NT / span, part = threadIdx.x / span;
+    for (int j = threadIdx.x & (span - 1); j < K; j += span) {
         const int id = t.id[j];
         if (id < 0) continue;
-        bool first = true;
-        float mass = 0.0f;
-        for (int i = 0; i < a.K; ++i) {
-            if (t.id[i] != id) continue;
-            first = first && i >= j;
-            mass += t.mass[i];
+        bool twice = false;
+        for (int q = 4 * part; q < K; q += 4 * parts) {
+            const int4 u = *(const int4 *)&t.id[q];
+            twice |= (u.x == id && q != j) | (u.y == id && q + 1 != j) | (u.z == id && q + 2 != j) |
+                     (u.w == id && q + 3 != j);
         }
-        if (first) grad[id] = value(t.l[j]) - soft * mass - (id == tgt ? hit : 0.0f);
-        target_taken = target_taken || id == tgt;
+        if (twice) t.twice[j] = 1;
     }
-    if (!__syncthreads_or(target_taken) && threadIdx.x == 0 && tgt >= 0) grad[tgt] = value(l_t) - hit;
 }
 
-// The factors of the row's gradient from its sums.
-__device__ __forceinline__ void factors(const Distill &a, int tgt, const RowSums &r, bool has, float &A, float &B,
-                                        float &C) {
-    const float hard = tgt >= 0 ? (1.0f - a.mix) * a.inv_norm : 0.0f;
-    A = hard * (1.0f + 2.0f * a.beta * r.lse) * r.inv_hard;
-    B = has ? a.mix * a.tau * a.inv_norm * r.inv_soft : 0.0f;
-    C = -hard * (a.alpha / (float)a.V);
-}
-
-__device__ __forceinline__ RowSums row_sums(const Distill &a, float top, float hard, float soft, float sum_l) {
+// What a row's losses and gradient are made of.
+struct RowSums {
+    float top, lse, log_soft, sum_l;
+    float A, B, C;  // the gradient's factors
+};
+__device__ __forceinline__ RowSums row_sums(const Distill &a, int tgt, bool taught, float top, float hard, float soft,
+                                            float sum_l) {
     RowSums r;
     r.top = top;
-    r.inv_hard = 1.0f / hard;
     r.lse = top + logf(hard);
-    r.inv_soft = 1.0f / soft;
     r.log_soft = logf(soft);
-    r.sum_l = sum_l;
+    r.sum_l = a.alpha > 0.0f ? sum_l : 0.0f;  // logits of minus infinity take part in it only when it is asked for
+    const float weight = tgt >= 0 ? (1.0f - a.mix) * a.inv_norm : 0.0f;
+    r.A = weight * (1.0f + 2.0f * a.beta * r.lse) / hard;
+    r.B = taught ? a.mix * a.tau * a.inv_norm / soft : 0.0f;
+    r.C = -weight * (a.alpha / (float)a.V);
     return r;
+}
+
+// e^x of x <= 0 for both terms' gradients and sums.
+template <bool T1>
+__device__ __forceinline__ float gradient(const Distill &a, const RowSums &r, float l) {
+    const float d = l - r.top;
+    if (T1) return (r.A + r.B) * __expf(d) + r.C;
+    return r.A * __expf(d) + r.B * __expf(d * a.inv_tau) + r.C;
+}
+
+// Sums three values over the workgroup at once, in wave order.
+template <int NW>
+__device__ __forceinline__ void block_sum3(float &x, float &y, float &z, float (*slots)[NW]) {
+    x = lanes_reduce<false>(x);
+    y = lanes_reduce<false>(y);
+    z = lanes_reduce<false>(z);
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    if (lane == 0) {
+        slots[0][wave] = x;
+        slots[1][wave] = y;
+        slots[2][wave] = z;
+    }
+    __syncthreads();
+    x = slots[0][0];
+    y = slots[1][0];
+    z = slots[2][0];
+#pragma unroll
+    for (int w = 1; w < NW; ++w) {
+        x += slots[0][w];
+        y += slots[1][w];
+        z += slots[2][w];
+    }
+}
+
+// Puts entries first, first + NT, ... of a row's teacher into LDS.
+template <int NT>
+__device__ __forceinline__ void load_teacher(const Distill &a, int s, const float *row, Teacher &t, int first) {
+    for (int j = first; j < a.K; j += NT) {
+        const int64_t i = (int64_t)s * a.K + j;
+        const int id = column(a.ids, a.ids64, i, a.V);
+        t.id[j] = id;
+        t.twice[j] = 0;
+        t.z[j] = teacher_logit(a, i) * a.inv_tau;
+        t.l[j] = id >= 0 ? row[id] : 0.0f;
+    }
+    // whole groups of four for the comparisons
+    if (threadIdx.x < 3 && a.K + (int)threadIdx.x < kMaxTop) t.id[a.K + threadIdx.x] = -1;
+}
+
+// The row's losses, and the columns whose gradient differs from the rest's.
+// Called once the stores of the row's gradient have been issued; waits for
+// them before any such column is written again.
+template <int NT, bool T1>
+__device__ __forceinline__ void finish_row(const Distill &a, int s, int tgt, float l_t, const RowSums &r,
+                                           const Masses &mass, const Teacher &t, float *grad) {
+    const int tid = threadIdx.x;
+    const float hit = (1.0f - a.mix) * (1.0f - a.alpha) * a.inv_norm, soft = a.mix * a.tau * a.inv_norm;
+    // Entry j of a thread is j = tid + NT i.  The first entry of a column
+    // writes it, with the masses of all of that column's entries in their order.
+    constexpr int EACH = (kMaxTop + NT - 1) / NT;
+    float value[EACH];
+    bool mine[EACH], target_named = false;
+#pragma unroll
+    for (int i = 0; i < EACH; ++i) {
+        const int j = tid + NT * i;
+        mine[i] = false;
+        const int id = j < a.K ? t.id[j] : -1;
+        if (id < 0) continue;
+        bool first = true;
+        float m = mass_of(t, mass, j);
+        if (t.twice[j]) {
+            m = 0.0f;
+            for (int e = 0; e < a.K; ++e) {
+                if (t.id[e] != id) continue;
+                first = first && e >= j;
+                m += mass_of(t, mass, e);
+            }
+        }
+        target_named = target_named || id == tgt;
+        mine[i] = first;
+        value[i] = gradient<T1>(a, r, t.l[j]) - soft * m - (id == tgt ? hit : 0.0f);
+    }
+    if (tid >= NT - 64) {
+        float kd = 0.0f;
+        for (int j = tid - (NT - 64); j < a.K; j += 64) {
+            const float m = mass_of(t, mass, j);
+            if (m != 0.0f)
+                kd += m * ((t.z[j] - mass.ref - mass.log_sum) - ((t.l[j] - r.top) * a.inv_tau - r.log_soft));
+        }
+        kd = lanes_reduce<false>(kd);
+        if (tid == NT - 1) {
+            a.losses[s] = tgt >= 0 ? row_loss(r.lse, l_t, r.sum_l / (float)a.V, a.alpha, a.beta) : 0.0f;
+            a.losses[(size_t)a.S + s] = mass.any ? a.tau * a.tau * kd : 0.0f;
+        }
+    }
+    __builtin_amdgcn_s_waitcnt(0);  // this wave's stores of the row are complete
+    const bool named = __syncthreads_or(target_named);
+#pragma unroll
+    for (int i = 0; i < EACH; ++i)
+        if (mine[i]) grad[t.id[tid + NT * i]] = value[i];
+    if (!named && tid == 0 && tgt >= 0) grad[tgt] = gradient<T1>(a, r, l_t) - hit;
 }
 
 // The row's layout for 16-byte accesses: `head` logits in front of the first
@@ -404,10 +509,10 @@ __device__ __forceinline__ int edge_column(const RowShape &r) {
     return -1;
 }
 
-template <int NT, int CAP, bool STREAM>
-__global__ __launch_bounds__(NT) void distill_resident(Distill a) {
+template <int NT, int CAP, bool STREAM, bool T1>
+__global__ __launch_bounds__(NT, CAP == 100 ? 4 : 1) void distill_resident(Distill a) {
     constexpr int NW = NT / 64, G = CAP / 4, POL = STREAM ? kNonTemporal : 0;
-    __shared__ float red[8][NW];
+    __shared__ float red[4][NW];
     __shared__ Teacher teacher;
     const int tid = threadIdx.x, s = blockIdx.x;
     const float *row = a.logits + (size_t)s * a.V;
@@ -431,9 +536,8 @@ __global__ __launch_bounds__(NT) void distill_resident(Distill a) {
         x[j] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rr, off(j), 0, POL));
     const float xe = edge >= 0 ? row[edge] : -INFINITY;
     const float l_t = tgt >= 0 ? row[tgt] : 0.0f;
+    load_teacher<NT>(a, s, row, teacher, tid);
     const int nv = shape.groups > tid ? min(G, (shape.groups - tid + NT - 1) / NT) : 0;  // this thread's groups
-    float logt_sum;
-    const bool has = load_teacher<NT>(a, s, row, teacher, &logt_sum, red[0]);
     float m = xe, sl = edge >= 0 ? xe : 0.0f;
 #pragma unroll
     for (int j = 0; j < G; ++j) {
@@ -442,58 +546,61 @@ __global__ __launch_bounds__(NT) void distill_resident(Distill a) {
             sl += (x[j][0] + x[j][1]) + (x[j][2] + x[j][3]);
         }
     }
-    const float top = block_reduce<NW, true>(m, red[2]);
+    // The barrier in here also makes the teacher's entries visible, and all
+    // reads of the row lie before it.
+    const float top = block_reduce<NW, true>(m, red[0]);
     float hard = 0.0f, soft = 0.0f;
     if (edge >= 0) {
         hard = __expf(xe - top);
-        soft = __expf((xe - top) * a.inv_tau);
+        if (!T1) soft = __expf((xe - top) * a.inv_tau);
     }
 #pragma unroll
     for (int j = 0; j < G; ++j) {
         if (j < nv) {
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                const float d = x[j][c] - top;
-                hard += __expf(d);
-                soft += __expf(d * a.inv_tau);
+                const float d = x[j][c] - top, e = __expf(d);
+                hard += e;
+                if (T1) x[j][c] = e;
+                else soft += __expf(d * a.inv_tau);
             }
         }
     }
-    hard = block_reduce<NW, false>(hard, red[3]);
-    soft = block_reduce<NW, false>(soft, red[4]);
-    const float sum_l = a.alpha > 0.0f ? block_reduce<NW, false>(sl, red[5]) : 0.0f;
-    const RowSums r = row_sums(a, top, hard, soft, sum_l);
-    float A, B, C;
-    factors(a, tgt, r, has, A, B, C);
-    // All reads of the row lie before the barriers above.
+    mark_repeats<NT>(teacher, a.K);
+    if (tid >= NT - 64) {
+        const Masses of = masses(teacher, a.K);
+        if (tid == NT - 1) teacher.mass = of;
+    }
+    block_sum3<NW>(hard, soft, sl, &red[1]);
+    const Masses mass = teacher.mass;
+    const RowSums r = row_sums(a, tgt, mass.any, top, hard, T1 ? hard : soft, sl);
 #pragma unroll
     for (int j = 0; j < G; ++j) {
         f32x4 g;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            const float d = x[j][c] - top;
-            g[c] = A * __expf(d) + B * __expf(d * a.inv_tau) + C;
-        }
+        for (int c = 0; c < 4; ++c) g[c] = T1 ? (r.A + r.B) * x[j][c] + r.C : gradient<false>(a, r, x[j][c]);
         __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4v, g), rg, off(j), 0, POL);
     }
-    if (edge >= 0) grad[edge] = A * __expf(xe - top) + B * __expf((xe - top) * a.inv_tau) + C;
-    // the stores above have to be complete before other waves write the same columns
-    __builtin_amdgcn_s_waitcnt(0);
-    __syncthreads();
-    finish_row<NT>(a, s, tgt, l_t, r, has, logt_sum, teacher, grad, A, B, C, red[6]);
+    if (edge >= 0) grad[edge] = gradient<T1>(a, r, xe);
+    finish_row<NT, T1>(a, s, tgt, l_t, r, mass, teacher, grad);
 }
 
 // Rows too long for the registers, or whose gradient lies at another
-// alignment than the row: one pass for the maximum and the sums, each thread
-// moving its own reference when it meets a larger logit, one for the gradient.
-template <int NT>
+// alignment than the row (VEC false: 4-byte accesses): one pass for the
+// maximum and the sums, each thread moving its own reference when it meets a
+// larger logit, one for the gradient.
+template <int NT, bool VEC>
 __global__ __launch_bounds__(NT) void distill_stream(Distill a) {
     constexpr int NW = NT / 64;
-    __shared__ float red[8][NW];
+    __shared__ float red[4][NW];
     __shared__ Teacher teacher;
     const int tid = threadIdx.x, s = blockIdx.x;
     const float *row = a.logits + (size_t)s * a.V;
     float *grad = a.grad + (size_t)s * a.V;
+    const RowShape shape = VEC ? row_shape(row, a.V) : RowShape{0, 0, 0};
+    const int edge = VEC ? edge_column(shape) : -1;
+    const f32x4 *groups = (const f32x4 *)(row + shape.head);
+    f32x4 *out = (f32x4 *)(grad + shape.head);
     const int tgt = a.targets ? column(a.targets, a.targets64, s, a.V) : -1;
     if (a.targets && tgt < 0) {
         if (tid < 2) a.losses[(size_t)tid * a.S + s] = 0.0f;
@@ -501,36 +608,68 @@ __global__ __launch_bounds__(NT) void distill_stream(Distill a) {
         return;
     }
     const float l_t = tgt >= 0 ? row[tgt] : 0.0f;
-    float logt_sum;
-    const bool has = load_teacher<NT>(a, s, row, teacher, &logt_sum, red[0]);
-    float m = -INFINITY, hard = 0.0f, soft = 0.0f, sl = 0.0f;
-    for (int v = tid; v < a.V; v += NT) {
-        const float l = row[v];
-        sl += l;
+    load_teacher<NT>(a, s, row, teacher, tid);
+    float m = -INFINITY, ref = 0.0f, hard = 0.0f, soft = 0.0f, sl = 0.0f;
+    auto raise = [&](float l) {  // to a larger reference
         if (l > m) {
-            hard *= __expf(m - l);
-            soft *= __expf((m - l) * a.inv_tau);
-            m = l;
+            if (m != -INFINITY) {
+                hard *= __expf(m - l);
+                soft *= __expf((m - l) * a.inv_tau);
+            }
+            m = ref = l;
         }
-        const float d = l == m ? 0.0f : l - m;  // also where both are minus infinity
-        hard += __expf(d);
-        soft += __expf(d * a.inv_tau);
+    };
+    auto add = [&](float l) {
+        sl += l;
+        hard += __expf(l - ref);
+        soft += __expf((l - ref) * a.inv_tau);
+    };
+    if (VEC) {
+        for (int i = tid; i < shape.groups; i += NT) {
+            const f32x4 l = groups[i];
+            raise(fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3])));
+#pragma unroll
+            for (int c = 0; c < 4; ++c) add(l[c]);
+        }
+        if (edge >= 0) {
+            raise(row[edge]);
+            add(row[edge]);
+        }
+    } else {
+        for (int v = tid; v < a.V; v += NT) {
+            const float l = row[v];
+            raise(l);
+            add(l);
+        }
     }
-    const float top = block_reduce<NW, true>(m, red[2]);
-    const float d0 = m == -INFINITY ? -INFINITY : m - top;
-    hard = block_reduce<NW, false>(m == -INFINITY ? 0.0f : hard * __expf(d0), red[3]);
-    soft = block_reduce<NW, false>(m == -INFINITY ? 0.0f : soft * __expf(d0 * a.inv_tau), red[4]);
-    const float sum_l = a.alpha > 0.0f ? block_reduce<NW, false>(sl, red[5]) : 0.0f;
-    const RowSums r = row_sums(a, top, hard, soft, sum_l);
-    float A, B, C;
-    factors(a, tgt, r, has, A, B, C);
-    for (int v = tid; v < a.V; v += NT) {
-        const float d = row[v] - top;
-        grad[v] = A * __expf(d) + B * __expf(d * a.inv_tau) + C;
+    const float top = block_reduce<NW, true>(m, red[0]);
+    if (m == -INFINITY) {  // nothing above minus infinity here
+        // a NaN's sums stay NaN
+    } else {
+        hard *= __expf(m - top);
+        soft *= __expf((m - top) * a.inv_tau);
     }
-    __builtin_amdgcn_s_waitcnt(0);
-    __syncthreads();
-    finish_row<NT>(a, s, tgt, l_t, r, has, logt_sum, teacher, grad, A, B, C, red[6]);
+    mark_repeats<NT>(teacher, a.K);
+    if (tid >= NT - 64) {
+        const Masses of = masses(teacher, a.K);
+        if (tid == NT - 1) teacher.mass = of;
+    }
+    block_sum3<NW>(hard, soft, sl, &red[1]);
+    const Masses mass = teacher.mass;
+    const RowSums r = row_sums(a, tgt, mass.any, top, hard, soft, sl);
+    if (VEC) {
+        for (int i = tid; i < shape.groups; i += NT) {
+            const f32x4 l = groups[i];
+            f32x4 g;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) g[c] = gradient<false>(a, r, l[c]);
+            out[i] = g;
+        }
+        if (edge >= 0) grad[edge] = gradient<false>(a, r, row[edge]);
+    } else {
+        for (int v = tid; v < a.V; v += NT) grad[v] = gradient<false>(a, r, row[v]);
+    }
+    finish_row<NT, false>(a, s, tgt, l_t, r, mass, teacher, grad);
 }
 
 bool overlaps(const void *a, size_t abytes, const void *b, size_t bbytes) {
@@ -652,17 +791,25 @@ int loss_distill_cross_entropy(const loss_distill_args *args, void *stream) {
     hipStream_t st = static_cast<hipStream_t>(stream);
     const bool nt = S * V * 4 >= kStreamBytes;
     const bool same_phase = ((reinterpret_cast<uintptr_t>(p.logits) ^ reinterpret_cast<uintptr_t>(p.dlogits)) & 15) == 0;
-#define DISTILL(NT, CAP)                                                                                     \
+#define DISTILL_AS(NT, CAP, T1)                                                                              \
     do {                                                                                                     \
-        if (nt) hipLaunchKernelGGL((distill_resident<NT, CAP, true>), dim3(a.S), dim3(NT), 0, st, a);        \
-        else hipLaunchKernelGGL((distill_resident<NT, CAP, false>), dim3(a.S), dim3(NT), 0, st, a);          \
+        if (nt) hipLaunchKernelGGL((distill_resident<NT, CAP, true, T1>), dim3(a.S), dim3(NT), 0, st, a);    \
+        else hipLaunchKernelGGL((distill_resident<NT, CAP, false, T1>), dim3(a.S), dim3(NT), 0, st, a);      \
     } while (0)
-    if (!same_phase || V > 1024 * 64) hipLaunchKernelGGL((distill_stream<1024>), dim3(a.S), dim3(1024), 0, st, a);
+#define DISTILL(NT, CAP)                       \
+    do {                                       \
+        if (tau == 1.0f) DISTILL_AS(NT, CAP, true); \
+        else DISTILL_AS(NT, CAP, false);       \
+    } while (0)
+    if (!same_phase) hipLaunchKernelGGL((distill_stream<1024, false>), dim3(a.S), dim3(1024), 0, st, a);
+    else if (V > 1024 * 64) hipLaunchKernelGGL((distill_stream<1024, true>), dim3(a.S), dim3(1024), 0, st, a);
     else if (V <= 256 * 16) DISTILL(256, 16);
     else if (V <= 512 * 16) DISTILL(512, 16);
     else if (V <= 512 * 32) DISTILL(512, 32);
-    else if (V <= 1024 * 32) DISTILL(1024, 32);
+    else if (V <= 512 * 64) DISTILL(512, 64);
+    else if (V <= 512 * 100) DISTILL(512, 100);
     else DISTILL(1024, 64);
+#undef DISTILL_AS
 #undef DISTILL
     return hipGetLastError() == hipSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
 }
