@@ -134,16 +134,11 @@ __global__ __launch_bounds__(256) void qk_norm_rope_fwd(Norm n, Strided q, Strid
     Place at[NP];
     bool in[NP];
     float c[NP][W], s[NP][W];
-    Pairs<W> wq[NP], wk[NP];
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
         const int p = (i * G + part) * W;
         in[i] = p < n.d / 2;
         at[i] = place(n, p, W);
-        if (in[i]) {
-            wq[i] = read_pairs<W>(n, n.qw, at[i]);
-            wk[i] = read_pairs<W>(n, n.kw, at[i]);
-        }
 #pragma unroll
         for (int e = 0; e < W; ++e) turn(n, pos, p + e, c[i][e], s[i][e]);
     }
@@ -152,12 +147,14 @@ __global__ __launch_bounds__(256) void qk_norm_rope_fwd(Norm n, Strided q, Strid
         const bool isq = h < n.hq;
         const float *x = isq ? q.p + t * q.st + h * q.sh : k.p + t * k.st + (h - n.hq) * k.sh;
         float *y = isq ? yq.p + t * yq.st + h * yq.sh : yk.p + t * yk.st + (h - n.hq) * yk.sh;
-        Pairs<W> v[NP];
+        const float *weight = isq ? n.qw : n.kw;
+        Pairs<W> v[NP], w[NP];
         float sq = 0.0f;
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
             if (in[i]) {
                 v[i] = read_pairs<W>(n, x, at[i]);
+                w[i] = read_pairs<W>(n, weight, at[i]);
 #pragma unroll
                 for (int e = 0; e < W; ++e) sq += v[i].a[e] * v[i].a[e] + v[i].b[e] * v[i].b[e];
             }
@@ -169,8 +166,8 @@ __global__ __launch_bounds__(256) void qk_norm_rope_fwd(Norm n, Strided q, Strid
             Pairs<W> o;
 #pragma unroll
             for (int e = 0; e < W; ++e) {
-                const float a = v[i].a[e] * r * (isq ? wq[i].a[e] : wk[i].a[e]);
-                const float b = v[i].b[e] * r * (isq ? wq[i].b[e] : wk[i].b[e]);
+                const float a = v[i].a[e] * r * w[i].a[e];
+                const float b = v[i].b[e] * r * w[i].b[e];
                 o.a[e] = a * c[i][e] - b * s[i][e];
                 o.b[e] = b * c[i][e] + a * s[i][e];
             }
@@ -182,31 +179,30 @@ __global__ __launch_bounds__(256) void qk_norm_rope_fwd(Norm n, Strided q, Strid
 // Backward.  Workgroup b writes its part of the weights' gradients, 2 D
 // doubles, to parts + 2 D b: each lane's sums, added over the lanes of one
 // pair in lane order and over the waves in wave order.
+constexpr int kWaves = 8;    // of a workgroup of the backward pass
+constexpr int kParts = 512;  // workgroups of the backward pass at most: two a CU
+
 template <int W, int G, int NP>
-__global__ __launch_bounds__(256) void qk_norm_rope_bwd(Norm n, Strided gq, Strided gk, Strided q, Strided k, Strided dq,
+__global__ __launch_bounds__(64 * kWaves) void qk_norm_rope_bwd(Norm n, Strided gq, Strided gk, Strided q, Strided k, Strided dq,
                                                         Strided dk, double *parts, int chunks) {
     constexpr int HW = 64 / G;
     const int lane = threadIdx.x & 63, part = lane % G, slot = lane / G;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     Place at[NP];
     bool in[NP];
-    Pairs<W> wq[NP], wk[NP];
     double sums[2][NP][2 * W];
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
         const int p = (i * G + part) * W;
         in[i] = p < n.d / 2;
         at[i] = place(n, p, W);
-        if (in[i]) {
-            wq[i] = read_pairs<W>(n, n.qw, at[i]);
-            wk[i] = read_pairs<W>(n, n.kw, at[i]);
-        }
 #pragma unroll
         for (int e = 0; e < 2 * W; ++e) sums[0][i][e] = sums[1][i][e] = 0.0;
     }
     const int heads = n.hq + n.hk;
     const int64_t items = (int64_t)n.tokens * chunks;
-    for (int64_t item = (int64_t)blockIdx.x * 4 + wave; item < items; item += (int64_t)gridDim.x * 4) {
+    for (int64_t item = (int64_t)blockIdx.x * kWaves + wave; item < items;
+         item += (int64_t)gridDim.x * kWaves) {
         const int t = (int)(item / chunks), chunk = (int)(item % chunks);
         const double pos = position(n, t);
         float c[NP][W], s[NP][W];
@@ -225,20 +221,22 @@ __global__ __launch_bounds__(256) void qk_norm_rope_bwd(Norm n, Strided gq, Stri
             const float *x = isq ? q.p + t * q.st + hh * q.sh : k.p + t * k.st + hh * k.sh;
             const float *g = isq ? gq.p + t * gq.st + hh * gq.sh : gk.p + t * gk.st + hh * gk.sh;
             float *d = isq ? dq.p + t * dq.st + hh * dq.sh : dk.p + t * dk.st + hh * dk.sh;
-            Pairs<W> v[NP], dn[NP];
+            const float *weight = isq ? n.qw : n.kw;
+            Pairs<W> v[NP], dn[NP], w[NP];
             float sq = 0.0f, dot = 0.0f;
 #pragma unroll
             for (int i = 0; i < NP; ++i) {
                 if (!in[i]) continue;
                 v[i] = read_pairs<W>(n, x, at[i]);
                 const Pairs<W> y = read_pairs<W>(n, g, at[i]);
+                w[i] = read_pairs<W>(n, weight, at[i]);
 #pragma unroll
                 for (int e = 0; e < W; ++e) {
                     dn[i].a[e] = y.a[e] * c[i][e] + y.b[e] * s[i][e];
                     dn[i].b[e] = y.b[e] * c[i][e] - y.a[e] * s[i][e];
                     sq += v[i].a[e] * v[i].a[e] + v[i].b[e] * v[i].b[e];
-                    dot += dn[i].a[e] * (isq ? wq[i].a[e] : wk[i].a[e]) * v[i].a[e] +
-                           dn[i].b[e] * (isq ? wq[i].b[e] : wk[i].b[e]) * v[i].b[e];
+                    dot += dn[i].a[e] * w[i].a[e] * v[i].a[e] +
+                           dn[i].b[e] * w[i].b[e] * v[i].b[e];
                 }
             }
             const float r = rsqrtf(lanes_sum<G>(sq) * n.inv_d + n.eps);
@@ -249,8 +247,8 @@ __global__ __launch_bounds__(256) void qk_norm_rope_bwd(Norm n, Strided gq, Stri
                 Pairs<W> o;
 #pragma unroll
                 for (int e = 0; e < W; ++e) {
-                    o.a[e] = r * (dn[i].a[e] * (isq ? wq[i].a[e] : wk[i].a[e]) - v[i].a[e] * f);
-                    o.b[e] = r * (dn[i].b[e] * (isq ? wq[i].b[e] : wk[i].b[e]) - v[i].b[e] * f);
+                    o.a[e] = r * (dn[i].a[e] * w[i].a[e] - v[i].a[e] * f);
+                    o.b[e] = r * (dn[i].b[e] * w[i].b[e] - v[i].b[e] * f);
                     const float pa = dn[i].a[e] * v[i].a[e] * r, pb = dn[i].b[e] * v[i].b[e] * r;
                     dw[0][i][e] += isq ? pa : 0.0f;
                     dw[0][i][W + e] += isq ? pb : 0.0f;
@@ -268,7 +266,7 @@ __global__ __launch_bounds__(256) void qk_norm_rope_bwd(Norm n, Strided gq, Stri
                 for (int e = 0; e < 2 * W; ++e) sums[a][i][e] += (double)dw[a][i][e];
     }
     // lanes of one pair, then waves
-    __shared__ double wsum[4][2][2 * W * G * NP];
+    __shared__ double wsum[kWaves][2][2 * W * G * NP];
 #pragma unroll
     for (int a = 0; a < 2; ++a)
 #pragma unroll
@@ -281,11 +279,13 @@ __global__ __launch_bounds__(256) void qk_norm_rope_bwd(Norm n, Strided gq, Stri
                 if (slot == 0) wsum[wave][a][((i * G + part) * 2 * W) + e] = v;
             }
     __syncthreads();
-    for (int j = threadIdx.x; j < 2 * 2 * W * G * NP; j += 256) {
+    for (int j = threadIdx.x; j < 2 * 2 * W * G * NP; j += 64 * kWaves) {
         const int a = j / (2 * W * G * NP), r = j % (2 * W * G * NP);
         const int p = r / (2 * W) * W, e = r % (2 * W);
         if (p >= n.d / 2) continue;
-        const double v = (wsum[0][a][r] + wsum[1][a][r]) + (wsum[2][a][r] + wsum[3][a][r]);
+        double v = wsum[0][a][r];
+#pragma unroll
+        for (int w = 1; w < kWaves; ++w) v += wsum[w][a][r];
         const Place w = place(n, p, W);
         const int d = n.interleaved ? w.first + 2 * (e % W) + e / W : (e < W ? w.first + e : w.second + e - W);
         parts[((int64_t)blockIdx.x * 2 + a) * n.d + d] = v;
@@ -293,18 +293,27 @@ __global__ __launch_bounds__(256) void qk_norm_rope_bwd(Norm n, Strided gq, Stri
 }
 
 // The weights' gradients from the workgroups' parts: one workgroup takes 16
-// values, each added over every 16th part by one thread and then over the 16
-// threads in order.
-__global__ __launch_bounds__(256) void weight_grads(const double *parts, int nparts, float *dqw, float *dkw, int d) {
-    __shared__ double sum[16][16];
-    const int col = blockIdx.x * 16 + (threadIdx.x & 15), first = threadIdx.x >> 4;
+// values, each added over every 64th part by one thread and then over the 64
+// threads in order.  Eight loads are in flight together, so the up to 512
+// parts cost one trip to memory (a thread for every 16th part took 20 us for
+// 1024 parts).
+__global__ __launch_bounds__(1024) void weight_grads(const double *parts, int nparts, float *dqw, float *dkw, int d) {
+    __shared__ double sum[64][16];
+    const int c = threadIdx.x & 15, col = blockIdx.x * 16 + c, first = threadIdx.x >> 4;
+    double part[kParts / 64];
+#pragma unroll
+    for (int i = 0; i < kParts / 64; ++i) {
+        const int b = first + 64 * i;
+        part[i] = col < 2 * d && b < nparts ? parts[(int64_t)b * 2 * d + col] : 0.0;
+    }
     double v = 0.0;
-    if (col < 2 * d)
-        for (int b = first; b < nparts; b += 16) v += parts[(int64_t)b * 2 * d + col];
-    sum[first][threadIdx.x & 15] = v;
+#pragma unroll
+    for (int i = 0; i < kParts / 64; ++i) v += part[i];
+    sum[first][c] = v;
     __syncthreads();
     if (first == 0 && col < 2 * d) {
-        for (int w = 1; w < 16; ++w) v += sum[w][threadIdx.x & 15];
+#pragma unroll
+        for (int w = 1; w < 64; ++w) v += sum[w][c];
         (col < d ? dqw[col] : dkw[col - d]) = (float)v;
     }
 }
@@ -377,8 +386,15 @@ int lanes_of(int64_t d, int w) {
     return g;
 }
 
-// Workgroups of the backward pass: up to eight a CU, each wave with a token or more.
-int64_t backward_groups(int64_t tokens) { return std::max<int64_t>(1, std::min<int64_t>((tokens + 3) / 4, 1024)); }
+// Waves a token's heads are split over, so that a few tokens still fill the
+// chip: one token of 40 heads of 128 would take one wave 10 rounds of loads.
+int chunks_of(int64_t tokens, int64_t heads, int heads_a_wave) {
+    const int64_t rounds = (heads + heads_a_wave - 1) / heads_a_wave;
+    return (int)std::max<int64_t>(1, std::min<int64_t>(rounds, 4096 / tokens));
+}
+
+// Workgroups of the backward pass with every wave at work.
+int64_t backward_groups(int64_t items) { return std::max<int64_t>(1, std::min<int64_t>((items + kWaves - 1) / kWaves, kParts)); }
 
 #define NORM_BY_LANES(LAUNCH)                                                                                 \
     do {                                                                                                      \
@@ -424,7 +440,7 @@ int attn_qk_norm_rope(const attn_qk_norm_rope_args *args, void *stream) {
     hipStream_t hs = static_cast<hipStream_t>(stream);
 #define FWD(W, G, NP)                                                                                              \
     do {                                                                                                            \
-        const int chunks = 1;                                                                                       \
+        const int chunks = chunks_of(T, HQ + HK, 64 / G);                                                           \
         const int64_t grid = (T * chunks + 3) / 4;                                                                  \
         hipLaunchKernelGGL((qk_norm_rope_fwd<W, G, NP>), dim3((unsigned)grid), dim3(256), 0, hs, n, sq, sk, oq, ok, \
                            chunks);                                                                                 \
@@ -436,7 +452,7 @@ int attn_qk_norm_rope(const attn_qk_norm_rope_args *args, void *stream) {
 
 int64_t attn_qk_norm_rope_workspace_bytes(int64_t tokens, int64_t head_dim) {
     if (tokens < 0 || tokens >= ((int64_t)1 << 30) || head_dim < 2 || head_dim > 256) return -1;
-    return backward_groups(tokens) * 2 * head_dim * 8;
+    return kParts * 2 * head_dim * 8;
 }
 
 int attn_qk_norm_rope_backward(const attn_qk_norm_rope_backward_args *args, void *stream) {
@@ -483,12 +499,17 @@ int attn_qk_norm_rope_backward(const attn_qk_norm_rope_backward_args *args, void
                   sk = strided(a.k, T, HK), o0 = strided(a.dq, T, HQ), o1 = strided(a.dk, T, HK);
     hipStream_t hs = static_cast<hipStream_t>(stream);
     double *parts = static_cast<double *>(a.workspace);
-    const int grid = (int)backward_groups(T);
-#define BWD(W, G, NP)                                                                                                \
-    hipLaunchKernelGGL((qk_norm_rope_bwd<W, G, NP>), dim3(grid), dim3(256), 0, hs, n, g0, g1, sq, sk, o0, o1, parts, 1)
+    int grid = 1;
+#define BWD(W, G, NP)                                                                                                  \
+    do {                                                                                                                \
+        const int chunks = T > 0 ? chunks_of(T, HQ + HK, 64 / G) : 1;                                                   \
+        grid = (int)backward_groups(T * chunks);                                                                        \
+        hipLaunchKernelGGL((qk_norm_rope_bwd<W, G, NP>), dim3(grid), dim3(64 * kWaves), 0, hs, n, g0, g1, sq, sk, o0,  \
+                           o1, parts, chunks);                                                                          \
+    } while (0)
     NORM_BY_LANES(BWD);
 #undef BWD
-    hipLaunchKernelGGL(weight_grads, dim3((unsigned)((2 * D + 15) / 16)), dim3(256), 0, hs, parts, grid, a.dq_weight,
+    hipLaunchKernelGGL(weight_grads, dim3((unsigned)((2 * D + 15) / 16)), dim3(1024), 0, hs, parts, grid, a.dq_weight,
                        a.dk_weight, (int)D);
     return hipGetLastError() == hipSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
 }
