@@ -8,11 +8,11 @@
 // is 10 D flops, but then dq or dk and dv would be summed by atomics, whose
 // order changes results, or kept as [tokens, tokens] arrays.)
 //
-//  * No operand passes through LDS.  A wave holds 16 rows (or keys) in
+//  * No operand passes through LDS.  A wave holds 16 or 32 rows (or keys) in
 //    registers and walks over blocks of 16 of the other side, whose operands
-//    it loads from memory straight into the registers that the MFMA reads;
-//    the four waves of a workgroup walk over the same blocks close together,
-//    so most of these loads hit the CU's L1.
+//    it loads from memory straight into the registers that the MFMA reads,
+//    each under one product or more before its own (a load of 4 KiB takes
+//    place of 32 to 64 MFMAs' 1024 to 2048 cycles).
 //  * The probabilities never leave the registers either.  A 16 x 16 product
 //    leaves lane (g, m) = (lane / 16, lane % 16) with its rows 4g .. 4g + 3
 //    of column m.  That is the B operand of the next product when its
@@ -29,10 +29,17 @@
 //    values past head_dim read as zeros, and offsets stay small however long
 //    the buffer is.
 //
-// A workgroup owns a tile of rows of one sequence and one head.  Where there
-// are enough tiles for the chip its waves own 16 rows each (WS = 1); with
-// fewer, all of them own the same rows, take every WS-th block of the
-// other side and are joined through LDS in wave order (WS = 4).
+// A workgroup owns a tile of rows of one sequence and one head.  Either its
+// waves own rows of their own (WS = 1), or all of them own the same rows, take
+// every WS-th block of the other side and are joined through LDS in order
+// (WS = 4).
+//
+// fp32 MFMAs and vector instructions do not overlap on a SIMD, so beside the
+// MFMAs' 32 cycles each the exponentials (16 cycles for a 16 x 4 block of
+// scores) and the few other instructions a score takes are what is left: at
+// 4096 rows, 16 heads of 64 the forward pass runs at 130 TFLOP/s, 85% of the
+// rate of a large fp32 product on this card, with the MFMAs busy 83% of the
+// time.
 
 #include <hip/hip_runtime.h>
 #include <stddef.h>
@@ -62,16 +69,15 @@ constexpr float kNoMax = -3.0e38f;
 
 struct Problem {
     const int *cu;
-    int nseq, tokens, hq, group, d, causal, window, tiles;
+    int nseq, tokens, hq, group, d, causal, window;
     float scale, c;  // c = scale log2(e): scores go through exp2
 };
 
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
-// Rows [row, end) of a head, at most N of them, as a buffer.
-template <int N>
+// Rows [row, end) of a head, at most 16 of them, as a buffer.
 __device__ __forceinline__ Rsrc rows_rsrc(const float *base, int64_t st, int row, int end, int d) {
-    const int n = min(end - row, N);
+    const int n = min(end - row, 16);
     const int bytes = n > 0 ? (int)(((n - 1) * st + d) * 4) : 0;
     return __builtin_amdgcn_make_buffer_rsrc((void *)(base + row * st), (short)0, bytes, 0x00020000);
 }
@@ -180,109 +186,155 @@ __device__ __forceinline__ f32x4 dots(const Rows<DP> &a, const Rows<DP> &b) {
     return s;
 }
 
-// Sum over the four lane groups (lanes of one m).
+// A value of the four lane groups (lanes of one m) combined in all of them.
+// Swapping a register's odd rows of 16 lanes with a copy's even rows, and its
+// upper half with a copy's lower half, leaves each lane's partner's value
+// beside its own, without a trip through LDS.
+template <class F>
+__device__ __forceinline__ float across_groups(float v, F f) {
+    unsigned u = __builtin_bit_cast(unsigned, v);
+    const auto a = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    v = f(__builtin_bit_cast(float, (unsigned)a[0]), __builtin_bit_cast(float, (unsigned)a[1]));
+    u = __builtin_bit_cast(unsigned, v);
+    const auto b = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    return f(__builtin_bit_cast(float, (unsigned)b[0]), __builtin_bit_cast(float, (unsigned)b[1]));
+}
 __device__ __forceinline__ float group_sum(float v) {
-    v += __shfl_xor(v, 16, 64);
-    return v + __shfl_xor(v, 32, 64);
+    return across_groups(v, [](float x, float y) { return x + y; });
 }
 __device__ __forceinline__ float group_max(float v) {
-    v = fmaxf(v, __shfl_xor(v, 16, 64));
-    return fmaxf(v, __shfl_xor(v, 32, 64));
+    return across_groups(v, [](float x, float y) { return fmaxf(x, y); });
 }
 
-// The sequence [s0, s1) and the first row of tile x of TILE rows, each
-// sequence cut into tiles by itself.  Sequence bounds are clamped to the
-// buffer.  Returns false when there is no such tile.  With `back`, a
-// sequence's tiles are taken from its end, where a causal row sees most.
+// Sum over the wave's lanes, the same in every lane: shifts within rows of 16
+// lanes, then broadcasts into the next rows.
+__device__ __forceinline__ int lanes_sum(int v) {
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, true);   // row_shr:1
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, true);   // row_shr:2
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, true);   // row_shr:4
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, true);   // row_shr:8
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);  // row_bcast:15 into rows 1 and 3
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);  // row_bcast:31 into rows 2 and 3
+    return __builtin_amdgcn_readlane(v, 63);
+}
+
+// What a workgroup finds in cu_seqlens for its x-th tile of TILE rows, each
+// sequence being cut into tiles by itself: the sequence [s0, s1) and the
+// tile's first row r0 (none when r0 < 0), and the rows [first, last) that
+// belong to sequences.  Bounds are clamped to the buffer.
+//
+// The tiles that take longest come first, over all sequences (of the next
+// 64): with `back` a sequence's last tile, whose causal rows see most keys,
+// else its first, whose keys the most rows see.  Tile n - 1 - l or l of a
+// sequence of n tiles has level l, work grows with the level, and S(l) = sum
+// over sequences of max(0, n - l) tiles have level l or more, so x's level is
+// the largest l with S(l) > x.  (Sequence by sequence, a long tile of the
+// last sequence starts when the chip is nearly done: dk and dv of 4 x 2048
+// rows, 2 heads of 128, took 910 us.)
+struct Tile {
+    int s0, s1, r0, first, last;
+};
 template <int TILE>
-__device__ __forceinline__ bool find_tile(const Problem &p, int x, bool back, int &s0, int &s1, int &r0) {
-    auto clamp = [&](int v) { return max(0, min(v, p.tokens)); };
-    int n = 0;
-    if (p.nseq <= 1) {
-        s0 = p.cu ? uniform(p.nseq ? clamp(p.cu[0]) : 0) : 0;
-        s1 = p.cu ? uniform(p.nseq ? max(s0, clamp(p.cu[1])) : 0) : p.tokens;
-        n = (s1 - s0 + TILE - 1) / TILE;
-        if (x >= n) return false;
+__device__ __forceinline__ Tile find_tile(const Problem &p, int x, bool back) {
+    Tile t = {0, p.tokens, -1, 0, p.tokens};
+    int n = 0, level = 0;
+    if (p.nseq == 1) {
+        if (p.cu) {
+            t.first = t.s0 = min(max(uniform(p.cu[0]), 0), p.tokens);
+            t.last = t.s1 = max(t.s0, min(uniform(p.cu[1]), p.tokens));
+        }
+        n = (t.s1 - t.s0 + TILE - 1) / TILE;
+        if (x >= n) return t;
+        level = n - 1 - x;
     } else {
         const int lane = threadIdx.x & 63;
-        int b = 0;
-        for (;; b += 64) {
-            if (b >= p.nseq) return false;
-            const bool in = b + lane < p.nseq;
-            const int lo = in ? clamp(p.cu[b + lane]) : 0;
-            const int hi = in ? max(lo, clamp(p.cu[b + lane + 1])) : 0;
+        const int c0 = p.cu[0], c1 = p.cu[p.nseq];
+        bool found = false;
+        for (int b = 0; b < p.nseq; b += 64) {
+            const int c = p.cu[min(b + lane, p.nseq)], d = p.cu[min(b + lane + 1, p.nseq)];
+            const int lo = min(max(c, 0), p.tokens), hi = max(lo, min(d, p.tokens));
             const int mine = (hi - lo + TILE - 1) / TILE;
-            int upto = mine;  // tiles of the sequences up to this lane's
-#pragma unroll
-            for (int o = 1; o < 64; o <<= 1) {
-                const int v = __shfl_up(upto, o, 64);
-                if (lane >= o) upto += v;
+            const int total = lanes_sum(mine);
+            if (x >= total) {
+                x -= total;
+                continue;
             }
-            const uint64_t past = __ballot(upto > x);
-            if (past) {
-                const int at = __builtin_ctzll(past);
-                s0 = __builtin_amdgcn_readlane(lo, at);
-                s1 = __builtin_amdgcn_readlane(hi, at);
-                n = __builtin_amdgcn_readlane(mine, at);
-                x -= __builtin_amdgcn_readlane(upto, at) - n;
-                break;
+            for (int bit = 1 << (31 - __builtin_clz(total)); bit > 0; bit >>= 1) {
+                if (!__any(mine > level + bit)) continue;
+                const int more = lanes_sum(max(0, mine - (level + bit)));
+                if (more > x) level += bit;
             }
-            x -= __builtin_amdgcn_readlane(upto, 63);
+            const int above = lanes_sum(max(0, mine - (level + 1)));  // tiles of higher levels
+            const uint64_t has = __ballot(mine > level);
+            const int rank = __builtin_amdgcn_mbcnt_hi((unsigned)(has >> 32), __builtin_amdgcn_mbcnt_lo((unsigned)has, 0));
+            const int at = __builtin_ctzll(__ballot(mine > level && rank == x - above));
+            t.s0 = __builtin_amdgcn_readlane(lo, at);
+            t.s1 = __builtin_amdgcn_readlane(hi, at);
+            n = __builtin_amdgcn_readlane(mine, at);
+            found = true;
+            break;
         }
+        t.first = min(max(uniform(c0), 0), p.tokens);
+        t.last = max(t.first, min(uniform(c1), p.tokens));
+        if (!found) return t;
     }
-    r0 = s0 + (back ? n - 1 - x : x) * TILE;
-    return true;
+    t.r0 = t.s0 + (back ? level : n - 1 - level) * TILE;
+    return t;
 }
 
-// Workgroups reach the 8 XCDs in turn; renumbered so that each XCD, with its
-// own L2, gets neighbouring tiles of neighbouring heads.
-__device__ __forceinline__ int xcd_order(int id, int total) {
-    const int xcd = id & 7, per = total >> 3, rest = total & 7;
-    return xcd * per + min(xcd, rest) + (id >> 3);
+// The head and tile of a workgroup.  Tiles come head by head, the longest
+// tiles of every head first, so that what is left at the end is short.
+// Workgroups reach the 8 XCDs, each with its own L2, in turn; the heads of a
+// step are ordered by the key/value head they read, so that with 4 or 8 of
+// those (or a multiple) an XCD meets the same one or two throughout.
+__device__ __forceinline__ void head_and_tile(int heads, int group, int &h, int &x) {
+    x = blockIdx.x / heads;
+    const int slot = blockIdx.x - x * heads, shared = heads / group;
+    const int turn = slot / shared;
+    h = (slot - turn * shared) * group + turn;
 }
 
-// Zeroes this workgroup's share of the rows that belong to no sequence: rows
-// [x TILE, x TILE + TILE) in front of the first sequence or behind the last.
+// Calls f for this workgroup's share of the rows that belong to no sequence:
+// rows [x TILE, x TILE + TILE) in front of the first sequence or behind the last.
 template <int TILE, class F>
-__device__ __forceinline__ void outside_rows(const Problem &p, int x, F f) {
-    if (!p.cu) return;
-    const int first = uniform(max(0, min(p.cu[0], p.tokens)));
-    const int last = uniform(max(first, min(p.cu[p.nseq], p.tokens)));
+__device__ __forceinline__ void outside_rows(const Problem &p, const Tile &t, int x, F f) {
     const int64_t a = (int64_t)x * TILE;
     if (a >= p.tokens) return;
     const int b = (int)min(a + TILE, (int64_t)p.tokens);
-    if (a >= first && b <= last) return;
+    if (a >= t.first && b <= t.last) return;
     for (int r = (int)a + (int)(threadIdx.x >> 6); r < b; r += blockDim.x >> 6)
-        if (r < first || r >= last) f(r);
+        if (r < t.first || r >= t.last) f(r);
 }
 __device__ __forceinline__ void zero_row(float *row, int d) {
     for (int i = threadIdx.x & 63; i < d; i += 64) row[i] = 0.0f;
 }
 
-// Which keys a block of rows may see.
+// The keys that rows [r, r + n) of a sequence may see, and the rows that may
+// see keys [k, k + n): ranges inside the sequence.
 struct Range {
     int lo, hi;
 };
-__device__ __forceinline__ Range keys_of(const Problem &p, int s0, int s1, int r0, int n) {
-    const int last = min(r0 + n, s1) - 1;
+__device__ __forceinline__ Range keys_of(const Problem &p, int s0, int s1, int r, int n) {
+    const int last = min(r + n, s1) - 1;
     Range k = {s0, s1};
-    if (p.window) k.lo = max(s0, r0 - p.window + 1);
+    if (p.window) {
+        k.lo = max(s0, r - p.window + 1);
+        if (s1 - last > p.window) k.hi = last + p.window;
+    }
     if (p.causal) k.hi = last + 1;
-    else if (p.window) k.hi = (int)min((int64_t)s1, (int64_t)last + p.window);
     return k;
 }
-// Which rows may see a block of keys.
-__device__ __forceinline__ Range rows_of(const Problem &p, int s0, int s1, int k0, int n) {
-    const int last = min(k0 + n, s1) - 1;
+__device__ __forceinline__ Range rows_of(const Problem &p, int s0, int s1, int k, int n) {
+    const int last = min(k + n, s1) - 1;
     Range r = {s0, s1};
-    if (p.causal) r.lo = k0;
-    else if (p.window) r.lo = max(s0, k0 - p.window + 1);
-    if (p.window) r.hi = (int)min((int64_t)s1, (int64_t)last + p.window);
+    if (p.window) {
+        r.lo = max(s0, k - p.window + 1);
+        if (s1 - last > p.window) r.hi = last + p.window;
+    }
+    if (p.causal) r.lo = k;
     return r;
 }
-__device__ __forceinline__ bool sees(const Problem &p, int i, int j) {
-    return (!p.causal || j <= i) && (!p.window || (i - j < p.window && j - i < p.window));
-}
+__device__ __forceinline__ bool inside(Range r, int x) { return (unsigned)(x - r.lo) < (unsigned)(r.hi - r.lo); }
 // Whether rows [r, r + n) of the sequence all see keys [k, k + m), both whole inside it.
 __device__ __forceinline__ bool all_see(const Problem &p, int s1, int r, int n, int k, int m) {
     if (r + n > s1 || k + m > s1) return false;
@@ -298,20 +350,21 @@ __device__ __forceinline__ bool all_see(const Problem &p, int s1, int r, int n, 
 // without loss, and most blocks need neither the maximum across lanes nor
 // the rescaling.
 template <int DP, bool EX, int RB, int WS>
-__global__ __launch_bounds__(256, 2) void attention_fwd(Problem p, Strided q, Strided k, Strided v, Strided o,
+__global__ __launch_bounds__(256, DP <= 64 ? 4 : 2) void attention_fwd(Problem p, Strided q, Strided k, Strided v, Strided o,
                                                         float *lse) {
-    constexpr int WROWS = 16 * RB, TILE = WS == 1 ? 4 * WROWS : WROWS;
+    constexpr int WROWS = 16 * RB, WR = 4 / WS, TILE = WR * WROWS;
     const int lane = threadIdx.x & 63, g = lane >> 4, m = lane & 15;
     const int wave = uniform(threadIdx.x >> 6);
-    const int id = xcd_order(blockIdx.x, gridDim.x);
-    const int h = id / p.tiles, x = id - h * p.tiles;
-    outside_rows<TILE>(p, x, [&](int r) {
+    int h, x;
+    head_and_tile(p.hq, p.group, h, x);
+    const Tile t = find_tile<TILE>(p, x, p.causal);
+    outside_rows<TILE>(p, t, x, [&](int r) {
         zero_row(o.p + r * o.st + h * o.sh, p.d);
         if (lane == 0) lse[(int64_t)h * p.tokens + r] = -INFINITY;
     });
-    int s0, s1, t0;
-    if (!find_tile<TILE>(p, x, p.causal, s0, s1, t0)) return;
-    const int r0 = t0 + (WS == 1 ? wave * WROWS : 0);
+    if (t.r0 < 0) return;
+    const int s0 = t.s0, s1 = t.s1;
+    const int part_of = wave / WR, r0 = t.r0 + wave % WR * WROWS;
     if (WS == 1 && r0 >= s1) return;
     const float *kp = k.p + (h / p.group) * k.sh, *vp = v.p + (h / p.group) * v.sh;
 
@@ -320,32 +373,35 @@ __global__ __launch_bounds__(256, 2) void attention_fwd(Problem p, Strided q, St
     float top[RB], sum[RB];
 #pragma unroll
     for (int b = 0; b < RB; ++b) {
-        Q[b].template load<EX>(rows_rsrc<16>(q.p + h * q.sh, q.st, r0 + 16 * b, s1, p.d), q.st, p.d);
+        Q[b].template load<EX>(rows_rsrc(q.p + h * q.sh, q.st, r0 + 16 * b, s1, p.d), q.st, p.d);
         O[b].clear();
         top[b] = kNoMax;
         sum[b] = 0.0f;
     }
     const Range kr = keys_of(p, s0, s1, r0, WROWS);
-    const int step = WS == 1 ? 16 : 16 * WS;
-    int kb = kr.lo + (WS == 1 ? 0 : 16 * wave);
+    const int step = 16 * WS;
+    int kb = kr.lo + 16 * part_of;
+    // The values of a block are asked for when its scores begin, the keys of
+    // the next one when they are done, so each load has a product to arrive under.
     Rows<DP> K;
     Cols<DP> V;
-    K.template load<EX>(rows_rsrc<16>(kp, k.st, kb, s1, p.d), k.st, p.d);
-    V.template load<EX>(rows_rsrc<16>(vp, v.st, kb, s1, p.d), v.st, p.d);
+    K.template load<EX>(rows_rsrc(kp, k.st, kb, s1, p.d), k.st, p.d);
     for (; kb < kr.hi; kb += step) {
         f32x4 s[RB];
+        V.template load<EX>(rows_rsrc(vp, v.st, kb, s1, p.d), v.st, p.d);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int b = 0; b < RB; ++b) s[b] = dots<DP>(K, Q[b]);
-        K.template load<EX>(rows_rsrc<16>(kp, k.st, kb + step, s1, p.d), k.st, p.d);
+        __builtin_amdgcn_sched_barrier(0);
+        K.template load<EX>(rows_rsrc(kp, k.st, kb + step, s1, p.d), k.st, p.d);
         __builtin_amdgcn_sched_barrier(0);
         if (!all_see(p, s1, r0, WROWS, kb, 16)) {
 #pragma unroll
-            for (int b = 0; b < RB; ++b)
+            for (int b = 0; b < RB; ++b) {
+                const Range seen = keys_of(p, s0, s1, r0 + 16 * b + m, 1);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int key = kb + 4 * g + i;
-                    if (key >= s1 || !sees(p, r0 + 16 * b + m, key)) s[b][i] = -INFINITY;
-                }
+                for (int i = 0; i < 4; ++i) s[b][i] = inside(seen, kb + 4 * g + i) ? s[b][i] : -INFINITY;
+            }
         }
 #pragma unroll
         for (int b = 0; b < RB; ++b) {
@@ -364,8 +420,6 @@ __global__ __launch_bounds__(256, 2) void attention_fwd(Problem p, Strided q, St
             }
             O[b].add(V, s[b]);
         }
-        V.template load<EX>(rows_rsrc<16>(vp, v.st, kb + step, s1, p.d), v.st, p.d);
-        __builtin_amdgcn_sched_barrier(0);
     }
 #pragma unroll
     for (int b = 0; b < RB; ++b) sum[b] = group_sum(sum[b]);
@@ -375,7 +429,7 @@ __global__ __launch_bounds__(256, 2) void attention_fwd(Problem p, Strided q, St
         for (int b = 0; b < RB; ++b) {
             const int r = r0 + 16 * b;
             if (r >= s1) break;
-            const Rsrc ro = rows_rsrc<16>(o.p + h * o.sh, o.st, r, s1, p.d);
+            const Rsrc ro = rows_rsrc(o.p + h * o.sh, o.st, r, s1, p.d);
             const float inv = 1.0f / sum[b];
             O[b].each4([&](int d0, f32x4 y) {
                 store4(ro, (EX || d0 < p.d) ? m * (int)o.st * 4 + d0 * 4 : kOOB, y * inv);
@@ -384,56 +438,90 @@ __global__ __launch_bounds__(256, 2) void attention_fwd(Problem p, Strided q, St
                 lse[(int64_t)h * p.tokens + r + m] = (top[b] + __builtin_amdgcn_logf(sum[b])) * kLn2;
         }
     } else {
-        // join the waves, in wave order
-        static_assert(RB == 1 || WS == 1, "joined waves hold 16 rows");
+        // join the waves of the same rows, in order, 16 rows at a time
         constexpr int LD = DP + 4;
-        __shared__ __align__(16) float part[WS == 1 ? 1 : WS][WS == 1 ? 1 : 16 * LD];
-        __shared__ float ptop[WS][16], psum[WS][16];
-        O[0].each4([&](int d0, f32x4 y) { *(f32x4 *)&part[wave][m * LD + d0] = y; });
-        if (g == 0) {
-            ptop[wave][m] = top[0];
-            psum[wave][m] = sum[0];
-        }
-        __syncthreads();
-        const int row = threadIdx.x >> 4, e = threadIdx.x & 15;
-        if (r0 + row >= s1) return;
-        float to = ptop[0][row], total = 0.0f, f[WS];
+        __shared__ __align__(16) float part[WS == 1 ? 1 : 4][WS == 1 ? 1 : 16 * LD];
+        __shared__ float ptop[4][16], psum[4][16];
+        const int mine = wave % WR, e = threadIdx.x & 15;
 #pragma unroll
-        for (int w = 1; w < WS; ++w) to = fmaxf(to, ptop[w][row]);
+        for (int b = 0; b < RB; ++b) {
+            if (b > 0) __syncthreads();
+            O[b].each4([&](int d0, f32x4 y) { *(f32x4 *)&part[wave][m * LD + d0] = y; });
+            if (g == 0) {
+                ptop[wave][m] = top[b];
+                psum[wave][m] = sum[b];
+            }
+            __syncthreads();
+            for (int row = part_of * 4 + g; row < 16; row += 4 * WS) {
+                const int r = r0 + 16 * b + row;
+                if (r >= s1) continue;
+                float to = ptop[mine][row], total = 0.0f, f[WS];
 #pragma unroll
-        for (int w = 0; w < WS; ++w) {
-            f[w] = __builtin_amdgcn_exp2f(ptop[w][row] - to);
-            total += f[w] * psum[w][row];
+                for (int w = 1; w < WS; ++w) to = fmaxf(to, ptop[w * WR + mine][row]);
+#pragma unroll
+                for (int w = 0; w < WS; ++w) {
+                    f[w] = __builtin_amdgcn_exp2f(ptop[w * WR + mine][row] - to);
+                    total += f[w] * psum[w * WR + mine][row];
+                }
+                const float inv = 1.0f / total;
+                float *dst = o.p + (int64_t)r * o.st + h * o.sh;
+#pragma unroll
+                for (int c = 0; c < (DP + 63) / 64; ++c) {
+                    const int d0 = 64 * c + 4 * e;
+                    if (d0 < p.d) {
+                        f32x4 y = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                        for (int w = 0; w < WS; ++w) y += f[w] * *(const f32x4 *)&part[w * WR + mine][row * LD + d0];
+                        *(f32x4 *)(dst + d0) = y * inv;
+                    }
+                }
+                if (e == 0) lse[(int64_t)h * p.tokens + r] = (to + __builtin_amdgcn_logf(total)) * kLn2;
+            }
         }
-        const float inv = 1.0f / total;
-        float *dst = o.p + (int64_t)(r0 + row) * o.st + h * o.sh;
+    }
+}
+
+// Adds the results of 16 rows of the WS waves that share them, in order,
+// times f, into rows [r, s1) of a head.  `part` holds 4 x 16 x (DP + 4) floats.
+template <int DP, int WS>
+__device__ __forceinline__ void join_rows(const Acc<DP> &acc, float *part, const Strided &to, int h, int r, int s1,
+                                          int d, float f) {
+    constexpr int LD = DP + 4, WR = 4 / WS;
+    const int wave = threadIdx.x >> 6, g = (threadIdx.x & 63) >> 4, m = threadIdx.x & 15;
+    __syncthreads();  // the buffer's last readers
+    acc.each4([&](int d0, f32x4 y) { *(f32x4 *)&part[(wave * 16 + m) * LD + d0] = y; });
+    __syncthreads();
+    const int mine = wave % WR, e = threadIdx.x & 15;
+    for (int row = wave / WR * 4 + g; row < 16; row += 4 * WS) {
+        if (r + row >= s1) continue;
+        float *dst = to.p + (int64_t)(r + row) * to.st + h * to.sh;
 #pragma unroll
         for (int c = 0; c < (DP + 63) / 64; ++c) {
             const int d0 = 64 * c + 4 * e;
-            if (d0 < p.d) {
-                f32x4 y = {0.0f, 0.0f, 0.0f, 0.0f};
+            if (d0 < d) {
+                f32x4 y = *(const f32x4 *)&part[(mine * 16 + row) * LD + d0];
 #pragma unroll
-                for (int w = 0; w < WS; ++w) y += f[w] * *(const f32x4 *)&part[w][row * LD + d0];
-                *(f32x4 *)(dst + d0) = y * inv;
+                for (int w = 1; w < WS; ++w) y += *(const f32x4 *)&part[((w * WR + mine) * 16 + row) * LD + d0];
+                *(f32x4 *)(dst + d0) = y * f;
             }
         }
-        if (e == 0) lse[(int64_t)h * p.tokens + r0 + row] = (to + __builtin_amdgcn_logf(total)) * kLn2;
     }
 }
 
 // --- backward: dq, and delta for the other kernel ---
 template <int DP, bool EX, int RB, int WS>
-__global__ __launch_bounds__(256, 2) void attention_bwd_dq(Problem p, Strided dout, Strided q, Strided k, Strided v,
+__global__ __launch_bounds__(256, DP >= 96 && RB == 2 ? 1 : 2) void attention_bwd_dq(Problem p, Strided dout, Strided q, Strided k, Strided v,
                                                            Strided o, const float *lse, float *delta, Strided dq) {
-    constexpr int WROWS = 16 * RB, TILE = WS == 1 ? 4 * WROWS : WROWS;
+    constexpr int WROWS = 16 * RB, WR = 4 / WS, TILE = WR * WROWS;
     const int lane = threadIdx.x & 63, g = lane >> 4, m = lane & 15;
     const int wave = uniform(threadIdx.x >> 6);
-    const int id = xcd_order(blockIdx.x, gridDim.x);
-    const int h = id / p.tiles, x = id - h * p.tiles;
-    outside_rows<TILE>(p, x, [&](int r) { zero_row(dq.p + r * dq.st + h * dq.sh, p.d); });
-    int s0, s1, t0;
-    if (!find_tile<TILE>(p, x, p.causal, s0, s1, t0)) return;
-    const int r0 = t0 + (WS == 1 ? wave * WROWS : 0);
+    int h, x;
+    head_and_tile(p.hq, p.group, h, x);
+    const Tile t = find_tile<TILE>(p, x, p.causal);
+    outside_rows<TILE>(p, t, x, [&](int r) { zero_row(dq.p + r * dq.st + h * dq.sh, p.d); });
+    if (t.r0 < 0) return;
+    const int s0 = t.s0, s1 = t.s1, t0 = t.r0;
+    const int part_of = wave / WR, r0 = t0 + wave % WR * WROWS;
     if (WS == 1 && r0 >= s1) return;
     const float *kp = k.p + (h / p.group) * k.sh, *vp = v.p + (h / p.group) * v.sh;
 
@@ -443,36 +531,36 @@ __global__ __launch_bounds__(256, 2) void attention_bwd_dq(Problem p, Strided do
 #pragma unroll
     for (int b = 0; b < RB; ++b) {
         const int r = r0 + 16 * b;
-        Q[b].template load<EX>(rows_rsrc<16>(q.p + h * q.sh, q.st, r, s1, p.d), q.st, p.d);
-        G[b].template load<EX>(rows_rsrc<16>(dout.p + h * dout.sh, dout.st, r, s1, p.d), dout.st, p.d);
+        Q[b].template load<EX>(rows_rsrc(q.p + h * q.sh, q.st, r, s1, p.d), q.st, p.d);
+        G[b].template load<EX>(rows_rsrc(dout.p + h * dout.sh, dout.st, r, s1, p.d), dout.st, p.d);
         Rows<DP> out;
-        out.template load<EX>(rows_rsrc<16>(o.p + h * o.sh, o.st, r, s1, p.d), o.st, p.d);
+        out.template load<EX>(rows_rsrc(o.p + h * o.sh, o.st, r, s1, p.d), o.st, p.d);
         f32x4 dot = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int j = 0; j < DP / 16; ++j) dot += G[b].x[j] * out.x[j];
         del[b] = group_sum((dot[0] + dot[1]) + (dot[2] + dot[3]));
         const int64_t at = (int64_t)h * p.tokens + r + m;
         l2[b] = r + m < s1 ? lse[at] * kLog2e : 0.0f;
-        if (g == 0 && r + m < s1 && (WS == 1 || wave == 0)) delta[at] = del[b];
+        if (g == 0 && r + m < s1 && part_of == 0) delta[at] = del[b];
         A[b].clear();
     }
     const Range kr = keys_of(p, s0, s1, r0, WROWS);
-    const int step = WS == 1 ? 16 : 16 * WS;
-    int kb = kr.lo + (WS == 1 ? 0 : 16 * wave);
+    const int step = 16 * WS;
+    int kb = kr.lo + 16 * part_of;
     Rows<DP> K, V;
     Cols<DP> T;
-    K.template load<EX>(rows_rsrc<16>(kp, k.st, kb, s1, p.d), k.st, p.d);
-    V.template load<EX>(rows_rsrc<16>(vp, v.st, kb, s1, p.d), v.st, p.d);
-    T.template load<EX>(rows_rsrc<16>(kp, k.st, kb, s1, p.d), k.st, p.d);
+    K.template load<EX>(rows_rsrc(kp, k.st, kb, s1, p.d), k.st, p.d);
+    V.template load<EX>(rows_rsrc(vp, v.st, kb, s1, p.d), v.st, p.d);
+    T.template load<EX>(rows_rsrc(kp, k.st, kb, s1, p.d), k.st, p.d);
     for (; kb < kr.hi; kb += step) {
         f32x4 s[RB], dp[RB];
 #pragma unroll
         for (int b = 0; b < RB; ++b) s[b] = dots<DP>(K, Q[b]);
-        K.template load<EX>(rows_rsrc<16>(kp, k.st, kb + step, s1, p.d), k.st, p.d);
+        K.template load<EX>(rows_rsrc(kp, k.st, kb + step, s1, p.d), k.st, p.d);
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int b = 0; b < RB; ++b) dp[b] = dots<DP>(V, G[b]);
-        V.template load<EX>(rows_rsrc<16>(vp, v.st, kb + step, s1, p.d), v.st, p.d);
+        V.template load<EX>(rows_rsrc(vp, v.st, kb + step, s1, p.d), v.st, p.d);
         __builtin_amdgcn_sched_barrier(0);
         const bool whole = all_see(p, s1, r0, WROWS, kb, 16);
 #pragma unroll
@@ -481,15 +569,13 @@ __global__ __launch_bounds__(256, 2) void attention_bwd_dq(Problem p, Strided do
             for (int i = 0; i < 4; ++i)
                 s[b][i] = __builtin_amdgcn_exp2f(fmaf(s[b][i], p.c, -l2[b])) * (dp[b][i] - del[b]);
             if (!whole) {
+                const Range seen = keys_of(p, s0, s1, r0 + 16 * b + m, 1);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int key = kb + 4 * g + i;
-                    if (key >= s1 || !sees(p, r0 + 16 * b + m, key)) s[b][i] = 0.0f;
-                }
+                for (int i = 0; i < 4; ++i) s[b][i] = inside(seen, kb + 4 * g + i) ? s[b][i] : 0.0f;
             }
             A[b].add(T, s[b]);
         }
-        T.template load<EX>(rows_rsrc<16>(kp, k.st, kb + step, s1, p.d), k.st, p.d);
+        T.template load<EX>(rows_rsrc(kp, k.st, kb + step, s1, p.d), k.st, p.d);
         __builtin_amdgcn_sched_barrier(0);
     }
 
@@ -498,72 +584,60 @@ __global__ __launch_bounds__(256, 2) void attention_bwd_dq(Problem p, Strided do
         for (int b = 0; b < RB; ++b) {
             const int r = r0 + 16 * b;
             if (r >= s1) break;
-            const Rsrc ro = rows_rsrc<16>(dq.p + h * dq.sh, dq.st, r, s1, p.d);
+            const Rsrc ro = rows_rsrc(dq.p + h * dq.sh, dq.st, r, s1, p.d);
             A[b].each4([&](int d0, f32x4 y) {
                 store4(ro, (EX || d0 < p.d) ? m * (int)dq.st * 4 + d0 * 4 : kOOB, y * p.scale);
             });
         }
     } else {
-        static_assert(RB == 1 || WS == 1, "joined waves hold 16 rows");
-        constexpr int LD = DP + 4;
-        __shared__ __align__(16) float part[WS == 1 ? 1 : WS][WS == 1 ? 1 : 16 * LD];
-        A[0].each4([&](int d0, f32x4 y) { *(f32x4 *)&part[wave][m * LD + d0] = y; });
-        __syncthreads();
-        const int row = threadIdx.x >> 4, e = threadIdx.x & 15;
-        if (r0 + row >= s1) return;
-        float *dst = dq.p + (int64_t)(r0 + row) * dq.st + h * dq.sh;
+        __shared__ __align__(16) float part[WS == 1 ? 1 : 4 * 16 * (DP + 4)];
 #pragma unroll
-        for (int c = 0; c < (DP + 63) / 64; ++c) {
-            const int d0 = 64 * c + 4 * e;
-            if (d0 < p.d) {
-                f32x4 y = *(const f32x4 *)&part[0][row * LD + d0];
-#pragma unroll
-                for (int w = 1; w < WS; ++w) y += *(const f32x4 *)&part[w][row * LD + d0];
-                *(f32x4 *)(dst + d0) = y * p.scale;
-            }
-        }
+        for (int b = 0; b < RB; ++b) join_rows<DP, WS>(A[b], part, dq, h, r0 + 16 * b, s1, p.d, p.scale);
     }
 }
 
 // --- backward: dk and dv ---
 //
 // The keys are held fixed and the blocks of 16 rows of every query head of
-// the group are walked over, in the order of the heads.
+// the group are walked over.
 template <int DP, bool EX, int RB, int WS>
-__global__ __launch_bounds__(256, 2) void attention_bwd_dkv(Problem p, Strided dout, Strided q, Strided k, Strided v,
+__global__ __launch_bounds__(256, DP >= 96 && RB == 2 ? 1 : 2) void attention_bwd_dkv(Problem p, Strided dout, Strided q, Strided k, Strided v,
                                                             const float *lse, const float *delta, Strided dk,
                                                             Strided dv) {
-    constexpr int WROWS = 16 * RB, TILE = WS == 1 ? 4 * WROWS : WROWS;
+    constexpr int WROWS = 16 * RB, WR = 4 / WS, TILE = WR * WROWS;
     const int lane = threadIdx.x & 63, g = lane >> 4, m = lane & 15;
     const int wave = uniform(threadIdx.x >> 6);
-    const int id = xcd_order(blockIdx.x, gridDim.x);
-    const int h = id / p.tiles, x = id - h * p.tiles;
-    outside_rows<TILE>(p, x, [&](int r) {
+    int h, x;
+    head_and_tile(p.hq / p.group, 1, h, x);
+    const Tile t = find_tile<TILE>(p, x, false);
+    outside_rows<TILE>(p, t, x, [&](int r) {
         zero_row(dk.p + r * dk.st + h * dk.sh, p.d);
         zero_row(dv.p + r * dv.st + h * dv.sh, p.d);
     });
-    int s0, s1, t0;
-    if (!find_tile<TILE>(p, x, false, s0, s1, t0)) return;
-    const int k0 = t0 + (WS == 1 ? wave * WROWS : 0);
+    if (t.r0 < 0) return;
+    const int s0 = t.s0, s1 = t.s1, t0 = t.r0;
+    const int part_of = wave / WR, k0 = t0 + wave % WR * WROWS;
     if (WS == 1 && k0 >= s1) return;
 
     Rows<DP> K[RB], V[RB];
     Acc<DP> DK[RB], DV[RB];
 #pragma unroll
     for (int b = 0; b < RB; ++b) {
-        K[b].template load<EX>(rows_rsrc<16>(k.p + h * k.sh, k.st, k0 + 16 * b, s1, p.d), k.st, p.d);
-        V[b].template load<EX>(rows_rsrc<16>(v.p + h * v.sh, v.st, k0 + 16 * b, s1, p.d), v.st, p.d);
+        K[b].template load<EX>(rows_rsrc(k.p + h * k.sh, k.st, k0 + 16 * b, s1, p.d), k.st, p.d);
+        V[b].template load<EX>(rows_rsrc(v.p + h * v.sh, v.st, k0 + 16 * b, s1, p.d), v.st, p.d);
         DK[b].clear();
         DV[b].clear();
     }
     const Range rr = rows_of(p, s0, s1, k0, WROWS);
     const int blocks = (rr.hi - rr.lo + 15) / 16, total = blocks * p.group;
-    // block n of the walk: head n / blocks of the group, rows from rr.lo + 16 (n % blocks)
-    int n = WS == 1 ? 0 : wave, qh = 0, qb = n;
-    const int step = WS == 1 ? 1 : WS;
-    while (blocks > 0 && qb >= blocks) {
-        qb -= blocks;
-        ++qh;
+    // Block n of the walk: head n % group of the group, and the n / group-th
+    // block of rows from the last one on.  Workgroups that start together then
+    // read the same rows of the same heads together, whatever their keys.
+    int n = part_of, qh = n, qb = 0;
+    const int step = WS;
+    while (qh >= p.group) {
+        qh -= p.group;
+        ++qb;
     }
     Rows<DP> Q, G;
     Cols<DP> QT, GT;
@@ -575,7 +649,7 @@ __global__ __launch_bounds__(256, 2) void attention_bwd_dkv(Problem p, Strided d
         const bool in = n < total;
         qp = q.p + head * q.sh;
         gp = dout.p + head * dout.sh;
-        r = in ? rr.lo + 16 * qb : s1;
+        r = in ? rr.lo + 16 * (blocks - 1 - qb) : s1;
     };
     auto stats = [&](const float *from) {
         const int left = r < s1 ? s1 - r : 0;
@@ -584,29 +658,28 @@ __global__ __launch_bounds__(256, 2) void attention_bwd_dkv(Problem p, Strided d
                      16 * g);
     };
     at();
-    Q.template load<EX>(rows_rsrc<16>(qp, q.st, r, s1, p.d), q.st, p.d);
-    G.template load<EX>(rows_rsrc<16>(gp, dout.st, r, s1, p.d), dout.st, p.d);
+    Q.template load<EX>(rows_rsrc(qp, q.st, r, s1, p.d), q.st, p.d);
+    G.template load<EX>(rows_rsrc(gp, dout.st, r, s1, p.d), dout.st, p.d);
     l4 = stats(lse);
     d4 = stats(delta);
-    GT.template load<EX>(rows_rsrc<16>(gp, dout.st, r, s1, p.d), dout.st, p.d);
-    QT.template load<EX>(rows_rsrc<16>(qp, q.st, r, s1, p.d), q.st, p.d);
     while (n < total) {
         const int row = r;
+        const float *qc = qp, *gc = gp;
         n += step;
-        qb += step;
-        while (qb >= blocks) {
-            qb -= blocks;
-            ++qh;
+        qh += step;
+        while (qh >= p.group) {
+            qh -= p.group;
+            ++qb;
         }
         at();
         f32x4 s[RB], dp[RB];
 #pragma unroll
         for (int b = 0; b < RB; ++b) s[b] = dots<DP>(Q, K[b]);
-        Q.template load<EX>(rows_rsrc<16>(qp, q.st, r, s1, p.d), q.st, p.d);
+        GT.template load<EX>(rows_rsrc(gc, dout.st, row, s1, p.d), dout.st, p.d);
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int b = 0; b < RB; ++b) dp[b] = dots<DP>(G, V[b]);
-        G.template load<EX>(rows_rsrc<16>(gp, dout.st, r, s1, p.d), dout.st, p.d);
+        QT.template load<EX>(rows_rsrc(qc, q.st, row, s1, p.d), q.st, p.d);
         __builtin_amdgcn_sched_barrier(0);
         const bool whole = all_see(p, s1, row, 16, k0, WROWS);
         const f32x4 l2 = l4 * kLog2e;
@@ -618,10 +691,12 @@ __global__ __launch_bounds__(256, 2) void attention_bwd_dkv(Problem p, Strided d
                 dp[b][i] = s[b][i] * (dp[b][i] - d4[i]);
             }
             if (!whole) {
+                const Range seen = rows_of(p, s0, s1, k0 + 16 * b + m, 1);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int qi = row + 4 * g + i;
-                    if (qi >= s1 || !sees(p, qi, k0 + 16 * b + m)) s[b][i] = dp[b][i] = 0.0f;
+                    const bool in = inside(seen, row + 4 * g + i);
+                    s[b][i] = in ? s[b][i] : 0.0f;
+                    dp[b][i] = in ? dp[b][i] : 0.0f;
                 }
             }
         }
@@ -629,11 +704,11 @@ __global__ __launch_bounds__(256, 2) void attention_bwd_dkv(Problem p, Strided d
         d4 = stats(delta);
 #pragma unroll
         for (int b = 0; b < RB; ++b) DV[b].add(GT, s[b]);
-        GT.template load<EX>(rows_rsrc<16>(gp, dout.st, r, s1, p.d), dout.st, p.d);
+        Q.template load<EX>(rows_rsrc(qp, q.st, r, s1, p.d), q.st, p.d);
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int b = 0; b < RB; ++b) DK[b].add(QT, dp[b]);
-        QT.template load<EX>(rows_rsrc<16>(qp, q.st, r, s1, p.d), q.st, p.d);
+        G.template load<EX>(rows_rsrc(gp, dout.st, r, s1, p.d), dout.st, p.d);
         __builtin_amdgcn_sched_barrier(0);
     }
 
@@ -642,8 +717,8 @@ __global__ __launch_bounds__(256, 2) void attention_bwd_dkv(Problem p, Strided d
         for (int b = 0; b < RB; ++b) {
             const int r1 = k0 + 16 * b;
             if (r1 >= s1) break;
-            const Rsrc rk = rows_rsrc<16>(dk.p + h * dk.sh, dk.st, r1, s1, p.d);
-            const Rsrc rv = rows_rsrc<16>(dv.p + h * dv.sh, dv.st, r1, s1, p.d);
+            const Rsrc rk = rows_rsrc(dk.p + h * dk.sh, dk.st, r1, s1, p.d);
+            const Rsrc rv = rows_rsrc(dv.p + h * dv.sh, dv.st, r1, s1, p.d);
             DK[b].each4([&](int d0, f32x4 y) {
                 store4(rk, (EX || d0 < p.d) ? m * (int)dk.st * 4 + d0 * 4 : kOOB, y * p.scale);
             });
@@ -652,28 +727,12 @@ __global__ __launch_bounds__(256, 2) void attention_bwd_dkv(Problem p, Strided d
             });
         }
     } else {
-        static_assert(RB == 1 || WS == 1, "joined waves hold 16 keys");
-        constexpr int LD = DP + 4;
-        __shared__ __align__(16) float part[2][WS == 1 ? 1 : WS][WS == 1 ? 1 : 16 * LD];
-        DK[0].each4([&](int d0, f32x4 y) { *(f32x4 *)&part[0][wave][m * LD + d0] = y; });
-        DV[0].each4([&](int d0, f32x4 y) { *(f32x4 *)&part[1][wave][m * LD + d0] = y; });
-        __syncthreads();
-        const int row = threadIdx.x >> 4, e = threadIdx.x & 15;
-        if (k0 + row >= s1) return;
-        float *dst[2] = {dk.p + (int64_t)(k0 + row) * dk.st + h * dk.sh, dv.p + (int64_t)(k0 + row) * dv.st + h * dv.sh};
-        const float f[2] = {p.scale, 1.0f};
+        __shared__ __align__(16) float part[WS == 1 ? 1 : 4 * 16 * (DP + 4)];
 #pragma unroll
-        for (int a = 0; a < 2; ++a)
-#pragma unroll
-            for (int c = 0; c < (DP + 63) / 64; ++c) {
-                const int d0 = 64 * c + 4 * e;
-                if (d0 < p.d) {
-                    f32x4 y = *(const f32x4 *)&part[a][0][row * LD + d0];
-#pragma unroll
-                    for (int w = 1; w < WS; ++w) y += *(const f32x4 *)&part[a][w][row * LD + d0];
-                    *(f32x4 *)(dst[a] + d0) = y * f[a];
-                }
-            }
+        for (int b = 0; b < RB; ++b) {
+            join_rows<DP, WS>(DK[b], part, dk, h, k0 + 16 * b, s1, p.d, p.scale);
+            join_rows<DP, WS>(DV[b], part, dv, h, k0 + 16 * b, s1, p.d, 1.0f);
+        }
     }
 }
 
@@ -716,7 +775,6 @@ Problem device_problem(const attn_problem &a) {
     p.window = a.window < a.tokens ? (int)a.window : 0;  // a wider window hides nothing
     p.scale = (float)a.scale;
     p.c = (float)(a.scale * 1.44269504088896340736);
-    p.tiles = 0;
     return p;
 }
 
@@ -726,9 +784,34 @@ int64_t tiles_of(const attn_problem &p, int64_t tile) {
     return p.cu_seqlens ? std::max(whole, p.tokens / tile + p.num_seqs) : whole;
 }
 
-// Waves that own 64 rows a workgroup when that gives every CU two workgroups,
-// else joined waves on 16.
-bool joined(const attn_problem &p, int64_t heads) { return (p.tokens / 64) * heads < 512; }
+// How a kernel's rows (or keys) are dealt out: RB blocks of 16 a wave, WS
+// waves of a workgroup to the same rows.  A second block a wave halves the
+// loads of the other side for each product; joined waves (WS = 4) make the
+// tiles short, so that the chip is full and evenly loaded, at the price of
+// the joining.  Measured over 1 to 64 sequences of 128 to 8192 rows, 8 to 16
+// heads of 32 to 128, causal and not:
+//  * few rows: one block a wave, joined (512 rows, 12 heads of 64: forward
+//    12.8 us against 13.7 with two blocks and 39.8 unjoined; backward 36, 42
+//    and 127 us);
+//  * many rows: two blocks, joined (2 x 4096 rows: forward 403 us against 455
+//    with one block and 506 unjoined; backward 1380, 1760 and 1500 us);
+//  * many short sequences: two blocks, each wave its own rows (64 x 128 rows:
+//    forward 26 us against 38 joined; backward 104 against 164; 16 x 512 rows:
+//    backward 232 against 266).
+// `most` is the sequence length that still counts as short.  The host knows
+// the average length only; the limits are where both are close.
+struct Plan {
+    int rb, ws;
+    int64_t rows() const { return 16 * rb * (4 / ws); }
+};
+Plan plan(const attn_problem &p, int64_t heads, int64_t many, int64_t most) {
+    int64_t length = p.cu_seqlens ? p.tokens / std::max<int64_t>(1, p.num_seqs) : p.tokens;
+    if (p.window > 0) length = std::min(length, p.window);
+    if (length <= most && p.tokens / 128 * heads >= 512) return {2, 1};
+    return {p.tokens / 32 * heads >= many ? 2 : 1, 4};
+}
+Plan plan_forward(const attn_problem &p) { return plan(p, p.q_heads, 1024, 256); }
+Plan plan_backward(const attn_problem &p, int64_t heads) { return plan(p, heads, 512, 512); }
 
 #define ATTN_BY_DIM(LAUNCH)                                                     \
     do {                                                                        \
@@ -767,25 +850,25 @@ int attn_forward(const attn_forward_args *args, void *stream) {
         in_range(k, a.lse, lse_bytes, T, D) || in_range(v, a.lse, lse_bytes, T, D) ||
         in_range(o, a.p.cu_seqlens, cu_bytes, T, D))
         return GEMM_ERR_ALIAS;
-    Problem p = device_problem(a.p);
-    const bool join = joined(a.p, a.p.q_heads);
-    p.tiles = (int)tiles_of(a.p, join ? 16 : 64);
-    const int64_t grid = (int64_t)p.tiles * a.p.q_heads;
+    const Problem p = device_problem(a.p);
+    const Plan how = plan_forward(a.p);
+    const int64_t grid = tiles_of(a.p, how.rows()) * a.p.q_heads;
     if (grid >= ((int64_t)1 << 31)) return GEMM_ERR_SHAPE;
     const Strided sq = strided(a.q, T, a.p.q_heads), sk = strided(a.k, T, a.p.kv_heads),
                   sv = strided(a.v, T, a.p.kv_heads), so = strided(a.out, T, a.p.q_heads);
     hipStream_t hs = static_cast<hipStream_t>(stream);
-#define FWD(DP, EX)                                                                                              \
-    do {                                                                                                          \
-        if (join)                                                                                                 \
-            hipLaunchKernelGGL((attention_fwd<DP, EX, 1, 4>), dim3((unsigned)grid), dim3(256), 0, hs, p, sq, sk, \
-                               sv, so, a.lse);                                                                    \
-        else                                                                                                      \
-            hipLaunchKernelGGL((attention_fwd<DP, EX, 1, 1>), dim3((unsigned)grid), dim3(256), 0, hs, p, sq, sk, \
-                               sv, so, a.lse);                                                                    \
+#define FWD_AS(DP, EX, RB, WS)                                                                                     \
+    hipLaunchKernelGGL((attention_fwd<DP, EX, RB, WS>), dim3((unsigned)grid), dim3(256), 0, hs, p, sq, sk, sv, so, \
+                       a.lse)
+#define FWD(DP, EX)                           \
+    do {                                      \
+        if (how.ws == 1) FWD_AS(DP, EX, 2, 1); \
+        else if (how.rb == 2) FWD_AS(DP, EX, 2, 4); \
+        else FWD_AS(DP, EX, 1, 4);            \
     } while (0)
     ATTN_BY_DIM(FWD);
 #undef FWD
+#undef FWD_AS
     return hipGetLastError() == hipSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
 }
 
@@ -819,34 +902,33 @@ int attn_backward(const attn_backward_args *args, void *stream) {
     const uintptr_t l0 = reinterpret_cast<uintptr_t>(a.lse), e0 = reinterpret_cast<uintptr_t>(a.delta);
     if (l0 < e0 + (uintptr_t)row_bytes && e0 < l0 + (uintptr_t)row_bytes) return GEMM_ERR_ALIAS;
 
-    Problem p = device_problem(a.p), pk;
-    pk = p;
-    const bool join = joined(a.p, HQ), joink = joined(a.p, HK);
-    p.tiles = (int)tiles_of(a.p, join ? 16 : 64);
-    pk.tiles = (int)tiles_of(a.p, joink ? 16 : 64);
-    const int64_t grid = (int64_t)p.tiles * HQ, gridk = (int64_t)pk.tiles * HK;
+    const Problem p = device_problem(a.p);
+    const Plan how = plan_backward(a.p, HQ), howk = plan_backward(a.p, HK);
+    const int64_t grid = tiles_of(a.p, how.rows()) * HQ, gridk = tiles_of(a.p, howk.rows()) * HK;
     if (grid >= ((int64_t)1 << 31) || gridk >= ((int64_t)1 << 31)) return GEMM_ERR_SHAPE;
     const Strided sg = strided(a.dout, T, HQ), sq = strided(a.q, T, HQ), sk = strided(a.k, T, HK),
                   sv = strided(a.v, T, HK), so = strided(a.out, T, HQ), dq = strided(a.dq, T, HQ),
                   dk = strided(a.dk, T, HK), dv = strided(a.dv, T, HK);
     hipStream_t hs = static_cast<hipStream_t>(stream);
-#define BWD(DP, EX)                                                                                                 \
-    do {                                                                                                             \
-        if (join)                                                                                                    \
-            hipLaunchKernelGGL((attention_bwd_dq<DP, EX, 1, 4>), dim3((unsigned)grid), dim3(256), 0, hs, p, sg, sq, \
-                               sk, sv, so, a.lse, a.delta, dq);                                                      \
-        else                                                                                                         \
-            hipLaunchKernelGGL((attention_bwd_dq<DP, EX, 1, 1>), dim3((unsigned)grid), dim3(256), 0, hs, p, sg, sq, \
-                               sk, sv, so, a.lse, a.delta, dq);                                                      \
-        if (joink)                                                                                                   \
-            hipLaunchKernelGGL((attention_bwd_dkv<DP, EX, 1, 4>), dim3((unsigned)gridk), dim3(256), 0, hs, pk, sg,  \
-                               sq, sk, sv, a.lse, a.delta, dk, dv);                                                  \
-        else                                                                                                         \
-            hipLaunchKernelGGL((attention_bwd_dkv<DP, EX, 1, 1>), dim3((unsigned)gridk), dim3(256), 0, hs, pk, sg,  \
-                               sq, sk, sv, a.lse, a.delta, dk, dv);                                                  \
+#define DQ_AS(DP, EX, RB, WS)                                                                                        \
+    hipLaunchKernelGGL((attention_bwd_dq<DP, EX, RB, WS>), dim3((unsigned)grid), dim3(256), 0, hs, p, sg, sq, sk, sv, \
+                       so, a.lse, a.delta, dq)
+#define DKV_AS(DP, EX, RB, WS)                                                                                     \
+    hipLaunchKernelGGL((attention_bwd_dkv<DP, EX, RB, WS>), dim3((unsigned)gridk), dim3(256), 0, hs, p, sg, sq, sk, \
+                       sv, a.lse, a.delta, dk, dv)
+#define BWD(DP, EX)                                   \
+    do {                                              \
+        if (how.ws == 1) DQ_AS(DP, EX, 2, 1);         \
+        else if (how.rb == 2) DQ_AS(DP, EX, 2, 4);    \
+        else DQ_AS(DP, EX, 1, 4);                     \
+        if (howk.ws == 1) DKV_AS(DP, EX, 2, 1);       \
+        else if (howk.rb == 2) DKV_AS(DP, EX, 2, 4);  \
+        else DKV_AS(DP, EX, 1, 4);                    \
     } while (0)
     ATTN_BY_DIM(BWD);
 #undef BWD
+#undef DQ_AS
+#undef DKV_AS
     return hipGetLastError() == hipSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
 }
 
