@@ -110,18 +110,22 @@ typedef struct attn_forward_args {
 int attn_forward(const attn_forward_args *args, void *stream);
 
 /*
- * dq, dk, dv from dout, q, k, v and the forward's out and lse.  delta is
- * scratch of q_heads * tokens floats; its contents need not be kept.  No
- * output may overlap another array of the call (views of one buffer whose
- * elements do not overlap are fine).
+ * dq, dk, dv from dout, q, k, v and the forward's out and lse.  No output may
+ * overlap another array of the call (views of one buffer whose elements do
+ * not overlap are fine).  The workspace holds at least
+ * attn_backward_workspace_bytes bytes (0 for small problems, -1 for ones the
+ * call refuses), 4-byte aligned, of any contents; calls that may run at the
+ * same time need one each (GEMM_ERR_WORKSPACE when it is too small).
  */
 typedef struct attn_backward_args {
     attn_problem p;
     attn_tensor dout, q, k, v, out;
     const float *lse;
-    float *delta;
     attn_tensor dq, dk, dv;
+    void *workspace;
+    int64_t workspace_bytes;
 } attn_backward_args;
+int64_t attn_backward_workspace_bytes(const attn_problem *problem);
 int attn_backward(const attn_backward_args *args, void *stream);
 
 /* The sizes of a norm and rotation and what all rows share. */

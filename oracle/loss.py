@@ -77,7 +77,7 @@ TOL_DLOGITS = (1e-5, 1e-9)
 
 
 def distill(logits, targets, ids, teacher, temperature=1.0, mix=0.5, alpha=0.0, beta=0.0, inv_norm=1.0):
-    """Losses and dLogits of distill_cross_entropy (include/loss.h):
+    """Losses and dLogits of distill_cross_entropy (include/distill.h):
 
         t    = softmax of the teacher's used logits / tau
         kd   = tau^2 sum_j t[j] (log t[j] - log softmax(l / tau)[id[j]])

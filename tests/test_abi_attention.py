@@ -34,7 +34,7 @@ def test_statuses():
 
 def test_exports(binding):
     lib = binding.load_library()
-    for name in ("attention.h", "loss.h"):
+    for name in ("attention.h", "distill.h"):
         text = re.sub(r"/\*.*?\*/", "", _header(name), flags=re.S)
         for fn in re.findall(r"\b((?:attn|loss)_[a-z_0-9]+)\s*\(", text):
             assert hasattr(lib, fn) and fn in binding.EXPORTED, fn
@@ -42,7 +42,7 @@ def test_exports(binding):
 
 def test_struct_sizes(binding, tmp_path):
     src = tmp_path / "sizes.c"
-    src.write_text('#include <stdio.h>\n#include "attention.h"\n#include "loss.h"\nint main(void) {\n'
+    src.write_text('#include <stdio.h>\n#include "attention.h"\n#include "distill.h"\nint main(void) {\n'
                    'printf("%zu %zu %zu %zu %zu", sizeof(attn_forward_args), sizeof(attn_backward_args),\n'
                    'sizeof(attn_qk_norm_rope_args), sizeof(attn_qk_norm_rope_backward_args),\n'
                    'sizeof(loss_distill_args));\nreturn 0; }\n')
@@ -94,10 +94,10 @@ def forward(binding):
 
 @pytest.fixture(scope="module")
 def backward(binding):
-    names = list(_problem()) + _named(["g", "q", "k", "v", "o"]) + ["lse", "delta"] + _named(["dq", "dk", "dv"])
+    names = list(_problem()) + _named(["g", "q", "k", "v", "o"]) + ["lse"] + _named(["dq", "dk", "dv"]) + ["ws", "wsb"]
     heads = [4, 4, 2, 2, 4]
     values = list(_problem().values()) + sum([_tensor(i, h) for i, h in enumerate(heads)], []) + \
-        [BASE + 9 * STEP, BASE + 10 * STEP] + _tensor(5, 4) + _tensor(6, 2) + _tensor(7, 2)
+        [BASE + 9 * STEP] + _tensor(5, 4) + _tensor(6, 2) + _tensor(7, 2) + [BASE + 10 * STEP, 1 << 20]
     a = Args(binding._BACKWARD_ARGS, names, values)
     return lambda **kw: binding.load_library().attn_backward(a.pack({k.replace("_", "."): v for k, v in kw.items()}), None)
 
@@ -142,19 +142,32 @@ def test_backward_refusals(binding, backward):
         assert backward(**{f"{t}_p": 0}) == NULL
         assert backward(**{f"{t}_p": BASE + 12 * STEP + 8}) == ALIGN
         assert backward(**{f"{t}_st": 60}) == SHAPE
-    assert backward(lse=0) == NULL and backward(delta=0) == NULL
+    assert backward(lse=0) == NULL and backward(lse=BASE + 9 * STEP + 2) == ALIGN
     for i, t in enumerate(("dq", "dk", "dv")):
         for j in range(5):                                  # over each input
             assert backward(**{f"{t}_p": BASE + j * STEP}) == ALIAS
         assert backward(**{f"{t}_p": BASE + 9 * STEP}) == ALIAS      # lse
-        assert backward(**{f"{t}_p": BASE + 10 * STEP}) == ALIAS     # delta
         assert backward(**{f"{t}_sh": 32}) == SHAPE
     assert backward(dk_p=BASE + 5 * STEP) == ALIAS and backward(dv_p=BASE + 6 * STEP) == ALIAS
-    assert backward(delta=BASE + 9 * STEP + 16) == ALIAS and backward(delta=BASE + 64) == ALIAS
     # interleaved columns of one buffer whose elements overlap
     assert backward(dq_st=512, dk_st=512, dv_st=512, dk_p=BASE + 5 * STEP + 4 * 255 + 4 - 16,
                     dv_p=BASE + 5 * STEP + 4 * 384) == ALIAS
     assert backward(tokens=0) == OK
+
+
+def test_backward_workspace(binding, backward):
+    lib = binding.load_library()
+
+    def need(**kw):
+        return lib.attn_backward_workspace_bytes(binding._PROBLEM.pack(*_problem(**kw).values()))
+    assert need() == 0 and need(tokens=4000) == 4 * 4 * 4000 and need(d=66) == -1 and need(tokens=-1) == -1
+    assert lib.attn_backward_workspace_bytes(None) == -1
+    T = 4000                                               # a problem whose scratch is used
+    assert backward(tokens=T, ws=0) == WORKSPACE and backward(tokens=T, wsb=4 * 4 * T - 1) == WORKSPACE
+    assert backward(tokens=T, ws=BASE + 10 * STEP + 2) == ALIGN
+    for i in (*range(8), 9):                               # over any other array
+        assert backward(tokens=T, ws=BASE + i * STEP + 64) == ALIAS
+    assert backward(tokens=T, ws=0x20000, cu=0x20040, nseq=1) == ALIAS
 
 
 def _norm(**kw):

@@ -29,7 +29,8 @@ EXPORTED = (
     "gemm_matmul_at_swiglu_a_ex", "gemm_bwd_num_configs", "gemm_bwd_config_name", "gemm_bwd_select_config",
     "gemm_bwd_workspace_bytes", "gemm_matmul_t_swiglu_bwd", "gemm_matmul_t_swiglu_bwd_ex",
     "loss_cross_entropy", "loss_sum_losses", "loss_distill_cross_entropy", "act_ffn_swiglu_backward",
-    "act_ffn_gelu_backward", "act_gelu_inplace", "attn_forward", "attn_backward", "attn_qk_norm_rope",
+    "act_ffn_gelu_backward", "act_gelu_inplace", "attn_forward", "attn_backward",
+    "attn_backward_workspace_bytes", "attn_qk_norm_rope",
     "attn_qk_norm_rope_backward", "attn_qk_norm_rope_workspace_bytes",
     "gemm_timing_event_create", "gemm_timing_event_record", "gemm_timing_elapsed_ms", "gemm_timing_event_destroy",
 )
@@ -135,6 +136,8 @@ def _open(path):
                  "loss_distill_cross_entropy"):
         getattr(lib, name).argtypes = [ctypes.c_char_p, p]  # the packed argument struct, the stream
         getattr(lib, name).restype = c_int
+    lib.attn_backward_workspace_bytes.argtypes = [ctypes.c_char_p]
+    lib.attn_backward_workspace_bytes.restype = i64
     lib.attn_qk_norm_rope_workspace_bytes.argtypes = [i64, i64]
     lib.attn_qk_norm_rope_workspace_bytes.restype = i64
     lib.gemm_timing_event_create.argtypes = [ctypes.POINTER(ctypes.c_void_p)]
@@ -537,6 +540,8 @@ def sum_losses(losses, out=None):
     return out
 
 
+# --- distillation (include/distill.h) ---
+
 _DISTILL_ARGS = struct.Struct("=6q 3q 3q 5d")
 
 
@@ -674,7 +679,8 @@ def gelu_inplace(x, pre_gelu=None):
 # --- attention (include/attention.h) ---
 
 _FORWARD_ARGS = struct.Struct("=8qd 12q q")
-_BACKWARD_ARGS = struct.Struct("=8qd 15q 2q 9q")
+_PROBLEM = struct.Struct("=8qd")
+_BACKWARD_ARGS = struct.Struct("=8qd 15q q 9q 2q")
 _NORM_ARGS = struct.Struct("=11qd 12q")
 _NORM_BACKWARD_ARGS = struct.Struct("=11qd 18q 4q")
 
@@ -772,8 +778,7 @@ def attention_backward(dout, q, k, v, out, lse, cu_seqlens=None, causal=True, wi
     tk = _heads(k, "k", shape_k, device)
     tv = _heads(v, "v", shape_k, device)
     to = _heads(out, "out", shape_q, device)
-    rows = (shape_q[1], shape_q[0])
-    pl = _row_values(lse, "lse", rows, device)
+    pl = _row_values(lse, "lse", (shape_q[1], shape_q[0]), device)
     if dq is None:
         dq = torch.empty(shape_q, dtype=torch.float32, device=device)
     if dk is None:
@@ -783,10 +788,14 @@ def attention_backward(dout, q, k, v, out, lse, cu_seqlens=None, causal=True, wi
     tdq = _heads(dq, "dq", shape_q, device)
     tdk = _heads(dk, "dk", shape_k, device)
     tdv = _heads(dv, "dv", shape_k, device)
+    nbytes = load_library().attn_backward_workspace_bytes(_PROBLEM.pack(*problem))
+    if nbytes < 0:
+        raise GemmError(-2, "attn_backward_workspace_bytes")
     # scratch of this call's own: two captured graphs share nothing
-    delta = torch.empty(rows, dtype=torch.float32, device=device)
-    _call_packed("attn_backward", _BACKWARD_ARGS.pack(*problem, *tg, *tq, *tk, *tv, *to, pl, delta.data_ptr(), *tdq,
-                                                      *tdk, *tdv), device)
+    scratch = torch.empty((nbytes,), dtype=torch.uint8, device=device) if nbytes else None
+    _call_packed("attn_backward",
+                 _BACKWARD_ARGS.pack(*problem, *tg, *tq, *tk, *tv, *to, pl, *tdq, *tdk, *tdv,
+                                     scratch.data_ptr() if nbytes else 0, nbytes), device)
     return dq, dk, dv
 
 

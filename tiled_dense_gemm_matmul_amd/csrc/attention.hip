@@ -287,9 +287,9 @@ __device__ __forceinline__ Tile find_tile(const Problem &p, int x, bool back) {
 // Workgroups reach the 8 XCDs, each with its own L2, in turn; the heads of a
 // step are ordered by the key/value head they read, so that with 4 or 8 of
 // those (or a multiple) an XCD meets the same one or two throughout.
-__device__ __forceinline__ void head_and_tile(int heads, int group, int &h, int &x) {
-    x = blockIdx.x / heads;
-    const int slot = blockIdx.x - x * heads, shared = heads / group;
+__device__ __forceinline__ void head_and_tile(int id, int heads, int group, int &h, int &x) {
+    x = id / heads;
+    const int slot = id - x * heads, shared = heads / group;
     const int turn = slot / shared;
     h = (slot - turn * shared) * group + turn;
 }
@@ -356,7 +356,7 @@ __global__ __launch_bounds__(256, DP <= 64 ? 4 : 2) void attention_fwd(Problem p
     const int lane = threadIdx.x & 63, g = lane >> 4, m = lane & 15;
     const int wave = uniform(threadIdx.x >> 6);
     int h, x;
-    head_and_tile(p.hq, p.group, h, x);
+    head_and_tile(blockIdx.x, p.hq, p.group, h, x);
     const Tile t = find_tile<TILE>(p, x, p.causal);
     outside_rows<TILE>(p, t, x, [&](int r) {
         zero_row(o.p + r * o.st + h * o.sh, p.d);
@@ -508,15 +508,58 @@ __device__ __forceinline__ void join_rows(const Acc<DP> &acc, float *part, const
     }
 }
 
-// --- backward: dq, and delta for the other kernel ---
-template <int DP, bool EX, int RB, int WS>
-__global__ __launch_bounds__(256, DP >= 96 && RB == 2 ? 1 : 2) void attention_bwd_dq(Problem p, Strided dout, Strided q, Strided k, Strided v,
-                                                           Strided o, const float *lse, float *delta, Strided dq) {
+// --- backward ---
+//
+// One launch forms all three: the first workgroups dk and dv of a tile of
+// keys, the rest dq of a tile of rows, longest tiles first in both, so that
+// the shorter dq tiles fill what the others leave of the chip.
+//
+// delta = dout . out of every row is needed by both parts.  A kernel in front
+// writes it to memory once, or, where a launch counts for more, each part
+// forms it for itself (OWN), which costs the walk over rows a quarter more
+// loads.
+
+struct Backward {
+    Strided dout, q, k, v, o, dq, dk, dv;
+    const float *lse, *delta;
+};
+
+// dout . out of 16 rows: row m's in lanes (g, m).
+template <int DP>
+__device__ __forceinline__ float row_dots(const Rows<DP> &a, const Rows<DP> &b) {
+    f32x4 dot = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int j = 0; j < DP / 16; ++j) dot += a.x[j] * b.x[j];
+    return group_sum((dot[0] + dot[1]) + (dot[2] + dot[3]));
+}
+
+// delta [heads, tokens]: 16 lanes a row, which take the head's values in
+// 16-byte pieces.
+__global__ __launch_bounds__(256) void attention_delta(Problem p, Strided dout, Strided o, float *delta) {
+    const int e = threadIdx.x & 15;
+    const int64_t row = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
+    if (row >= (int64_t)p.hq * p.tokens) return;
+    const int t = (int)(row / p.hq), h = (int)(row - (int64_t)t * p.hq);
+    const float *x = dout.p + t * dout.st + h * dout.sh, *y = o.p + t * o.st + h * o.sh;
+    float sum = 0.0f;
+    for (int d = 4 * e; d < p.d; d += 64) {
+        const f32x4 u = *(const f32x4 *)(x + d) * *(const f32x4 *)(y + d);
+        sum += (u[0] + u[1]) + (u[2] + u[3]);
+    }
+#pragma unroll
+    for (int i = 1; i < 16; i <<= 1) sum += __shfl_xor(sum, i, 64);
+    if (e == 0) delta[(int64_t)h * p.tokens + t] = sum;
+}
+
+template <int DP, bool EX, int RB, int WS, bool OWN>
+__device__ __forceinline__ void backward_dq(const Problem &p, const Backward &a, int id, float *part) {
+    const Strided &dout = a.dout, &q = a.q, &k = a.k, &v = a.v, &o = a.o, &dq = a.dq;
+    const float *lse = a.lse;
     constexpr int WROWS = 16 * RB, WR = 4 / WS, TILE = WR * WROWS;
     const int lane = threadIdx.x & 63, g = lane >> 4, m = lane & 15;
     const int wave = uniform(threadIdx.x >> 6);
     int h, x;
-    head_and_tile(p.hq, p.group, h, x);
+    head_and_tile(id, p.hq, p.group, h, x);
     const Tile t = find_tile<TILE>(p, x, p.causal);
     outside_rows<TILE>(p, t, x, [&](int r) { zero_row(dq.p + r * dq.st + h * dq.sh, p.d); });
     if (t.r0 < 0) return;
@@ -533,15 +576,15 @@ __global__ __launch_bounds__(256, DP >= 96 && RB == 2 ? 1 : 2) void attention_bw
         const int r = r0 + 16 * b;
         Q[b].template load<EX>(rows_rsrc(q.p + h * q.sh, q.st, r, s1, p.d), q.st, p.d);
         G[b].template load<EX>(rows_rsrc(dout.p + h * dout.sh, dout.st, r, s1, p.d), dout.st, p.d);
-        Rows<DP> out;
-        out.template load<EX>(rows_rsrc(o.p + h * o.sh, o.st, r, s1, p.d), o.st, p.d);
-        f32x4 dot = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int j = 0; j < DP / 16; ++j) dot += G[b].x[j] * out.x[j];
-        del[b] = group_sum((dot[0] + dot[1]) + (dot[2] + dot[3]));
         const int64_t at = (int64_t)h * p.tokens + r + m;
+        if (OWN) {
+            Rows<DP> out;
+            out.template load<EX>(rows_rsrc(o.p + h * o.sh, o.st, r, s1, p.d), o.st, p.d);
+            del[b] = row_dots<DP>(G[b], out);
+        } else {
+            del[b] = r + m < s1 ? a.delta[at] : 0.0f;
+        }
         l2[b] = r + m < s1 ? lse[at] * kLog2e : 0.0f;
-        if (g == 0 && r + m < s1 && part_of == 0) delta[at] = del[b];
         A[b].clear();
     }
     const Range kr = keys_of(p, s0, s1, r0, WROWS);
@@ -590,25 +633,22 @@ __global__ __launch_bounds__(256, DP >= 96 && RB == 2 ? 1 : 2) void attention_bw
             });
         }
     } else {
-        __shared__ __align__(16) float part[WS == 1 ? 1 : 4 * 16 * (DP + 4)];
 #pragma unroll
         for (int b = 0; b < RB; ++b) join_rows<DP, WS>(A[b], part, dq, h, r0 + 16 * b, s1, p.d, p.scale);
     }
 }
 
-// --- backward: dk and dv ---
-//
-// The keys are held fixed and the blocks of 16 rows of every query head of
-// the group are walked over.
-template <int DP, bool EX, int RB, int WS>
-__global__ __launch_bounds__(256, DP >= 96 && RB == 2 ? 1 : 2) void attention_bwd_dkv(Problem p, Strided dout, Strided q, Strided k, Strided v,
-                                                            const float *lse, const float *delta, Strided dk,
-                                                            Strided dv) {
+// dk and dv: the keys are held fixed and the blocks of 16 rows of every query
+// head of the group are walked over.
+template <int DP, bool EX, int RB, int WS, bool OWN>
+__device__ __forceinline__ void backward_dkv(const Problem &p, const Backward &a, int id, float *part) {
+    const Strided &dout = a.dout, &q = a.q, &k = a.k, &v = a.v, &o = a.o, &dk = a.dk, &dv = a.dv;
+    const float *lse = a.lse;
     constexpr int WROWS = 16 * RB, WR = 4 / WS, TILE = WR * WROWS;
     const int lane = threadIdx.x & 63, g = lane >> 4, m = lane & 15;
     const int wave = uniform(threadIdx.x >> 6);
     int h, x;
-    head_and_tile(p.hq / p.group, 1, h, x);
+    head_and_tile(id, p.hq / p.group, 1, h, x);
     const Tile t = find_tile<TILE>(p, x, false);
     outside_rows<TILE>(p, t, x, [&](int r) {
         zero_row(dk.p + r * dk.st + h * dk.sh, p.d);
@@ -639,16 +679,17 @@ __global__ __launch_bounds__(256, DP >= 96 && RB == 2 ? 1 : 2) void attention_bw
         qh -= p.group;
         ++qb;
     }
-    Rows<DP> Q, G;
+    Rows<DP> Q, G, out;
     Cols<DP> QT, GT;
     f32x4 l4, d4;
-    const float *qp, *gp;
+    const float *qp, *gp, *op;
     int r;
     auto at = [&]() {
         const int head = h * p.group + qh;
         const bool in = n < total;
         qp = q.p + head * q.sh;
         gp = dout.p + head * dout.sh;
+        op = o.p + head * o.sh;
         r = in ? rr.lo + 16 * (blocks - 1 - qb) : s1;
     };
     auto stats = [&](const float *from) {
@@ -660,8 +701,9 @@ __global__ __launch_bounds__(256, DP >= 96 && RB == 2 ? 1 : 2) void attention_bw
     at();
     Q.template load<EX>(rows_rsrc(qp, q.st, r, s1, p.d), q.st, p.d);
     G.template load<EX>(rows_rsrc(gp, dout.st, r, s1, p.d), dout.st, p.d);
+    if (OWN) out.template load<EX>(rows_rsrc(op, o.st, r, s1, p.d), o.st, p.d);
+    else d4 = stats(a.delta);
     l4 = stats(lse);
-    d4 = stats(delta);
     while (n < total) {
         const int row = r;
         const float *qc = qp, *gc = gp;
@@ -675,6 +717,11 @@ __global__ __launch_bounds__(256, DP >= 96 && RB == 2 ? 1 : 2) void attention_bw
         f32x4 s[RB], dp[RB];
 #pragma unroll
         for (int b = 0; b < RB; ++b) s[b] = dots<DP>(Q, K[b]);
+        if (OWN) {
+            const float del = row_dots<DP>(G, out);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) d4[i] = __shfl(del, 4 * g + i, 64);
+        }
         GT.template load<EX>(rows_rsrc(gc, dout.st, row, s1, p.d), dout.st, p.d);
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -701,7 +748,7 @@ __global__ __launch_bounds__(256, DP >= 96 && RB == 2 ? 1 : 2) void attention_bw
             }
         }
         l4 = stats(lse);
-        d4 = stats(delta);
+        if (!OWN) d4 = stats(a.delta);
 #pragma unroll
         for (int b = 0; b < RB; ++b) DV[b].add(GT, s[b]);
         Q.template load<EX>(rows_rsrc(qp, q.st, r, s1, p.d), q.st, p.d);
@@ -709,6 +756,7 @@ __global__ __launch_bounds__(256, DP >= 96 && RB == 2 ? 1 : 2) void attention_bw
 #pragma unroll
         for (int b = 0; b < RB; ++b) DK[b].add(QT, dp[b]);
         G.template load<EX>(rows_rsrc(gp, dout.st, r, s1, p.d), dout.st, p.d);
+        if (OWN) out.template load<EX>(rows_rsrc(op, o.st, r, s1, p.d), o.st, p.d);
         __builtin_amdgcn_sched_barrier(0);
     }
 
@@ -727,13 +775,20 @@ __global__ __launch_bounds__(256, DP >= 96 && RB == 2 ? 1 : 2) void attention_bw
             });
         }
     } else {
-        __shared__ __align__(16) float part[WS == 1 ? 1 : 4 * 16 * (DP + 4)];
 #pragma unroll
         for (int b = 0; b < RB; ++b) {
             join_rows<DP, WS>(DK[b], part, dk, h, k0 + 16 * b, s1, p.d, p.scale);
             join_rows<DP, WS>(DV[b], part, dv, h, k0 + 16 * b, s1, p.d, 1.0f);
         }
     }
+}
+
+template <int DP, bool EX, int RBQ, int RBK, int WS, bool OWN>
+__global__ __launch_bounds__(256, DP >= 96 && (RBQ == 2 || RBK == 2) ? 1 : 2) void attention_bwd(Problem p, Backward a,
+                                                                                              int key_groups) {
+    __shared__ __align__(16) float part[WS == 1 ? 1 : 4 * 16 * (DP + 4)];
+    if ((int)blockIdx.x < key_groups) backward_dkv<DP, EX, RBK, WS, OWN>(p, a, blockIdx.x, part);
+    else backward_dq<DP, EX, RBQ, WS, OWN>(p, a, blockIdx.x - key_groups, part);
 }
 
 // --- host ---
@@ -788,30 +843,52 @@ int64_t tiles_of(const attn_problem &p, int64_t tile) {
 // waves of a workgroup to the same rows.  A second block a wave halves the
 // loads of the other side for each product; joined waves (WS = 4) make the
 // tiles short, so that the chip is full and evenly loaded, at the price of
-// the joining.  Measured over 1 to 64 sequences of 128 to 8192 rows, 8 to 16
+// the joining.  Measured over 1 to 64 sequences of 64 to 8192 rows, 8 to 16
 // heads of 32 to 128, causal and not:
 //  * few rows: one block a wave, joined (512 rows, 12 heads of 64: forward
-//    12.8 us against 13.7 with two blocks and 39.8 unjoined; backward 36, 42
-//    and 127 us);
+//    12.8 us against 13.7 with two blocks and 39.8 unjoined; backward 27.5
+//    against 33.3);
 //  * many rows: two blocks, joined (2 x 4096 rows: forward 403 us against 455
-//    with one block and 506 unjoined; backward 1380, 1760 and 1500 us);
+//    with one block and 506 unjoined; backward 1371 against 1733);
 //  * many short sequences: two blocks, each wave its own rows (64 x 128 rows:
-//    forward 26 us against 38 joined; backward 104 against 164; 16 x 512 rows:
-//    backward 232 against 266).
-// `most` is the sequence length that still counts as short.  The host knows
-// the average length only; the limits are where both are close.
+//    forward 26 us against 38 joined; backward 110 against 156; 16 x 512 rows:
+//    backward 231 against 261).
+// `many` is the number of 32-row tiles from which two blocks win, `most` the
+// average sequence length (all that the host knows) that counts as short.
 struct Plan {
     int rb, ws;
     int64_t rows() const { return 16 * rb * (4 / ws); }
 };
+int64_t average_length(const attn_problem &p) {
+    const int64_t length = p.cu_seqlens ? p.tokens / std::max<int64_t>(1, p.num_seqs) : p.tokens;
+    return p.window > 0 ? std::min(length, p.window) : length;
+}
 Plan plan(const attn_problem &p, int64_t heads, int64_t many, int64_t most) {
-    int64_t length = p.cu_seqlens ? p.tokens / std::max<int64_t>(1, p.num_seqs) : p.tokens;
-    if (p.window > 0) length = std::min(length, p.window);
-    if (length <= most && p.tokens / 128 * heads >= 512) return {2, 1};
+    if (average_length(p) <= most && p.tokens / 128 * heads >= 512) return {2, 1};
     return {p.tokens / 32 * heads >= many ? 2 : 1, 4};
 }
 Plan plan_forward(const attn_problem &p) { return plan(p, p.q_heads, 1024, 256); }
-Plan plan_backward(const attn_problem &p, int64_t heads) { return plan(p, heads, 512, 512); }
+// Keys of the backward pass: a tile of few keys takes all rows of the group's
+// heads, so two blocks pay from fewer tiles where no mask makes tiles uneven.
+Plan plan_keys(const attn_problem &p) {
+    return plan(p, p.kv_heads, !p.causal ? 192 : p.head_dim > 64 ? 256 : 320, 512);
+}
+// Rows of the backward pass: as the keys, but with shared heads two blocks
+// throughout, as there are several times as many tiles of rows then (2048
+// rows, 8 heads on 2 of 128: 299 us against 391).
+Plan plan_rows(const attn_problem &p) {
+    const Plan keys = plan_keys(p);
+    return {p.q_heads > p.kv_heads ? 2 : keys.rb, keys.ws};
+}
+
+// Whether the backward pass forms delta in its own kernel: where that is
+// short, so that a launch in front counts for more than the loads (256 rows,
+// 12 heads of 64: 16.5 us a call against 20.6; 512 rows: 30.6 against 27.5;
+// 256 rows, 8 heads of 128: 24.6 against 21.8).
+bool own_delta(const attn_problem &p) {
+    const double pairs = (double)p.tokens * (double)average_length(p) / (p.causal ? 2 : 1);
+    return pairs * (double)(p.q_heads * (p.q_heads / p.kv_heads)) * (double)(p.head_dim * p.head_dim) <= 3.3e9;
+}
 
 #define ATTN_BY_DIM(LAUNCH)                                                     \
     do {                                                                        \
@@ -872,6 +949,11 @@ int attn_forward(const attn_forward_args *args, void *stream) {
     return hipGetLastError() == hipSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
 }
 
+int64_t attn_backward_workspace_bytes(const attn_problem *problem) {
+    if (problem == nullptr || check_problem(*problem) != GEMM_OK) return -1;
+    return own_delta(*problem) ? 0 : problem->q_heads * problem->tokens * 4;
+}
+
 int attn_backward(const attn_backward_args *args, void *stream) {
     if (args == nullptr) return GEMM_ERR_NULL;
     const attn_backward_args &a = *args;
@@ -885,50 +967,55 @@ int attn_backward(const attn_backward_args *args, void *stream) {
         if ((st = check_tensor(x, T, D)) != GEMM_OK) return st;
     for (const View &x : res)
         if ((st = check_tensor(x, T, D)) != GEMM_OK) return st;
-    if (a.lse == nullptr || a.delta == nullptr) return GEMM_ERR_NULL;
-    if (!aligned(a.lse, 4) || !aligned(a.delta, 4)) return GEMM_ERR_ALIGN;
+    if (a.lse == nullptr) return GEMM_ERR_NULL;
+    if (!aligned(a.lse, 4)) return GEMM_ERR_ALIGN;
     const int64_t row_bytes = HQ * T * 4, cu_bytes = (a.p.num_seqs + 1) * 4;
+    const bool own = own_delta(a.p);
+    if (!own) {
+        if (a.workspace == nullptr || a.workspace_bytes < row_bytes) return GEMM_ERR_WORKSPACE;
+        if (!aligned(a.workspace, 4)) return GEMM_ERR_ALIGN;
+        const Span delta = {a.workspace, row_bytes};
+        if (spans_overlap(delta, {a.lse, row_bytes}) || spans_overlap(delta, {a.p.cu_seqlens, cu_bytes}))
+            return GEMM_ERR_ALIAS;
+        for (const View &x : in)
+            if (in_range(x, a.workspace, row_bytes, T, D)) return GEMM_ERR_ALIAS;
+        for (const View &x : res)
+            if (in_range(x, a.workspace, row_bytes, T, D)) return GEMM_ERR_ALIAS;
+    }
     for (int i = 0; i < 3; ++i) {
         for (const View &x : in)
             if (overlap(res[i], x, T, D)) return GEMM_ERR_ALIAS;
         for (int j = 0; j < i; ++j)
             if (overlap(res[i], res[j], T, D)) return GEMM_ERR_ALIAS;
-        if (in_range(res[i], a.lse, row_bytes, T, D) || in_range(res[i], a.delta, row_bytes, T, D) ||
-            in_range(res[i], a.p.cu_seqlens, cu_bytes, T, D))
+        if (in_range(res[i], a.lse, row_bytes, T, D) || in_range(res[i], a.p.cu_seqlens, cu_bytes, T, D))
             return GEMM_ERR_ALIAS;
     }
-    for (const View &x : in)
-        if (in_range(x, a.delta, row_bytes, T, D)) return GEMM_ERR_ALIAS;
-    const uintptr_t l0 = reinterpret_cast<uintptr_t>(a.lse), e0 = reinterpret_cast<uintptr_t>(a.delta);
-    if (l0 < e0 + (uintptr_t)row_bytes && e0 < l0 + (uintptr_t)row_bytes) return GEMM_ERR_ALIAS;
-
     const Problem p = device_problem(a.p);
-    const Plan how = plan_backward(a.p, HQ), howk = plan_backward(a.p, HK);
-    const int64_t grid = tiles_of(a.p, how.rows()) * HQ, gridk = tiles_of(a.p, howk.rows()) * HK;
-    if (grid >= ((int64_t)1 << 31) || gridk >= ((int64_t)1 << 31)) return GEMM_ERR_SHAPE;
-    const Strided sg = strided(a.dout, T, HQ), sq = strided(a.q, T, HQ), sk = strided(a.k, T, HK),
-                  sv = strided(a.v, T, HK), so = strided(a.out, T, HQ), dq = strided(a.dq, T, HQ),
-                  dk = strided(a.dk, T, HK), dv = strided(a.dv, T, HK);
+    const Plan keys = own ? Plan{1, 4} : plan_keys(a.p), rows = own ? keys : plan_rows(a.p);
+    // whole turns of the 8 XCDs, so that the second part's heads keep to theirs
+    const int64_t nk = (tiles_of(a.p, keys.rows()) * HK + 7) / 8 * 8, grid = nk + tiles_of(a.p, rows.rows()) * HQ;
+    if (grid >= ((int64_t)1 << 31) || (HQ * T + 15) / 16 >= ((int64_t)1 << 31)) return GEMM_ERR_SHAPE;
+    const Backward b = {strided(a.dout, T, HQ), strided(a.q, T, HQ),  strided(a.k, T, HK),  strided(a.v, T, HK),
+                        strided(a.out, T, HQ),  strided(a.dq, T, HQ), strided(a.dk, T, HK), strided(a.dv, T, HK),
+                        a.lse, static_cast<const float *>(a.workspace)};
     hipStream_t hs = static_cast<hipStream_t>(stream);
-#define DQ_AS(DP, EX, RB, WS)                                                                                        \
-    hipLaunchKernelGGL((attention_bwd_dq<DP, EX, RB, WS>), dim3((unsigned)grid), dim3(256), 0, hs, p, sg, sq, sk, sv, \
-                       so, a.lse, a.delta, dq)
-#define DKV_AS(DP, EX, RB, WS)                                                                                     \
-    hipLaunchKernelGGL((attention_bwd_dkv<DP, EX, RB, WS>), dim3((unsigned)gridk), dim3(256), 0, hs, p, sg, sq, sk, \
-                       sv, a.lse, a.delta, dk, dv)
-#define BWD(DP, EX)                                   \
-    do {                                              \
-        if (how.ws == 1) DQ_AS(DP, EX, 2, 1);         \
-        else if (how.rb == 2) DQ_AS(DP, EX, 2, 4);    \
-        else DQ_AS(DP, EX, 1, 4);                     \
-        if (howk.ws == 1) DKV_AS(DP, EX, 2, 1);       \
-        else if (howk.rb == 2) DKV_AS(DP, EX, 2, 4);  \
-        else DKV_AS(DP, EX, 1, 4);                    \
+    if (!own)
+        hipLaunchKernelGGL(attention_delta, dim3((unsigned)((HQ * T + 15) / 16)), dim3(256), 0, hs, p, b.dout, b.o,
+                           static_cast<float *>(a.workspace));
+#define BWD_AS(DP, EX, RBQ, RBK, WS, OWN)                                                                         \
+    hipLaunchKernelGGL((attention_bwd<DP, EX, RBQ, RBK, WS, OWN>), dim3((unsigned)grid), dim3(256), 0, hs, p, b, \
+                       (int)nk)
+#define BWD(DP, EX)                                              \
+    do {                                                         \
+        if (own) BWD_AS(DP, EX, 1, 1, 4, true);                  \
+        else if (keys.ws == 1) BWD_AS(DP, EX, 2, 2, 1, false);   \
+        else if (keys.rb == 2) BWD_AS(DP, EX, 2, 2, 4, false);   \
+        else if (rows.rb == 2) BWD_AS(DP, EX, 2, 1, 4, false);   \
+        else BWD_AS(DP, EX, 1, 1, 4, false);                     \
     } while (0)
     ATTN_BY_DIM(BWD);
 #undef BWD
-#undef DQ_AS
-#undef DKV_AS
+#undef BWD_AS
     return hipGetLastError() == hipSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
 }
 

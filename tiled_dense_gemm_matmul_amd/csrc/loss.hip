@@ -36,6 +36,7 @@
 #include <type_traits>
 #include <utility>
 
+#include "distill.h"
 #include "gemm_fwd.h"
 #include "loss.h"
 
