@@ -110,6 +110,13 @@ struct Rows {
 #pragma unroll
         for (int j = 0; j < NJ; ++j) x[j] = load4(r, (EX || 16 * j + 4 * g < d) ? at + 64 * j : kOOB);
     }
+    // Lays the rows out in LDS, DP + 4 values apart: the 16 lanes that write or
+    // read together then meet 64 different banks, along a row or across.
+    __device__ __forceinline__ void stage(float *to) const {
+        const int lane = threadIdx.x & 63, g = lane >> 4, m = lane & 15;
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) *(f32x4 *)(to + m * (DP + 4) + 16 * j + 4 * g) = x[j];
+    }
 };
 
 // 16 rows of a head with lane (g, m) holding, of rows 4g + i, the values that
@@ -130,6 +137,17 @@ struct Cols {
 #pragma unroll
             for (int c = 0; c < N4; ++c) x[i][c] = load4(r, (EX || 64 * c + 4 * m < d) ? row + 256 * c + 16 * m : kOOB);
             if (N2) y[i] = load2(r, (EX || 64 * N4 + 2 * m < d) ? row + 256 * N4 + 8 * m : kOOB);
+        }
+    }
+    // the same from a wave's staged rows (Rows::stage)
+    __device__ __forceinline__ void take(const float *staged) {
+        const int lane = threadIdx.x & 63, g = lane >> 4, m = lane & 15;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float *row = staged + (4 * g + i) * (DP + 4);
+#pragma unroll
+            for (int c = 0; c < N4; ++c) x[i][c] = *(const f32x4 *)(row + 64 * c + 4 * m);
+            if (N2) y[i] = *(const f32x2 *)(row + 64 * N4 + 2 * m);
         }
     }
     // the value of row 4g + i that belongs to MFMA tile t
@@ -527,6 +545,16 @@ __device__ __forceinline__ void join_rows(const Acc<DP> &acc, float *part, const
 // forms it for itself (OWN), which costs the walk over rows a quarter more
 // loads.
 
+//
+// Keys, queries and dout are needed both along the rows and across them.
+// Heads of up to 64 are loaded once and turned in LDS, in a space of each
+// wave's own (no barrier); with one block a wave the turned rows are read a
+// product ahead of their own (EARLY), with two there are no registers for it.
+// Wider heads are loaded twice, which was faster for them (8 heads of 128,
+// 4096 rows: 1011 us against 1024; 12 heads of 64, 512 rows: 27.7 us loaded
+// twice against 25.5).
+constexpr int kStagedWidth = 64;
+
 struct Backward {
     Strided dout, q, k, v, o, dq, dk, dv;
     const float *lse, *delta;
@@ -560,7 +588,7 @@ __global__ __launch_bounds__(256) void attention_delta(Problem p, Strided dout, 
 }
 
 template <int DP, bool EX, int RB, int WS, bool OWN>
-__device__ __forceinline__ void backward_dq(const Problem &p, const Backward &a, int id, float *part) {
+__device__ __forceinline__ void backward_dq(const Problem &p, const Backward &a, int id, float *shared) {
     const Strided &dout = a.dout, &q = a.q, &k = a.k, &v = a.v, &o = a.o, &dq = a.dq;
     const float *lse = a.lse;
     constexpr int WROWS = 16 * RB, WR = 4 / WS, TILE = WR * WROWS;
@@ -598,20 +626,25 @@ __device__ __forceinline__ void backward_dq(const Problem &p, const Backward &a,
     const Range kr = keys_of(p, s0, s1, r0, WROWS);
     const int step = 16 * WS;
     int kb = kr.lo + 16 * part_of;
+    constexpr bool STAGED = DP <= kStagedWidth, EARLY = RB == 1;
     Rows<DP> K, V;
     Cols<DP> T;
+    float *staged = shared + wave * 2 * 16 * (DP + 4);  // this wave's own
     K.template load<EX>(rows_rsrc(kp, k.st, kb, s1, p.d), k.st, p.d);
     V.template load<EX>(rows_rsrc(vp, v.st, kb, s1, p.d), v.st, p.d);
-    T.template load<EX>(rows_rsrc(kp, k.st, kb, s1, p.d), k.st, p.d);
+    if (!STAGED) T.template load<EX>(rows_rsrc(kp, k.st, kb, s1, p.d), k.st, p.d);
     for (; kb < kr.hi; kb += step) {
         f32x4 s[RB], dp[RB];
+        if (STAGED) K.stage(staged);
 #pragma unroll
         for (int b = 0; b < RB; ++b) s[b] = dots<DP>(K, Q[b]);
         K.template load<EX>(rows_rsrc(kp, k.st, kb + step, s1, p.d), k.st, p.d);
+        if (STAGED && EARLY) T.take(staged);
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int b = 0; b < RB; ++b) dp[b] = dots<DP>(V, G[b]);
         V.template load<EX>(rows_rsrc(vp, v.st, kb + step, s1, p.d), v.st, p.d);
+        if (STAGED && !EARLY) T.take(staged);
         __builtin_amdgcn_sched_barrier(0);
         const bool whole = all_see(p, s1, r0, WROWS, kb, 16);
 #pragma unroll
@@ -626,8 +659,10 @@ __device__ __forceinline__ void backward_dq(const Problem &p, const Backward &a,
             }
             A[b].add(T, s[b]);
         }
-        T.template load<EX>(rows_rsrc(kp, k.st, kb + step, s1, p.d), k.st, p.d);
-        __builtin_amdgcn_sched_barrier(0);
+        if (!STAGED) {
+            T.template load<EX>(rows_rsrc(kp, k.st, kb + step, s1, p.d), k.st, p.d);
+            __builtin_amdgcn_sched_barrier(0);
+        }
     }
 
     if (WS == 1) {
@@ -642,14 +677,14 @@ __device__ __forceinline__ void backward_dq(const Problem &p, const Backward &a,
         }
     } else {
 #pragma unroll
-        for (int b = 0; b < RB; ++b) join_rows<DP, WS>(A[b], part, dq, h, r0 + 16 * b, s1, p.d, p.scale);
+        for (int b = 0; b < RB; ++b) join_rows<DP, WS>(A[b], shared, dq, h, r0 + 16 * b, s1, p.d, p.scale);
     }
 }
 
 // dk and dv: the keys are held fixed and the blocks of 16 rows of every query
 // head of the group are walked over.
 template <int DP, bool EX, int RB, int WS, bool OWN>
-__device__ __forceinline__ void backward_dkv(const Problem &p, const Backward &a, int id, float *part) {
+__device__ __forceinline__ void backward_dkv(const Problem &p, const Backward &a, int id, float *shared) {
     const Strided &dout = a.dout, &q = a.q, &k = a.k, &v = a.v, &o = a.o, &dk = a.dk, &dv = a.dv;
     const float *lse = a.lse;
     constexpr int WROWS = 16 * RB, WR = 4 / WS, TILE = WR * WROWS;
@@ -712,9 +747,15 @@ __device__ __forceinline__ void backward_dkv(const Problem &p, const Backward &a
     if (OWN) out.template load<EX>(rows_rsrc(op, o.st, r, s1, p.d), o.st, p.d);
     else d4 = stats(a.delta);
     l4 = stats(lse);
+    constexpr bool STAGED = DP <= kStagedWidth, EARLY = RB == 1;
+    float *staged = shared + wave * 2 * 16 * (DP + 4), *staged_g = staged + 16 * (DP + 4);  // this wave's own
     while (n < total) {
         const int row = r;
         const float *qc = qp, *gc = gp;
+        if (STAGED) {
+            Q.stage(staged);
+            G.stage(staged_g);
+        }
         n += step;
         qh += step;
         while (qh >= p.group) {
@@ -730,11 +771,22 @@ __device__ __forceinline__ void backward_dkv(const Problem &p, const Backward &a
 #pragma unroll
             for (int i = 0; i < 4; ++i) d4[i] = __shfl(del, 4 * g + i, 64);
         }
-        GT.template load<EX>(rows_rsrc(gc, dout.st, row, s1, p.d), dout.st, p.d);
+        if (STAGED) {
+            Q.template load<EX>(rows_rsrc(qp, q.st, r, s1, p.d), q.st, p.d);
+            if (EARLY) GT.take(staged_g);
+        } else {
+            GT.template load<EX>(rows_rsrc(gc, dout.st, row, s1, p.d), dout.st, p.d);
+        }
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int b = 0; b < RB; ++b) dp[b] = dots<DP>(G, V[b]);
-        QT.template load<EX>(rows_rsrc(qc, q.st, row, s1, p.d), q.st, p.d);
+        if (STAGED) {
+            G.template load<EX>(rows_rsrc(gp, dout.st, r, s1, p.d), dout.st, p.d);
+            if (OWN) out.template load<EX>(rows_rsrc(op, o.st, r, s1, p.d), o.st, p.d);
+            if (!EARLY) GT.take(staged_g);
+        } else {
+            QT.template load<EX>(rows_rsrc(qc, q.st, row, s1, p.d), q.st, p.d);
+        }
         __builtin_amdgcn_sched_barrier(0);
         const bool whole = all_see(p, s1, row, 16, k0, WROWS);
         const f32x4 l2 = l4 * kLog2e;
@@ -757,15 +809,25 @@ __device__ __forceinline__ void backward_dkv(const Problem &p, const Backward &a
         }
         l4 = stats(lse);
         if (!OWN) d4 = stats(a.delta);
+        if (STAGED && EARLY) {
+            QT.take(staged);
+            __builtin_amdgcn_sched_barrier(0);
+        }
 #pragma unroll
         for (int b = 0; b < RB; ++b) DV[b].add(GT, s[b]);
-        Q.template load<EX>(rows_rsrc(qp, q.st, r, s1, p.d), q.st, p.d);
-        __builtin_amdgcn_sched_barrier(0);
+        if (STAGED) {
+            if (!EARLY) QT.take(staged);
+        } else {
+            Q.template load<EX>(rows_rsrc(qp, q.st, r, s1, p.d), q.st, p.d);
+            __builtin_amdgcn_sched_barrier(0);
+        }
 #pragma unroll
         for (int b = 0; b < RB; ++b) DK[b].add(QT, dp[b]);
-        G.template load<EX>(rows_rsrc(gp, dout.st, r, s1, p.d), dout.st, p.d);
-        if (OWN) out.template load<EX>(rows_rsrc(op, o.st, r, s1, p.d), o.st, p.d);
-        __builtin_amdgcn_sched_barrier(0);
+        if (!STAGED) {
+            G.template load<EX>(rows_rsrc(gp, dout.st, r, s1, p.d), dout.st, p.d);
+            if (OWN) out.template load<EX>(rows_rsrc(op, o.st, r, s1, p.d), o.st, p.d);
+            __builtin_amdgcn_sched_barrier(0);
+        }
     }
 
     if (WS == 1) {
@@ -785,8 +847,8 @@ __device__ __forceinline__ void backward_dkv(const Problem &p, const Backward &a
     } else {
 #pragma unroll
         for (int b = 0; b < RB; ++b) {
-            join_rows<DP, WS>(DK[b], part, dk, h, k0 + 16 * b, s1, p.d, p.scale);
-            join_rows<DP, WS>(DV[b], part, dv, h, k0 + 16 * b, s1, p.d, 1.0f);
+            join_rows<DP, WS>(DK[b], shared, dk, h, k0 + 16 * b, s1, p.d, p.scale);
+            join_rows<DP, WS>(DV[b], shared, dv, h, k0 + 16 * b, s1, p.d, 1.0f);
         }
     }
 }
@@ -794,9 +856,10 @@ __device__ __forceinline__ void backward_dkv(const Problem &p, const Backward &a
 template <int DP, bool EX, int RBQ, int RBK, int WS, bool OWN>
 __global__ __launch_bounds__(256, DP >= 96 && (RBQ == 2 || RBK == 2) ? 1 : 2) void attention_bwd(Problem p, Backward a,
                                                                                               int key_groups) {
-    __shared__ __align__(16) float part[WS == 1 ? 1 : 4 * 16 * (DP + 4)];
-    if ((int)blockIdx.x < key_groups) backward_dkv<DP, EX, RBK, WS, OWN>(p, a, blockIdx.x, part);
-    else backward_dq<DP, EX, RBQ, WS, OWN>(p, a, blockIdx.x - key_groups, part);
+    // the waves' turned rows, and in the end what they join
+    __shared__ __align__(16) float shared[(DP <= kStagedWidth ? 8 : 4) * 16 * (DP + 4)];
+    if ((int)blockIdx.x < key_groups) backward_dkv<DP, EX, RBK, WS, OWN>(p, a, blockIdx.x, shared);
+    else backward_dq<DP, EX, RBQ, WS, OWN>(p, a, blockIdx.x - key_groups, shared);
 }
 
 // --- host ---
