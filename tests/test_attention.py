@@ -116,6 +116,22 @@ def test_masks_on_many_rows(d, causal, window):
                layout="dense"), f"D={d} {causal} {window}")
 
 
+# one problem for each way the kernels deal out rows and keys: few rows, many
+# rows, shared heads, and many short sequences, with widths that fill the
+# kernels' and that do not
+PLANS = {"few": dict(lengths=[900], hq=8, hk=8), "many": dict(lengths=[520], tail=3, hq=64, hk=64),
+         "shared": dict(lengths=[300, 33], hq=32, hk=2),
+         "short": dict(lengths=[200, 1, 0, 130, 120, 77], first=2, tail=9, hq=128, hk=128)}
+
+
+@pytest.mark.parametrize("d", [20, 32, 48, 64, 80, 96, 100, 128])
+@pytest.mark.parametrize("plan", PLANS)
+@pytest.mark.parametrize("causal,window", [(True, 0), (False, 70)])
+def test_plans(plan, d, causal, window):
+    say(f"attention {plan} D={d} causal={causal} window={window}")
+    check(Case(d, d=d, causal=causal, window=window, **PLANS[plan]), f"{plan} D={d}")
+
+
 @pytest.mark.parametrize("lengths", [[1], [2], [15], [16], [17], [63], [64], [65], [1] * 40, [0, 5, 0, 0, 3, 0],
                                      [127, 129], [513], list(range(1, 24))])
 @pytest.mark.parametrize("causal", [True, False])
@@ -131,11 +147,14 @@ def test_shared_heads_and_layouts(hq, hk, layout):
     check(Case(hq, [200, 57], first=1, tail=5, hq=hq, hk=hk, d=64, layout=layout, window=90), f"{hq}/{hk} {layout}")
 
 
-def test_many_sequences():
-    """More sequences than one look of 64 finds, some empty."""
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("heads,longest", [(2, 9), (64, 40)])
+def test_many_sequences(causal, heads, longest):
+    """More sequences than one look of 64 finds, some empty, some of several tiles."""
     r = np.random.default_rng(3)
-    lengths = [int(x) for x in r.integers(0, 9, 300)]
-    check(Case(4, lengths, tail=3, hq=2, hk=1, d=32), "300 sequences")
+    lengths = [int(x) for x in r.integers(0, longest, 300)]
+    lengths[70], lengths[200] = 150, 70
+    check(Case(4, lengths, tail=3, hq=heads, hk=heads, d=32, causal=causal), "300 sequences")
 
 
 @pytest.mark.parametrize("gain,scale", [(6.0, None), (1.0, 2.5), (0.01, 1e-4)])
@@ -295,3 +314,18 @@ def test_streams_and_graphs():
         torch.cuda.synchronize()
         for a, b in zip(fresh, held):
             assert all(torch.equal(x, y) for x, y in zip(a, b)), turn
+
+
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("plan", PLANS)
+def test_verification_build(plan, d, monkeypatch):
+    """The shipping library against the build with fences and full waits
+    around the rows staged in LDS (heads of up to 64): the same bits."""
+    import torch
+    from tiled_dense_gemm_matmul_amd import binding
+    c = Case(d, d=d, **PLANS[plan])
+    out, lse = call(c)
+    got = (out, lse, *call_backward(c, out, lse))
+    monkeypatch.setattr(binding, "_lib", binding.load_sync_check_library())
+    want = (*call(c), *call_backward(c, out, lse))
+    assert all(torch.equal(a, b) for a, b in zip(got, want))

@@ -326,6 +326,7 @@ struct Teacher {
     __align__(16) int id[kMaxTop];
     float z[kMaxTop], l[kMaxTop];
     unsigned char twice[kMaxTop];
+    float target;  // the student's logit at the target
     Masses mass;
 };
 
@@ -440,7 +441,7 @@ __device__ __forceinline__ void load_teacher(const Distill &a, int s, const floa
 // Called once the stores of the row's gradient have been issued; waits for
 // them before any such column is written again.
 template <int NT, bool T1>
-__device__ __forceinline__ void finish_row(const Distill &a, int s, int tgt, float l_t, const RowSums &r,
+__device__ __forceinline__ void finish_row(const Distill &a, int s, int tgt, const RowSums &r,
                                            const Masses &mass, const Teacher &t, float *grad) {
     const int tid = threadIdx.x;
     const float hit = (1.0f - a.mix) * (1.0f - a.alpha) * a.inv_norm, soft = a.mix * a.tau * a.inv_norm;
@@ -478,7 +479,7 @@ __device__ __forceinline__ void finish_row(const Distill &a, int s, int tgt, flo
         }
         kd = lanes_reduce<false>(kd);
         if (tid == NT - 1) {
-            a.losses[s] = tgt >= 0 ? row_loss(r.lse, l_t, r.sum_l / (float)a.V, a.alpha, a.beta) : 0.0f;
+            a.losses[s] = tgt >= 0 ? row_loss(r.lse, t.target, r.sum_l / (float)a.V, a.alpha, a.beta) : 0.0f;
             a.losses[(size_t)a.S + s] = mass.any ? a.tau * a.tau * kd : 0.0f;
         }
     }
@@ -487,7 +488,7 @@ __device__ __forceinline__ void finish_row(const Distill &a, int s, int tgt, flo
 #pragma unroll
     for (int i = 0; i < EACH; ++i)
         if (mine[i]) grad[t.id[tid + NT * i]] = value[i];
-    if (!named && tid == 0 && tgt >= 0) grad[tgt] = gradient<T1>(a, r, l_t) - hit;
+    if (!named && tid == 0 && tgt >= 0) grad[tgt] = gradient<T1>(a, r, t.target) - hit;
 }
 
 // The row's layout for 16-byte accesses: `head` logits in front of the first
@@ -536,7 +537,7 @@ __global__ __launch_bounds__(NT, CAP == 100 ? 4 : 1) void distill_resident(Disti
     for (int j = 0; j < G; ++j)
         x[j] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rr, off(j), 0, POL));
     const float xe = edge >= 0 ? row[edge] : -INFINITY;
-    const float l_t = tgt >= 0 ? row[tgt] : 0.0f;
+    if (tid == 0) teacher.target = tgt >= 0 ? row[tgt] : 0.0f;
     load_teacher<NT>(a, s, row, teacher, tid);
     const int nv = shape.groups > tid ? min(G, (shape.groups - tid + NT - 1) / NT) : 0;  // this thread's groups
     float m = xe, sl = edge >= 0 ? xe : 0.0f;
@@ -548,7 +549,8 @@ __global__ __launch_bounds__(NT, CAP == 100 ? 4 : 1) void distill_resident(Disti
         }
     }
     // The barrier in here also makes the teacher's entries visible, and all
-    // reads of the row lie before it.
+    // reads of the row are complete before it: what they gave has been used,
+    // or written to LDS.
     const float top = block_reduce<NW, true>(m, red[0]);
     float hard = 0.0f, soft = 0.0f;
     if (edge >= 0) {
@@ -583,7 +585,7 @@ __global__ __launch_bounds__(NT, CAP == 100 ? 4 : 1) void distill_resident(Disti
         __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4v, g), rg, off(j), 0, POL);
     }
     if (edge >= 0) grad[edge] = gradient<T1>(a, r, xe);
-    finish_row<NT, T1>(a, s, tgt, l_t, r, mass, teacher, grad);
+    finish_row<NT, T1>(a, s, tgt, r, mass, teacher, grad);
 }
 
 // Rows too long for the registers, or whose gradient lies at another
@@ -608,7 +610,7 @@ __global__ __launch_bounds__(NT) void distill_stream(Distill a) {
         for (int v = tid; v < a.V; v += NT) grad[v] = 0.0f;
         return;
     }
-    const float l_t = tgt >= 0 ? row[tgt] : 0.0f;
+    if (tid == 0) teacher.target = tgt >= 0 ? row[tgt] : 0.0f;
     load_teacher<NT>(a, s, row, teacher, tid);
     float m = -INFINITY, ref = 0.0f, hard = 0.0f, soft = 0.0f, sl = 0.0f;
     auto raise = [&](float l) {  // to a larger reference
@@ -670,7 +672,7 @@ __global__ __launch_bounds__(NT) void distill_stream(Distill a) {
     } else {
         for (int v = tid; v < a.V; v += NT) grad[v] = gradient<false>(a, r, row[v]);
     }
-    finish_row<NT, false>(a, s, tgt, l_t, r, mass, teacher, grad);
+    finish_row<NT, false>(a, s, tgt, r, mass, teacher, grad);
 }
 
 bool overlaps(const void *a, size_t abytes, const void *b, size_t bbytes) {

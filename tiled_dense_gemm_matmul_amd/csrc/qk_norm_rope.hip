@@ -318,7 +318,7 @@ __global__ __launch_bounds__(1024) void weight_grads(const double *parts, int np
     }
 }
 
-bool vector_access(const attn_norm &n, const attn_tensor *const *t, int count, int64_t q_heads) {
+bool vector_access(const attn_norm &n, const attn_tensor *const *t, int count) {
     const int64_t half = n.rotated / 2, rest = n.head_dim / 2 - half;
     if (n.head_dim % 8 || (!n.interleaved && (half % 4 || rest % 4))) return false;
     if (!aligned(n.q_weight, 16) || !aligned(n.k_weight, 16)) return false;
@@ -346,8 +346,9 @@ int check_norm(const attn_norm &n) {
 
 int check_view(const View &v, int64_t tokens, int64_t d) {
     if (v.t->data == nullptr) return GEMM_ERR_NULL;
-    const int64_t most = (int64_t)1 << 40;
-    if (v.t->token_stride < 0 || v.t->head_stride < 0 || v.t->token_stride > most || v.t->head_stride > most)
+    const int64_t most = (int64_t)1 << 56;  // elements from the first to the last
+    if (v.t->token_stride < 0 || v.t->head_stride < 0 || v.t->token_stride > most / std::max<int64_t>(tokens, 1) ||
+        v.t->head_stride > most / v.heads)
         return GEMM_ERR_SHAPE;
     if (v.output && !rows_apart(v, tokens, d)) return GEMM_ERR_SHAPE;
     if (!aligned(v.t->data, 4)) return GEMM_ERR_ALIGN;
@@ -433,7 +434,7 @@ int attn_qk_norm_rope(const attn_qk_norm_rope_args *args, void *stream) {
         covers_shared(yk, a.n))
         return GEMM_ERR_ALIAS;
     const attn_tensor *all[4] = {&a.q, &a.k, &a.q_out, &a.k_out};
-    const bool vec = vector_access(a.n, all, 4, HQ);
+    const bool vec = vector_access(a.n, all, 4);
     const Norm n = device_norm(a.n);
     const Strided sq = strided(a.q, T, HQ), sk = strided(a.k, T, HK), oq = strided(a.q_out, T, HQ),
                   ok = strided(a.k_out, T, HK);
@@ -493,7 +494,7 @@ int attn_qk_norm_rope_backward(const attn_qk_norm_rope_backward_args *args, void
             if (T > 0 && in_range(*x, small[i].p, small[i].bytes, T, D)) return GEMM_ERR_ALIAS;
     }
     const attn_tensor *all[6] = {&a.dq_out, &a.dk_out, &a.q, &a.k, &a.dq, &a.dk};
-    const bool vec = vector_access(a.n, all, 6, HQ);
+    const bool vec = vector_access(a.n, all, 6);
     const Norm n = device_norm(a.n);
     const Strided g0 = strided(a.dq_out, T, HQ), g1 = strided(a.dk_out, T, HK), sq = strided(a.q, T, HQ),
                   sk = strided(a.k, T, HK), o0 = strided(a.dq, T, HQ), o1 = strided(a.dk, T, HK);
