@@ -87,6 +87,12 @@ def parse():
     ap.add_argument("--activation", action="store_true",
                     help="instead of the step: time the FFN activation kernels (ffn_swiglu_backward, "
                          "ffn_gelu_backward, gelu_inplace) at the seq-512 and 8192-token hidden sizes")
+    ap.add_argument("--attention", action="store_true",
+                    help="instead of the step: time attention and the query/key norm with rotation, forward and "
+                         "backward, on the seq-512 model's heads and on wider and longer ones")
+    ap.add_argument("--distill", action="store_true",
+                    help="instead of the step: time distill_cross_entropy (64 teacher logits a row, gradient in a "
+                         "buffer of its own) on the seq-512 logits and on 4096 rows of wider vocabularies")
     ap.add_argument("--mfma-ceiling", action="store_true",
                     help="instead of the step: run the MFMA ceiling probe (independent fp32 MFMAs only) at 4, 8 "
                          "and 16 waves per CU and print the sustained TFLOP/s and engine clock")
@@ -333,6 +339,129 @@ def time_activation():
             lines.append(f"| {name} | {n} | {bpe} | {warm:.2f} | {nbytes / warm / 1e3:.0f} | {cold:.2f} | "
                          f"{nbytes / cold / 1e3:.0f} | {100 * nbytes / cold / 1e3 / PEAK_HBM_GBS:.1f} |")
     print("\n".join(lines))
+    return rows
+
+
+def visible_pairs(lengths, causal, window):
+    """How many (row, key) pairs attention over these sequences scores."""
+    import numpy as np
+    pairs = 0
+    for n in lengths:
+        i, w = np.arange(n, dtype=np.int64), window or n
+        pairs += int(np.minimum(i + 1, w).sum())
+        if not causal:
+            pairs += int(np.minimum(n - 1 - i, w - 1).sum())
+    return pairs
+
+
+# label, sequence lengths, query heads, key/value heads, head width, causal, window
+ATTENTION_CASES = [
+    ("seq 512", [512], 12, 12, 64, True, 0),
+    ("16 x 512", [512] * 16, 12, 12, 64, True, 0),
+    ("16 x 512, both ways", [512] * 16, 12, 12, 64, False, 0),
+    ("8192", [8192], 12, 12, 64, True, 0),
+    ("8192, shared heads", [8192], 12, 4, 64, True, 0),
+    ("4096, wide heads", [4096], 8, 8, 128, True, 0),
+    ("2 x 4096, window 512", [4096] * 2, 16, 4, 128, True, 512),
+]
+# label, tokens, query heads, key heads, head width
+NORM_CASES = [("seq 512", 512, 12, 12, 64), ("16 x 512", 8192, 12, 12, 64), ("8192, wide heads", 8192, 32, 8, 128)]
+
+
+def time_attention():
+    """attention and attention_backward, then qk_norm_rope and its backward,
+    through the binding with preallocated results, back to back behind
+    busy_blocker() (launch gaps included).  Flops: 4 a (row, key, dimension)
+    forward and 10 backward, where the kernels do 14 (they form the scores
+    and dout v twice).  Bytes: each array of the norm read or written once."""
+    import numpy as np
+    import torch
+    from tiled_dense_gemm_matmul_amd import binding
+    dev = torch.device("cuda:0")
+    g = torch.Generator(device="cuda").manual_seed(0)
+
+    def per_call(fn):
+        t0 = time.perf_counter()
+        while time.perf_counter() - t0 < 0.2:
+            fn()
+            torch.cuda.synchronize()
+        return float(np.median([batch_time(fn, 10) for _ in range(5)]))
+
+    rows = []
+    print("| sequences | heads (q/kv x width) | mask | forward us | TFLOP/s | backward us | TFLOP/s |\n"
+          "|---|---|---|---|---|---|---|")
+    for label, lengths, hq, hk, d, causal, window in ATTENTION_CASES:
+        T = sum(lengths)
+        qkv = torch.randn((T, (hq + 2 * hk) * d), device=dev, generator=g)
+        q, k, v = (x.unflatten(1, (-1, d)) for x in qkv.split([hq * d, hk * d, hk * d], 1))
+        dq, dk, dv = (x.unflatten(1, (-1, d)) for x in torch.empty_like(qkv).split([hq * d, hk * d, hk * d], 1))
+        cu = torch.tensor([0, *np.cumsum(lengths)], dtype=torch.int32, device=dev)
+        kw = {"cu_seqlens": cu, "causal": causal, "window": window}
+        out, lse = binding.attention(q, k, v, **kw)
+        dout = torch.randn(out.shape, device=dev, generator=g)
+        fwd = per_call(lambda: binding.attention(q, k, v, out=out, lse=lse, **kw))
+        bwd = per_call(lambda: binding.attention_backward(dout, q, k, v, out, lse, dq=dq, dk=dk, dv=dv, **kw))
+        work = visible_pairs(lengths, causal, window) * hq * d
+        row = {"case": label, "tokens": T, "heads": f"{hq}/{hk} x {d}", "fwd_us": round(fwd, 1),
+               "fwd_tflops": round(4e-6 * work / fwd, 1), "bwd_us": round(bwd, 1),
+               "bwd_tflops": round(10e-6 * work / bwd, 1)}
+        rows.append(row)
+        mask = ("causal" if causal else "none") + (f", window {window}" if window else "")
+        print(f"| {label} | {row['heads']} | {mask} | {fwd:.1f} | {row['fwd_tflops']} | {bwd:.1f} | "
+              f"{row['bwd_tflops']} |", flush=True)
+    print("\n| tokens | heads (q + k x width) | norm and rotation us | GB/s | backward us | GB/s |\n"
+          "|---|---|---|---|---|---|")
+    for label, T, hq, hk, d in NORM_CASES:
+        q, k, gq, gk = (torch.randn((T, h, d), device=dev, generator=g) for h in (hq, hk, hq, hk))
+        w = torch.ones(d, device=dev)
+        common = (w, w, torch.arange(T, dtype=torch.int32, device=dev),
+                  10000.0 ** (-torch.arange(d // 2, device=dev) / (d // 2)))
+        a, b = torch.empty_like(q), torch.empty_like(k)
+        fwd = per_call(lambda: binding.qk_norm_rope(q, k, *common, q_out=a, k_out=b))
+        dw = torch.empty((2, d), device=dev)
+        bwd = per_call(lambda: binding.qk_norm_rope_backward(gq, gk, q, k, *common, dq=a, dk=b, dq_weight=dw[0],
+                                                             dk_weight=dw[1]))
+        nbytes = 4 * T * (hq + hk) * d
+        row = {"case": label, "tokens": T, "heads": f"{hq} + {hk} x {d}", "fwd_us": round(fwd, 1),
+               "fwd_GBps": round(2e-3 * nbytes / fwd), "bwd_us": round(bwd, 1), "bwd_GBps": round(3e-3 * nbytes / bwd)}
+        rows.append(row)
+        print(f"| {label} | {row['heads']} | {fwd:.1f} | {row['fwd_GBps']} | {bwd:.1f} | {row['bwd_GBps']} |", flush=True)
+    return rows
+
+
+DISTILL_CASES = [(512, 16384, 2.0), (4096, 4096, 2.0), (4096, 32000, 2.0), (4096, 50304, 2.0), (4096, 50304, 1.0),
+                 (1024, 100000, 2.0)]
+
+
+def time_distill():
+    """distill_cross_entropy with 64 teacher logits (binary16) a row and the
+    gradient in a buffer of its own, back to back behind busy_blocker().
+    Bytes: the logits read once, the gradient written once."""
+    import numpy as np
+    import torch
+    from tiled_dense_gemm_matmul_amd import binding
+    dev = torch.device("cuda:0")
+    g = torch.Generator(device="cuda").manual_seed(0)
+    rows = []
+    print("| logits | temperature | us | GB/s |\n|---|---|---|---|")
+    for S, V, tau in DISTILL_CASES:
+        logits = torch.randn((S, V), device=dev, generator=g) * 3
+        dl = torch.empty_like(logits)
+        losses = torch.empty((2, S), device=dev)
+        t = torch.randint(V, (S,), device=dev, dtype=torch.int32, generator=g)
+        ids = torch.randint(V, (S, 64), device=dev, dtype=torch.int32, generator=g)
+        z = (torch.randn((S, 64), device=dev, generator=g) * 2).half()
+        run = lambda: binding.distill_cross_entropy(logits, t, ids, z, tau, 0.5, inv_norm=1.0 / S,  # noqa: E731
+                                                    dlogits=dl, losses=losses)
+        t0 = time.perf_counter()
+        while time.perf_counter() - t0 < 0.2:
+            run()
+            torch.cuda.synchronize()
+        us = float(np.median([batch_time(run, 10) for _ in range(5)]))
+        rows.append({"S": S, "V": V, "temperature": tau, "us": round(us, 1), "GBps": round(8e-3 * S * V / us)})
+        print(f"| {S} x {V} | {tau:g} | {us:.1f} | {rows[-1]['GBps']} |", flush=True)
+        del logits, dl
+        torch.cuda.empty_cache()
     return rows
 
 
@@ -1137,6 +1266,12 @@ def main():
         return
     if args.activation:
         time_activation()
+        return
+    if args.attention:
+        time_attention()
+        return
+    if args.distill:
+        time_distill()
         return
     if args.copy_calibration:
         copy_calibration()
