@@ -25,8 +25,8 @@
  *   dv_j = sum_{heads of the group, i} p_ij dout_i
  *
  * Rows in front of cu_seqlens[0] and from cu_seqlens[num_seqs] on belong to
- * no sequence: they are not read, and their out, dq, dk and dv are zero and
- * their lse is minus infinity.  Nothing passes between sequences, whatever
+ * no sequence: what they hold takes no part, their out, dq, dk and dv are
+ * zero and their lse is minus infinity.  Nothing passes between sequences, whatever
  * the rows of another one or of none hold; inside a sequence a NaN or an
  * infinity can reach all of its rows.  cu_seqlens must not decrease; entries
  * outside [0, tokens] are clamped to it and a decreasing entry reads as an

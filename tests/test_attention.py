@@ -239,6 +239,28 @@ def test_writes_stay_inside(heads):
     assert got is q and torch.equal(q, plain[0])
 
 
+def test_heads_of_three_tensors_in_turn():
+    """Queries, keys and values of each head side by side, as some projections
+    lay them out: inputs and gradients as views of such buffers, and a layout
+    whose views do share elements refused."""
+    import torch
+    from tiled_dense_gemm_matmul_amd import binding
+    T, H, d = 90, 5, 32
+    buf = torch.randn((T, H, 3, d), device=device())
+    q, k, v = buf.unbind(2)
+    out, lse = binding.attention(q, k, v)
+    do = torch.randn_like(out)
+    want = binding.attention_backward(do, *(x.contiguous() for x in (q, k, v)), out, lse)
+    grad = torch.full((T, H, 3, d), SENTINEL, device=device())
+    dq, dk, dv = grad.unbind(2)
+    binding.attention_backward(do, q, k, v, out, lse, dq=dq, dk=dk, dv=dv)
+    assert all(torch.equal(a, b) for a, b in zip((dq, dk, dv), want))
+    near = grad.view(T, -1)[:, 16:16 + (H - 1) * 3 * d + d].as_strided((T, H, d), (H * 3 * d, 3 * d, 1))
+    with pytest.raises(binding.GemmError) as e:
+        binding.attention_backward(do, q, k, v, out, lse, dq=near, dk=dk, dv=dv)
+    assert e.value.status == -5
+
+
 def test_offsets_past_32_bits():
     """Rows 16 K values apart, past 8 GiB into the buffer: sampled tiles of a windowed sequence."""
     import torch
@@ -263,6 +285,81 @@ def test_offsets_past_32_bits():
     assert res["fails"] == 0, res
     del buf, a, b, q, k, v, do
     torch.cuda.empty_cache()
+
+
+def test_many_rows():
+    """Three million rows: row numbers, tile numbers and offsets far past any
+    other test's, sampled against the oracle at both ends."""
+    import torch
+    from tiled_dense_gemm_matmul_amd import binding
+    T, d, w = 3000000, 32, 8
+    g = torch.Generator(device=device())
+    g.manual_seed(2)
+    q, k, v, do = (torch.randn((T, 1, d), generator=g, device=device()) for _ in range(4))
+    out, lse = binding.attention(q, k, v, window=w)
+    grads = binding.attention_backward(do, q, k, v, out, lse, window=w)
+    for rows in (slice(0, 120), slice(T - 120, T)):
+        host = [x[rows].cpu().numpy() for x in (do, q, k, v, out)]
+        keep = slice(0, 120 - w) if rows.start == 0 else slice(w, 120)   # rows whose neighbours are all here
+        ro, _, eo, _ = OA.attention(*host[1:4], window=w)
+        res = OA.compare(host[4][keep], ro[keep], eo[keep])
+        assert res["fails"] == 0, res
+        want = OA.attention_backward(*host, lse[:, rows].cpu().numpy(), window=w)
+        for y, ref, err in zip(grads, want[:3], want[3:]):
+            res = OA.compare(y[rows][keep].cpu().numpy(), ref[keep], err[keep])
+            assert res["fails"] == 0, res
+
+
+def test_broadcast_views():
+    """Key/value heads that are one tensor seen several times are read like
+    any others; rows that are one row seen several times are refused, and so
+    are outputs of either kind."""
+    import torch
+    from tiled_dense_gemm_matmul_amd import binding
+    r = torch.randn((50, 1, 64), device=device())
+    q = torch.randn((50, 4, 64), device=device())
+    k = r.expand(50, 4, 64)
+    out, lse = binding.attention(q, k, k)
+    want = binding.attention(q, k.contiguous(), k.contiguous())
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    got = binding.attention_backward(q, q, k, k, out, lse)
+    want = binding.attention_backward(q, q, k.contiguous(), k.contiguous(), out, lse)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    rows = torch.randn((1, 4, 64), device=device()).expand(50, 4, 64)
+    for call_it in (lambda: binding.attention(rows, k, k), lambda: binding.attention(q, k, k, out=rows),
+                    lambda: binding.attention_backward(rows, q, k, k, out, lse),
+                    lambda: binding.attention_backward(q, q, k, k, out, lse, dk=torch.empty_like(r).expand(50, 4, 64))):
+        with pytest.raises(binding.GemmError) as e:
+            call_it()
+        assert e.value.status == -2
+    # one token has no stride between tokens
+    one = torch.randn((4, 64), device=device()).as_strided((1, 4, 64), (0, 64, 1))
+    out, lse = binding.attention(one, one, one)
+    assert torch.allclose(out, one) and bool(torch.isfinite(lse).all())
+    grads = binding.attention_backward(one, one, one, one, out, lse)
+    # a single key: the probability is 1 whatever the scores
+    assert torch.allclose(grads[2], one) and float(grads[0].abs().max()) < 1e-5
+
+
+def test_refusals_on_the_device():
+    """Views that cannot be taken in 16-byte pieces, and results over inputs."""
+    import torch
+    from tiled_dense_gemm_matmul_amd import binding
+    buf = torch.randn((20, 4 * 64 + 2), device=device())
+    odd = buf[:, 1:257].unflatten(1, (4, 64))              # base and token stride off
+    q = odd.contiguous()
+    for bad, status in ((lambda: binding.attention(odd, q, q), -3), (lambda: binding.attention(q, q, q, out=q), -5),
+                        (lambda: binding.attention(q, q.clone(), q.clone(), scale=0.0), -4),
+                        (lambda: binding.attention(q[..., :62], q[..., :62], q[..., :62]), -2)):
+        with pytest.raises(binding.GemmError) as e:
+            bad()
+        assert e.value.status == status
+    with pytest.raises(ValueError):
+        binding.attention(q, q.cpu(), q)
+    with pytest.raises(TypeError):
+        binding.attention(q.double(), q, q)
+    with pytest.raises(ValueError):
+        binding.attention(q.transpose(1, 2), q.transpose(1, 2), q.transpose(1, 2))
 
 
 @pytest.mark.parametrize("heads", [2, 64])

@@ -35,15 +35,21 @@ int64_t extent(const View &v, int64_t tokens, int64_t d) {
 
 // Whether two tensors may share an element.  Tensors in separate ranges do
 // not; nor do views of one buffer with the same token stride whose spans
-// within a token's row lie apart.
+// within a token's row lie apart, or whose heads lie between one another's.
 bool overlap(const View &a, const View &b, int64_t tokens, int64_t d) {
     const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.t->data), b0 = reinterpret_cast<uintptr_t>(b.t->data);
     if (a0 >= b0 + (uintptr_t)extent(b, tokens, d) || b0 >= a0 + (uintptr_t)extent(a, tokens, d)) return false;
-    const int64_t st = a.t->token_stride * 4;
-    const int64_t sa = ((a.heads - 1) * a.t->head_stride + d) * 4, sb = ((b.heads - 1) * b.t->head_stride + d) * 4;
+    const int64_t st = a.t->token_stride * 4, sh = a.t->head_stride * 4, bytes = d * 4;
+    const int64_t sa = (a.heads - 1) * sh + bytes, sb = (b.heads - 1) * b.t->head_stride * 4 + bytes;
     if (a.t->token_stride != b.t->token_stride || sa > st || sb > st) return true;
-    const int64_t from_a = (int64_t)(((int64_t)(b0 - a0) % st + st) % st);
-    return from_a < sa || from_a + sb > st;
+    const int64_t from_a = (int64_t)(((int64_t)(b0 - a0) % st + st) % st);  // b's place in a token's row of a
+    if (from_a >= sa && from_a + sb <= st) return false;
+    auto between = [&](int64_t off) {  // heads at this distance fall between the other's
+        const int64_t r = (off % sh + sh) % sh;
+        return r >= bytes && sh - r >= bytes;
+    };
+    return !(a.heads > 1 && b.heads > 1 && a.t->head_stride == b.t->head_stride && sh > 0 && between(from_a) &&
+             between(from_a - st));
 }
 
 bool in_range(const View &v, const void *p, int64_t bytes, int64_t tokens, int64_t d) {
