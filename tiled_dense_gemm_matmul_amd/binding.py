@@ -755,10 +755,10 @@ def attention(q, k, v, cu_seqlens=None, causal=True, window=0, scale=None, out=N
     tv = _heads(v, "v", shape_k, device)
     tokens, hq, _ = shape_q
     if out is None:
-        out = torch.empty(shape_q, dtype=torch.float32, device=device)
+        out = q.new_empty(shape_q)
     to = _heads(out, "out", shape_q, device)
     if lse is None:
-        lse = torch.empty((hq, tokens), dtype=torch.float32, device=device)
+        lse = q.new_empty((hq, tokens))
     pl = _row_values(lse, "lse", (hq, tokens), device)
     _call_packed("attn_forward", _FORWARD_ARGS.pack(*problem, *tq, *tk, *tv, *to, pl), device)
     return out, lse
@@ -780,11 +780,11 @@ def attention_backward(dout, q, k, v, out, lse, cu_seqlens=None, causal=True, wi
     to = _heads(out, "out", shape_q, device)
     pl = _row_values(lse, "lse", (shape_q[1], shape_q[0]), device)
     if dq is None:
-        dq = torch.empty(shape_q, dtype=torch.float32, device=device)
+        dq = q.new_empty(shape_q)
     if dk is None:
-        dk = torch.empty(shape_k, dtype=torch.float32, device=device)
+        dk = q.new_empty(shape_k)
     if dv is None:
-        dv = torch.empty(shape_k, dtype=torch.float32, device=device)
+        dv = q.new_empty(shape_k)
     tdq = _heads(dq, "dq", shape_q, device)
     tdk = _heads(dk, "dk", shape_k, device)
     tdv = _heads(dv, "dv", shape_k, device)
@@ -792,7 +792,7 @@ def attention_backward(dout, q, k, v, out, lse, cu_seqlens=None, causal=True, wi
     if nbytes < 0:
         raise GemmError(-2, "attn_backward_workspace_bytes")
     # scratch of this call's own: two captured graphs share nothing
-    scratch = torch.empty((nbytes,), dtype=torch.uint8, device=device) if nbytes else None
+    scratch = q.new_empty((nbytes // 4,)) if nbytes else None
     _call_packed("attn_backward",
                  _BACKWARD_ARGS.pack(*problem, *tg, *tq, *tk, *tv, *to, pl, *tdq, *tdk, *tdv,
                                      scratch.data_ptr() if nbytes else 0, nbytes), device)
@@ -846,9 +846,9 @@ def qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, eps=1e-6, interl
     tq = _heads(q, "q", shape_q, device)
     tk = _heads(k, "k", shape_k, device)
     if q_out is None:
-        q_out = torch.empty(shape_q, dtype=torch.float32, device=device)
+        q_out = q.new_empty(shape_q)
     if k_out is None:
-        k_out = torch.empty(shape_k, dtype=torch.float32, device=device)
+        k_out = q.new_empty(shape_k)
     toq = _heads(q_out, "q_out", shape_q, device)
     tok = _heads(k_out, "k_out", shape_k, device)
     _call_packed("attn_qk_norm_rope", _NORM_ARGS.pack(*fields, *tq, *tk, *toq, *tok), device)
@@ -868,23 +868,23 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, positions, i
     tq = _heads(q, "q", shape_q, device)
     tk = _heads(k, "k", shape_k, device)
     if dq is None:
-        dq = torch.empty(shape_q, dtype=torch.float32, device=device)
+        dq = q.new_empty(shape_q)
     if dk is None:
-        dk = torch.empty(shape_k, dtype=torch.float32, device=device)
+        dk = q.new_empty(shape_k)
     tdq = _heads(dq, "dq", shape_q, device)
     tdk = _heads(dk, "dk", shape_k, device)
     tokens, _, dim = shape_q
     if dq_weight is None:
-        dq_weight = torch.empty((dim,), dtype=torch.float32, device=device)
+        dq_weight = q.new_empty((dim,))
     if dk_weight is None:
-        dk_weight = torch.empty((dim,), dtype=torch.float32, device=device)
+        dk_weight = q.new_empty((dim,))
     pqw = _vector(dq_weight, "dq_weight", device, dim)
     pkw = _vector(dk_weight, "dk_weight", device, dim)
     nbytes = load_library().attn_qk_norm_rope_workspace_bytes(tokens, dim)
     if nbytes < 0:
         raise GemmError(-2, "attn_qk_norm_rope_workspace_bytes")
     # scratch of this call's own: two captured graphs share nothing
-    scratch = torch.empty((nbytes,), dtype=torch.uint8, device=device)
+    scratch = q.new_empty((nbytes // 4,))
     _call_packed("attn_qk_norm_rope_backward",
                  _NORM_BACKWARD_ARGS.pack(*fields, *tgq, *tgk, *tq, *tk, *tdq, *tdk, pqw, pkw, scratch.data_ptr(),
                                           nbytes), device)
