@@ -96,14 +96,14 @@ __device__ __forceinline__ f32x4 mfma(float a, float b, f32x4 c) {
 }
 
 // Between a wave's writes of staged rows and its reads of them by other lanes,
-// and the other way round: its LDS accesses complete in the order they are
-// issued, and the compiler, which cannot tell the lanes' addresses apart,
-// issues them in program order.  A fence here cost up to 2.8% (16 x 512 rows
-// backward, 229 against 236 us), so only the verification build has it, with
-// a full wait; the results are compared bit for bit.
+// and the other way round.  A wave's LDS accesses complete in the order they
+// are issued, so this only keeps the compiler from moving LDS accesses across
+// (a fence of all memory also holds back the loads in flight and cost up to
+// 2.8%: 16 x 512 rows backward, 229 against 236 us).  The verification build
+// waits in full; the results are compared bit for bit.
 __device__ __forceinline__ void staged_order() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
 #ifdef GEMM_SYNC_CHECK
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_s_waitcnt(0);
 #endif
 }
@@ -126,10 +126,10 @@ struct Rows {
     // Lays the rows out in LDS, DP + 4 values apart: the 16 lanes that write or
     // read together then meet 64 different banks, along a row or across.
     __device__ __forceinline__ void stage(float *to) const {
+        staged_order();
         const int lane = threadIdx.x & 63, g = lane >> 4, m = lane & 15;
 #pragma unroll
         for (int j = 0; j < NJ; ++j) *(f32x4 *)(to + m * (DP + 4) + 16 * j + 4 * g) = x[j];
-        staged_order();
     }
 };
 
