@@ -95,7 +95,7 @@ typedef struct attn_problem {
  * not overlap q otherwise, nor k, v, lse or cu_seqlens.
  *
  * GEMM_ERR_NULL for a missing array, GEMM_ERR_SHAPE for sizes outside the
- * above (tokens < 2^30, heads <= 65535, num_seqs < 2^24) or strides that are
+ * above (tokens < 2^30 - 64, heads <= 65535, num_seqs < 2^24) or strides that are
  * too small, overlap an output's own elements or reach 2^22 elements from one
  * token to the next, GEMM_ERR_ALIGN, GEMM_ERR_DTYPE for a scale that is not
  * positive and finite or a causal that is neither 0 nor 1, GEMM_ERR_ALIAS,

@@ -115,6 +115,13 @@ def test_problem_refusals(forward, backward, bad, status):
     assert forward(**bad) == status and backward(**bad) == status
 
 
+def test_most_tokens(forward, backward):
+    """The tiles of 64 sequences still sum to less than 2^31."""
+    assert forward(tokens=(1 << 30) - 64) == SHAPE and backward(tokens=(1 << 30) - 64) == SHAPE
+    rises = 32 * ((1 << 30) - 65)      # of 65 bounds that go up and down
+    assert rises // 16 + 64 < 1 << 31
+
+
 def test_forward_refusals(binding, forward):
     assert binding.load_library().attn_forward(None, None) == NULL
     for t in "qkvo":
