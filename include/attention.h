@@ -27,8 +27,9 @@
  * Rows in front of cu_seqlens[0] and from cu_seqlens[num_seqs] on belong to
  * no sequence: what they hold takes no part, their out, dq, dk and dv are
  * zero and their lse is minus infinity.  Nothing passes between sequences, whatever
- * the rows of another one or of none hold; inside a sequence a NaN or an
- * infinity can reach all of its rows.  cu_seqlens must not decrease; entries
+ * the rows of another one or of none hold; inside a sequence a NaN, an
+ * infinity or a score of 2^30 or more in magnitude can reach all of its rows
+ * (as NaN).  cu_seqlens must not decrease; entries
  * outside [0, tokens] are clamped to it and a decreasing entry reads as an
  * empty sequence (the results are then unspecified, but no access leaves the
  * arrays).

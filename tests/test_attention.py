@@ -163,6 +163,33 @@ def test_scales(gain, scale):
     check(Case(9, [150], hq=2, hk=2, d=64, gain=gain, scale=scale), f"gain {gain} scale {scale}")
 
 
+@pytest.mark.parametrize("tokens,heads", [(40, 1), (128, 512)])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_scores_near_the_largest(sign, tokens, heads):
+    """Scores up to 1.4 2^29, 2^20 and more apart: each row takes one key's
+    value.  That value is multiplied by a probability, divided by the same
+    one (a reciprocal and a product) and rounded each time, so it is off by
+    less than 2^-21 of itself.  lse is the largest score through the product
+    with scale log2(e) and back with ln 2, four roundings and two constants'
+    of 2^-24, and the logarithm of a sum of up to 2^63, another 2^-24."""
+    import torch
+    from tiled_dense_gemm_matmul_amd import binding
+    dev = device()
+    r = np.random.default_rng(12)
+    q = torch.zeros((tokens, heads, 32), device=dev)
+    k, v = torch.zeros_like(q), to_dev(r.standard_normal((tokens, heads, 32)).astype(np.float32))
+    steps = (1.0 + torch.arange(tokens, device=dev) / (4.0 * tokens)) * 1.1
+    q[:, :, 3] = 2.0 ** 14
+    k[:, :, 3] = (sign * 2.0 ** 15 * steps)[:, None]
+    out, lse = binding.attention(q, k, v, causal=False, scale=1.0)
+    torch.cuda.synchronize()
+    best = tokens - 1 if sign > 0 else 0
+    score = float(q[0, 0, 3].double() * k[best, 0, 3].double())
+    err = (out.double() - v[best].double()).abs()
+    assert bool((err <= 2.0 ** -21 * v[best].double().abs()).all())
+    assert bool(((lse.double() - score).abs() <= 2.0 ** -21 * abs(score)).all())
+
+
 def test_empty():
     import torch
     from tiled_dense_gemm_matmul_amd import binding

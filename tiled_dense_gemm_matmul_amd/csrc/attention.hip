@@ -879,7 +879,10 @@ __global__ __launch_bounds__(256, DP >= 96 && (RBQ == 2 || RBK == 2) ? 1 : 2) vo
 
 // --- host ---
 
-constexpr int64_t kMaxTokens = (int64_t)1 << 30, kMaxStride = (int64_t)1 << 22, kMaxHeadStride = (int64_t)1 << 40;
+// Tokens stay so far below 2^30 that the tiles of 64 sequences, as find_tile
+// counts them, sum to less than 2^31 whatever cu_seqlens holds: 64 bounds that
+// go up and down rise by 32 times the tokens at most, in tiles of 16 rows or more.
+constexpr int64_t kMaxTokens = ((int64_t)1 << 30) - 64, kMaxStride = (int64_t)1 << 22, kMaxHeadStride = (int64_t)1 << 40;
 
 int check_tensor(const View &v, int64_t tokens, int64_t d) {
     if (v.t->data == nullptr) return GEMM_ERR_NULL;
