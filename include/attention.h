@@ -29,7 +29,10 @@
  * zero and their lse is minus infinity.  Nothing passes between sequences, whatever
  * the rows of another one or of none hold; inside a sequence a NaN, an
  * infinity or a score of 2^30 or more in magnitude can reach all of its rows
- * (as NaN).  cu_seqlens must not decrease; entries
+ * (as NaN).  The backward pass forms p_ij from the score and from lse, both
+ * rounded to fp32: each is off by about 2^-23 |s_ij| of itself, except where
+ * one key holds all of a row's probability: that key's is 1 at any score.
+ * cu_seqlens must not decrease; entries
  * outside [0, tokens] are clamped to it and a decreasing entry reads as an
  * empty sequence (the results are then unspecified, but no access leaves the
  * arrays).

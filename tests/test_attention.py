@@ -190,6 +190,65 @@ def test_scores_near_the_largest(sign, tokens, heads):
     assert bool(((lse.double() - score).abs() <= 2.0 ** -21 * abs(score)).all())
 
 
+# the ways the backward pass deals out rows: few (delta formed within), many, and many short sequences' worth
+LARGE = {"few": (40, 1), "many": (1024, 32), "short": (128, 512)}
+
+
+@pytest.mark.parametrize("shape", LARGE)
+@pytest.mark.parametrize("d,scale", [(20, 0.37), (32, None), (64, None), (128, None)])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_gradients_of_large_scores(shape, d, scale, sign):
+    """Scores from 2^12 to 2^30 in magnitude, of rows that see one key and of
+    rows that see all of them, one 2^-12 of the score or more above the rest
+    (exp of -256 is below every fp32 number).  The one key's probability is 1 whatever its score:
+    lse is the score in fp32 (q holds one power of two, so q.k is exact and
+    the product with scale its only rounding) and dv of a row that only itself
+    sees is its dout, both to the bit; dv of the best key is the sum of all
+    rows' dout and of the others zero.  ds is dout.v - dout.out, two sums of d
+    products each off by (d + 1) u, with an out that is off by 2^-21; dq and
+    dk are its products with k and q."""
+    import torch
+    from tiled_dense_gemm_matmul_amd import binding
+    T, heads = LARGE[shape]
+    u, factor = 2.0 ** -24, np.float32(d ** -0.5 if scale is None else scale)
+    g = torch.Generator(device=device())
+    g.manual_seed(d)
+    v, do = (torch.randn((T, heads, d), generator=g, device=device()) for _ in range(2))
+    size = (do * v).abs().double().sum(2)
+    for power in (12, 20, 24, 29):
+        q, k = torch.zeros_like(v), torch.zeros_like(v)
+        q[:, :, 3] = 2.0 ** (power // 2)
+        key = sign * 2.0 ** (power - power // 2) / float(factor)
+        # one visible key, of any score
+        k[:, :, 3] = key * (1.0 + 0.9 * torch.rand((T, heads), generator=g, device=device()))
+        out, lse = binding.attention(q, k, v, window=1, scale=scale)
+        dq, dk, dv = binding.attention_backward(do, q, k, v, out, lse, window=1, scale=scale)
+        score = (q[:, :, 3] * k[:, :, 3]).cpu().numpy() * factor
+        assert np.array_equal(lse.t().cpu().numpy(), score), (power, "lse")
+        assert torch.equal(dv, do), (power, "dv")
+        e = (2 * (d + 2) * u + 2.0 ** -21) * size * float(factor) * (1 + 8 * u)
+        assert bool((dq[:, :, 3].double().abs() <= e * k[:, :, 3].double().abs()).all()), (power, "dq")
+        assert bool((dk[:, :, 3].double().abs() <= e * q[:, :, 3].double().abs()).all()), (power, "dk")
+        if power < 20:
+            continue
+        # all keys, one of them far above the rest
+        steps = 1.0 + torch.arange(T, device=device()) / (4.0 * T)
+        k[:, :, 3] = (key * steps * 1.1)[:, None]
+        best = T - 1 if sign > 0 else 0
+        out, lse = binding.attention(q, k, v, causal=False, scale=scale)
+        dq, dk, dv = binding.attention_backward(do, q, k, v, out, lse, causal=False, scale=scale)
+        score = (q[0, 0, 3] * k[best, 0, 3]).cpu().numpy() * factor
+        assert bool((lse == float(score)).all()), (power, "lse of many")
+        total, most = do.double().sum(0), do.double().abs().sum(0)
+        assert bool(((dv[best].double() - total).abs() <= (T + 2) * u * most).all()), (power, "dv of many")
+        dv[best], dk_best = 0.0, dk[best].clone()
+        dk[best] = 0.0
+        assert not dv.any() and not dk.any(), power
+        e = (2 * (d + 2) * u + 2.0 ** -21) * (do * v[best]).abs().double().sum(2) * float(factor) * (1 + (T + 8) * u)
+        assert bool((dq[:, :, 3].double().abs() <= e * k[best, 0, 3].double().abs()).all()), (power, "dq of many")
+        assert bool((dk_best[:, 3].double().abs() <= e.sum(0) * 2.0 ** (power // 2)).all()), (power, "dk of many")
+
+
 def test_empty():
     import torch
     from tiled_dense_gemm_matmul_amd import binding

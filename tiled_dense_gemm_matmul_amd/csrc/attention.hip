@@ -73,6 +73,29 @@ struct Problem {
     float scale, c;  // c = scale log2(e): scores go through exp2
 };
 
+// A row's lse from the sum of exp2(s c - top) over its raw scores s and the
+// largest of them, most: the largest score, rounded to fp32 once, plus the
+// logarithm of the sum relative to that score.  Where one key holds all of
+// the probability the second part is next to nothing, so lse is that score to
+// the bit and the backward pass gets 1 back however large the score is.
+// (Taken as (top + log2(sum)) ln 2, it came back an ulp or two of the score
+// away: probabilities were off by up to 14% at scores of 2^20 and by up to a
+// factor of 2^96 at 2^29.)
+__device__ __forceinline__ float lse_of(const Problem &p, float sum, float top, float most) {
+#pragma clang fp contract(off)  // the largest score's rounding is the backward pass's
+    const float score = most * p.scale;
+    const float rest = (__builtin_amdgcn_logf(sum) - fmaf(most, p.c, -top)) * kLn2;
+    return score + rest;
+}
+// The probability of a raw score in the backward pass.  The score is rounded
+// as in lse_of before lse is taken from it: two instructions a score more than
+// one multiply-add with scale log2(e).
+__device__ __forceinline__ float probability(const Problem &p, float s, float lse) {
+#pragma clang fp contract(off)
+    const float score = s * p.scale;
+    return __builtin_amdgcn_exp2f((score - lse) * kLog2e);
+}
+
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
 // Rows [row, end) of a head, at most 16 of them, as a buffer.
@@ -411,13 +434,14 @@ __global__ __launch_bounds__(256, DP <= 64 ? 4 : 2) void attention_fwd(Problem p
 
     Rows<DP> Q[RB];
     Acc<DP> O[RB];
-    float top[RB], sum[RB];
+    float top[RB], sum[RB], largest[RB];  // the reference in units of log 2, the sum, the largest raw score
 #pragma unroll
     for (int b = 0; b < RB; ++b) {
         Q[b].template load<EX>(rows_rsrc(q.p + h * q.sh, q.st, r0 + 16 * b, s1, p.d), q.st, p.d);
         O[b].clear();
         top[b] = kNoMax;
         sum[b] = 0.0f;
+        largest[b] = -INFINITY;
     }
     const Range kr = keys_of(p, s0, s1, r0, WROWS);
     const int step = 16 * WS;
@@ -446,7 +470,8 @@ __global__ __launch_bounds__(256, DP <= 64 ? 4 : 2) void attention_fwd(Problem p
         }
 #pragma unroll
         for (int b = 0; b < RB; ++b) {
-            const float most = fmaxf(fmaxf(s[b][0], s[b][1]), fmaxf(s[b][2], s[b][3])) * p.c;
+            largest[b] = fmaxf(fmaxf(fmaxf(fmaxf(largest[b], s[b][0]), s[b][1]), s[b][2]), s[b][3]);
+            const float most = largest[b] * p.c;  // once the reference has moved, no longer above it
             if (__any(most > top[b] + 8.0f)) {
                 const float to = fmaxf(top[b], group_max(most));
                 const float f = __builtin_amdgcn_exp2f(top[b] - to);
@@ -463,7 +488,10 @@ __global__ __launch_bounds__(256, DP <= 64 ? 4 : 2) void attention_fwd(Problem p
         }
     }
 #pragma unroll
-    for (int b = 0; b < RB; ++b) sum[b] = group_sum(sum[b]);
+    for (int b = 0; b < RB; ++b) {
+        sum[b] = group_sum(sum[b]);
+        largest[b] = group_max(largest[b]);
+    }
 
     if (WS == 1) {
 #pragma unroll
@@ -476,13 +504,13 @@ __global__ __launch_bounds__(256, DP <= 64 ? 4 : 2) void attention_fwd(Problem p
                 store4(ro, (EX || d0 < p.d) ? m * (int)o.st * 4 + d0 * 4 : kOOB, y * inv);
             });
             if (g == 0 && r + m < s1)
-                lse[(int64_t)h * p.tokens + r + m] = (top[b] + __builtin_amdgcn_logf(sum[b])) * kLn2;
+                lse[(int64_t)h * p.tokens + r + m] = lse_of(p, sum[b], top[b], largest[b]);
         }
     } else {
         // join the waves of the same rows, in order, 16 rows at a time
         constexpr int LD = DP + 4;
         __shared__ __align__(16) float part[WS == 1 ? 1 : 4][WS == 1 ? 1 : 16 * LD];
-        __shared__ float ptop[4][16], psum[4][16];
+        __shared__ float ptop[4][16], psum[4][16], plargest[4][16];
         const int mine = wave % WR, e = threadIdx.x & 15;
 #pragma unroll
         for (int b = 0; b < RB; ++b) {
@@ -491,14 +519,18 @@ __global__ __launch_bounds__(256, DP <= 64 ? 4 : 2) void attention_fwd(Problem p
             if (g == 0) {
                 ptop[wave][m] = top[b];
                 psum[wave][m] = sum[b];
+                plargest[wave][m] = largest[b];
             }
             __syncthreads();
             for (int row = part_of * 4 + g; row < 16; row += 4 * WS) {
                 const int r = r0 + 16 * b + row;
                 if (r >= s1) continue;
-                float to = ptop[mine][row], total = 0.0f, f[WS];
+                float to = ptop[mine][row], most = plargest[mine][row], total = 0.0f, f[WS];
 #pragma unroll
-                for (int w = 1; w < WS; ++w) to = fmaxf(to, ptop[w * WR + mine][row]);
+                for (int w = 1; w < WS; ++w) {
+                    to = fmaxf(to, ptop[w * WR + mine][row]);
+                    most = fmaxf(most, plargest[w * WR + mine][row]);
+                }
 #pragma unroll
                 for (int w = 0; w < WS; ++w) {
                     f[w] = __builtin_amdgcn_exp2f(ptop[w * WR + mine][row] - to);
@@ -516,7 +548,7 @@ __global__ __launch_bounds__(256, DP <= 64 ? 4 : 2) void attention_fwd(Problem p
                         *(f32x4 *)(dst + d0) = y * inv;
                     }
                 }
-                if (e == 0) lse[(int64_t)h * p.tokens + r] = (to + __builtin_amdgcn_logf(total)) * kLn2;
+                if (e == 0) lse[(int64_t)h * p.tokens + r] = lse_of(p, total, to, most);
             }
         }
     }
@@ -621,7 +653,7 @@ __device__ __forceinline__ void backward_dq(const Problem &p, const Backward &a,
 
     Rows<DP> Q[RB], G[RB];
     Acc<DP> A[RB];
-    float l2[RB], del[RB];
+    float l[RB], del[RB];
 #pragma unroll
     for (int b = 0; b < RB; ++b) {
         const int r = r0 + 16 * b;
@@ -635,7 +667,7 @@ __device__ __forceinline__ void backward_dq(const Problem &p, const Backward &a,
         } else {
             del[b] = r + m < s1 ? a.delta[at] : 0.0f;
         }
-        l2[b] = r + m < s1 ? lse[at] * kLog2e : 0.0f;
+        l[b] = r + m < s1 ? lse[at] : 0.0f;
         A[b].clear();
     }
     const Range kr = keys_of(p, s0, s1, r0, WROWS);
@@ -666,7 +698,7 @@ __device__ __forceinline__ void backward_dq(const Problem &p, const Backward &a,
         for (int b = 0; b < RB; ++b) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                s[b][i] = __builtin_amdgcn_exp2f(fmaf(s[b][i], p.c, -l2[b])) * (dp[b][i] - del[b]);
+                s[b][i] = probability(p, s[b][i], l[b]) * (dp[b][i] - del[b]);
             if (!whole) {
                 const Range seen = keys_of(p, s0, s1, r0 + 16 * b + m, 1);
 #pragma unroll
@@ -804,12 +836,11 @@ __device__ __forceinline__ void backward_dkv(const Problem &p, const Backward &a
         }
         __builtin_amdgcn_sched_barrier(0);
         const bool whole = all_see(p, s1, row, 16, k0, WROWS);
-        const f32x4 l2 = l4 * kLog2e;
 #pragma unroll
         for (int b = 0; b < RB; ++b) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                s[b][i] = __builtin_amdgcn_exp2f(fmaf(s[b][i], p.c, -l2[i]));
+                s[b][i] = probability(p, s[b][i], l4[i]);
                 dp[b][i] = s[b][i] * (dp[b][i] - d4[i]);
             }
             if (!whole) {
