@@ -96,7 +96,8 @@ typedef struct attn_problem {
 
 /*
  * out and lse from q, k, v.  out may be the very same tensor as q; it may
- * not overlap q otherwise, nor k, v, lse or cu_seqlens.
+ * not overlap q otherwise, nor k, v, lse or cu_seqlens, and lse overlaps no
+ * other array of the call.
  *
  * GEMM_ERR_NULL for a missing array, GEMM_ERR_SHAPE for sizes outside the
  * above (tokens < 2^30 - 64, heads <= 65535, num_seqs < 2^24) or strides that are

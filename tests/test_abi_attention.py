@@ -143,6 +143,13 @@ def test_forward_refusals(binding, forward):
     assert forward(tokens=0, q_p=0, k_p=0, v_p=0, o_p=0, lse=0) == OK
 
 
+@pytest.mark.parametrize("offset", [0, 4, 8, -4 * 4 * 100 + 4])
+def test_lse_over_the_bounds_of_sequences(forward, offset):
+    """Workgroups that are done would overwrite what later ones read."""
+    lse = BASE + 9 * STEP
+    assert forward(cu=lse - offset, nseq=2) == ALIAS
+
+
 def test_backward_refusals(binding, backward):
     assert binding.load_library().attn_backward(None, None) == NULL
     for t in ("g", "q", "k", "v", "o", "dq", "dk", "dv"):

@@ -1045,7 +1045,7 @@ int attn_forward(const attn_forward_args *args, void *stream) {
     if ((!in_place && overlap(o, q, T, D)) || overlap(o, k, T, D) || overlap(o, v, T, D) ||
         in_range(o, a.lse, lse_bytes, T, D) || in_range(q, a.lse, lse_bytes, T, D) ||
         in_range(k, a.lse, lse_bytes, T, D) || in_range(v, a.lse, lse_bytes, T, D) ||
-        in_range(o, a.p.cu_seqlens, cu_bytes, T, D))
+        in_range(o, a.p.cu_seqlens, cu_bytes, T, D) || spans_overlap({a.lse, lse_bytes}, {a.p.cu_seqlens, cu_bytes}))
         return GEMM_ERR_ALIAS;
     const Problem p = device_problem(a.p);
     const Plan how = plan_forward(a.p);
