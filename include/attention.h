@@ -91,7 +91,7 @@ typedef struct attn_problem {
     int64_t head_dim;          /* a multiple of 4, 4 to 128 */
     int64_t causal;            /* 0 or 1 */
     int64_t window;            /* 0: none */
-    double scale;              /* positive and finite */
+    double scale;              /* positive, scale log2(e) finite in fp32 (up to 2.35e38) */
 } attn_problem;
 
 /*
@@ -102,8 +102,8 @@ typedef struct attn_problem {
  * GEMM_ERR_NULL for a missing array, GEMM_ERR_SHAPE for sizes outside the
  * above (tokens < 2^30 - 64, heads <= 65535, num_seqs < 2^24) or strides that are
  * too small, overlap an output's own elements or reach 2^22 elements from one
- * token to the next, GEMM_ERR_ALIGN, GEMM_ERR_DTYPE for a scale that is not
- * positive and finite or a causal that is neither 0 nor 1, GEMM_ERR_ALIAS,
+ * token to the next, GEMM_ERR_ALIGN, GEMM_ERR_DTYPE for a scale outside the
+ * above or a causal that is neither 0 nor 1, GEMM_ERR_ALIAS,
  * and GEMM_ERR_LAUNCH when the runtime rejects the launch.  tokens == 0
  * enqueues nothing.
  */

@@ -115,6 +115,13 @@ def test_problem_refusals(forward, backward, bad, status):
     assert forward(**bad) == status and backward(**bad) == status
 
 
+@pytest.mark.parametrize("scale,status", [(2.35e38, OK), (2.37e38, DTYPE), (3.4e38, DTYPE), (1e-45, OK), (1e-46, DTYPE)])
+def test_scale_times_log2_e(forward, backward, scale, status):
+    """A scale whose product with log2(e) is infinite in fp32 would turn a
+    score of zero into NaN."""
+    assert forward(scale=scale, tokens=0) == status and backward(scale=scale, tokens=0) == status
+
+
 def test_most_tokens(forward, backward):
     """The tiles of 64 sequences still sum to less than 2^31."""
     assert forward(tokens=(1 << 30) - 64) == SHAPE and backward(tokens=(1 << 30) - 64) == SHAPE

@@ -925,14 +925,17 @@ int check_tensor(const View &v, int64_t tokens, int64_t d) {
     return GEMM_OK;
 }
 
+// scale log2(e) as the forward pass folds it into its exponents: the largest
+// scales would make it infinite, and a score of zero NaN.
+float folded(double scale) { return (float)(scale * 1.44269504088896340736); }
+
 int check_problem(const attn_problem &p) {
     if (p.tokens < 0 || p.tokens >= kMaxTokens || p.q_heads < 1 || p.q_heads > 65535 || p.kv_heads < 1 ||
         p.kv_heads > p.q_heads || p.q_heads % p.kv_heads || p.head_dim < 4 || p.head_dim > 128 || p.head_dim % 4 ||
         p.window < 0)
         return GEMM_ERR_SHAPE;
     if (p.cu_seqlens && (p.num_seqs < 0 || p.num_seqs >= ((int64_t)1 << 24))) return GEMM_ERR_SHAPE;
-    if (!(p.scale > 0.0) || !std::isfinite((float)p.scale) || !((float)p.scale > 0.0f) ||
-        (p.causal != 0 && p.causal != 1))
+    if (!((float)p.scale > 0.0f) || !std::isfinite(folded(p.scale)) || (p.causal != 0 && p.causal != 1))
         return GEMM_ERR_DTYPE;
     if (!aligned(p.cu_seqlens, 4)) return GEMM_ERR_ALIGN;
     return GEMM_OK;
@@ -949,7 +952,7 @@ Problem device_problem(const attn_problem &a) {
     p.causal = (int)a.causal;
     p.window = a.window < a.tokens ? (int)a.window : 0;  // a wider window hides nothing
     p.scale = (float)a.scale;
-    p.c = (float)(a.scale * 1.44269504088896340736);
+    p.c = folded(a.scale);
     return p;
 }
 
