@@ -62,8 +62,9 @@
  * NULL for the null stream).  Every sum has a fixed order: results are
  * bitwise reproducible.
  *
- * Errors are returned synchronously, before anything is enqueued (the status
- * values are those of gemm_fwd.h).
+ * Errors are returned synchronously, before anything is enqueued, except
+ * GEMM_ERR_LAUNCH from a later one of a call's launches (the status values are
+ * those of gemm_fwd.h).
  */
 #ifndef ATTENTION_H
 #define ATTENTION_H
@@ -81,7 +82,10 @@ typedef struct attn_tensor {
     int64_t head_stride;
 } attn_tensor;
 
-/* The sizes and the mask of an attention call. */
+/* The sizes and the mask of an attention call.  The tiles of all heads,
+ * q_heads (tokens / 16 + num_seqs) or fewer, number less than 2^31
+ * (GEMM_ERR_SHAPE), those of q_heads and kv_heads together in the backward
+ * pass. */
 typedef struct attn_problem {
     const int32_t *cu_seqlens; /* [num_seqs + 1] device array, or NULL: one sequence of all tokens */
     int64_t num_seqs;          /* ignored when cu_seqlens is NULL */

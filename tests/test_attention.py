@@ -396,6 +396,36 @@ def test_many_rows():
             assert res["fails"] == 0, res
 
 
+def wide_case(seed):
+    """More workgroups than one launch takes: 65535 heads by 300 sequences,
+    most of them empty, over 64 rows."""
+    import torch
+    from tiled_dense_gemm_matmul_amd import binding
+    g = torch.Generator(device=device())
+    g.manual_seed(seed)
+    T, H, d = 64, 65535, 4
+    cu = np.full(301, T, np.int32)
+    cu[:4] = 1, 20, 20, 57
+    q, k, v, do = (torch.randn((T, H, d), generator=g, device=device()) for _ in range(4))
+    return binding, cu, to_dev(cu), q, k, v, do
+
+
+def test_more_workgroups_than_one_launch_takes():
+    """Every part of the grid is done: the same bits as calls over fewer heads."""
+    import torch
+    binding, cu, dcu, q, k, v, _ = wide_case(1)
+    out, lse = binding.attention(q, k, v, cu_seqlens=dcu)
+    for at in range(0, q.shape[1], 8000):
+        some = slice(at, min(at + 8000, q.shape[1]))
+        o2, l2 = binding.attention(*(x[:, some].contiguous() for x in (q, k, v)), cu_seqlens=dcu)
+        assert torch.equal(out[:, some], o2) and torch.equal(lse[some], l2)
+    some = slice(65532, 65535)
+    ro, rl, eo, el = OA.attention(*(x[:, some].cpu().numpy() for x in (q, k, v)), cu=cu)
+    for y, ref, err in ((out[:, some], ro, eo), (lse[some], rl, el)):
+        res = OA.compare(y.cpu().numpy(), ref, err)
+        assert res["fails"] == 0, res
+
+
 def test_broadcast_views():
     """Key/value heads that are one tensor seen several times are read like
     any others; rows that are one row seen several times are refused, and so

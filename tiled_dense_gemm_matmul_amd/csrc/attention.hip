@@ -50,6 +50,7 @@
 
 #include "attention.h"
 #include "gemm_fwd.h"
+#include "launch.h"
 #include "strided.h"
 
 namespace {
@@ -70,6 +71,7 @@ constexpr float kNoMax = -3.0e38f;
 struct Problem {
     const int *cu;
     int nseq, tokens, hq, group, d, causal, window;
+    int first;       // workgroups in front of this launch's
     float scale, c;  // c = scale log2(e): scores go through exp2
 };
 
@@ -420,7 +422,7 @@ __global__ __launch_bounds__(256, DP <= 64 ? 4 : 2) void attention_fwd(Problem p
     const int lane = threadIdx.x & 63, g = lane >> 4, m = lane & 15;
     const int wave = uniform(threadIdx.x >> 6);
     int h, x;
-    head_and_tile(blockIdx.x, p.hq, p.group, h, x);
+    head_and_tile(p.first + (int)blockIdx.x, p.hq, p.group, h, x);
     const Tile t = find_tile<TILE>(p, x, p.causal);
     outside_rows<TILE>(p, t, x, [&](int r) {
         zero_row(o.p + r * o.st + h * o.sh, p.d);
@@ -951,6 +953,7 @@ Problem device_problem(const attn_problem &a) {
     p.d = (int)a.head_dim;
     p.causal = (int)a.causal;
     p.window = a.window < a.tokens ? (int)a.window : 0;  // a wider window hides nothing
+    p.first = 0;
     p.scale = (float)a.scale;
     p.c = folded(a.scale);
     return p;
@@ -1050,26 +1053,27 @@ int attn_forward(const attn_forward_args *args, void *stream) {
         in_range(k, a.lse, lse_bytes, T, D) || in_range(v, a.lse, lse_bytes, T, D) ||
         in_range(o, a.p.cu_seqlens, cu_bytes, T, D) || spans_overlap({a.lse, lse_bytes}, {a.p.cu_seqlens, cu_bytes}))
         return GEMM_ERR_ALIAS;
-    const Problem p = device_problem(a.p);
+    Problem p = device_problem(a.p);
     const Plan how = plan_forward(a.p);
     const int64_t grid = tiles_of(a.p, how.rows()) * a.p.q_heads;
     if (grid >= ((int64_t)1 << 31)) return GEMM_ERR_SHAPE;
     const Strided sq = strided(a.q, T, a.p.q_heads), sk = strided(a.k, T, a.p.kv_heads),
                   sv = strided(a.v, T, a.p.kv_heads), so = strided(a.out, T, a.p.q_heads);
     hipStream_t hs = static_cast<hipStream_t>(stream);
-#define FWD_AS(DP, EX, RB, WS)                                                                                     \
-    hipLaunchKernelGGL((attention_fwd<DP, EX, RB, WS>), dim3((unsigned)grid), dim3(256), 0, hs, p, sq, sk, sv, so, \
-                       a.lse)
+    return in_slices(grid, 256, [&](int64_t first, unsigned count) {
+        p.first = (int)first;
+#define FWD_AS(DP, EX, RB, WS) \
+    hipLaunchKernelGGL((attention_fwd<DP, EX, RB, WS>), dim3(count), dim3(256), 0, hs, p, sq, sk, sv, so, a.lse)
 #define FWD(DP, EX)                           \
     do {                                      \
         if (how.ws == 1) FWD_AS(DP, EX, 2, 1); \
         else if (how.rb == 2) FWD_AS(DP, EX, 2, 4); \
         else FWD_AS(DP, EX, 1, 4);            \
     } while (0)
-    ATTN_BY_DIM(FWD);
+        ATTN_BY_DIM(FWD);
 #undef FWD
 #undef FWD_AS
-    return hipGetLastError() == hipSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
+    });
 }
 
 int64_t attn_backward_workspace_bytes(const attn_problem *problem) {
