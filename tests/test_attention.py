@@ -397,15 +397,14 @@ def test_many_rows():
 
 
 def wide_case(seed):
-    """More workgroups than one launch takes: 65535 heads by 300 sequences,
-    most of them empty, over 64 rows."""
+    """More workgroups than one launch takes, nearly all with rows of their
+    own: 65535 heads by 300 sequences of one or two rows."""
     import torch
     from tiled_dense_gemm_matmul_amd import binding
     g = torch.Generator(device=device())
     g.manual_seed(seed)
-    T, H, d = 64, 65535, 4
-    cu = np.full(301, T, np.int32)
-    cu[:4] = 1, 20, 20, 57
+    cu = cu_of([1, 2] * 150, first=1)
+    T, H, d = int(cu[-1]) + 2, 65535, 4
     q, k, v, do = (torch.randn((T, H, d), generator=g, device=device()) for _ in range(4))
     return binding, cu, to_dev(cu), q, k, v, do
 

@@ -12,8 +12,9 @@
 namespace {
 
 // Calls launch(first, count) for `groups` workgroups of `threads` threads, in
-// slices of 2^31 threads: HIP refuses a grid of 2^32 or more.  Stops at a
-// slice that the runtime does not take.
+// slices of 2^31 threads: a grid has to stay below 2^32 (from there on it was
+// taken without an error and its last workgroups never ran).  Stops at a slice
+// that the runtime does not take.
 template <class F>
 int in_slices(int64_t groups, int threads, F launch) {
     const int64_t most = ((int64_t)1 << 31) / threads;
