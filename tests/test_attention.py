@@ -425,6 +425,52 @@ def test_more_workgroups_than_one_launch_takes():
         assert res["fails"] == 0, res
 
 
+def test_gradients_of_more_workgroups_than_one_launch_takes():
+    import torch
+    binding, cu, dcu, q, k, v, do = wide_case(2)
+    out, lse = binding.attention(q, k, v, cu_seqlens=dcu)
+    grads = binding.attention_backward(do, q, k, v, out, lse, cu_seqlens=dcu)
+    for at in range(0, q.shape[1], 8000):
+        some = slice(at, min(at + 8000, q.shape[1]))
+        part = [x[:, some].contiguous() for x in (do, q, k, v, out)]
+        got = binding.attention_backward(*part, lse[some].contiguous(), cu_seqlens=dcu)
+        assert all(torch.equal(a[:, some], b) for a, b in zip(grads, got))
+    some = slice(65532, 65535)
+    want = OA.attention_backward(*(x[:, some].cpu().numpy() for x in (do, q, k, v, out)), lse[some].cpu().numpy(), cu=cu)
+    for y, ref, err in zip(grads, want[:3], want[3:]):
+        res = OA.compare(y[:, some].cpu().numpy(), ref, err)
+        assert res["fails"] == 0, res
+
+
+def test_more_rows_than_one_launch_takes():
+    """2^28 and more rows over all heads, so that the kernel in front of the
+    backward pass needs slices too: sampled heads at both ends of the rows."""
+    import torch
+    from tiled_dense_gemm_matmul_amd import binding
+    T, H, d, w = 4100, 65535, 4, 2
+    g = torch.Generator(device=device())
+    g.manual_seed(3)
+    q, k, v, do = (torch.randn((T, H, d), generator=g, device=device()) for _ in range(4))
+    out, lse = binding.attention(q, k, v, window=w)
+    assert binding.load_library().attn_backward_workspace_bytes(
+        binding._PROBLEM.pack(0, 0, T, H, H, d, 1, w, 0.5)) == 4 * T * H
+    grads = binding.attention_backward(do, q, k, v, out, lse, window=w)
+    for heads in (slice(0, 2), slice(32767, 32769), slice(65533, 65535)):
+        for rows in (slice(0, 100), slice(T // 2 - 50, T // 2 + 50), slice(T - 100, T)):
+            host = [x[rows, heads].cpu().numpy() for x in (do, q, k, v, out)]
+            # rows whose neighbours are all here
+            keep = slice(0 if rows.start == 0 else w, 100 if rows.stop == T else 100 - w)
+            ro, _, eo, _ = OA.attention(*host[1:4], window=w)
+            res = OA.compare(host[4][keep], ro[keep], eo[keep])
+            assert res["fails"] == 0, res
+            want = OA.attention_backward(*host, lse[heads, rows].cpu().numpy(), window=w)
+            for y, ref, err in zip(grads, want[:3], want[3:]):
+                res = OA.compare(y[rows, heads].cpu().numpy()[keep], ref[keep], err[keep])
+                assert res["fails"] == 0, res
+    del q, k, v, do, out, grads
+    torch.cuda.empty_cache()
+
+
 def test_broadcast_views():
     """Key/value heads that are one tensor seen several times are read like
     any others; rows that are one row seen several times are refused, and so

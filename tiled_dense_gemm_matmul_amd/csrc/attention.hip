@@ -620,9 +620,9 @@ __device__ __forceinline__ float row_dots(const Rows<DP> &a, const Rows<DP> &b) 
 
 // delta [heads, tokens]: 16 lanes a row, which take the head's values in
 // 16-byte pieces.
-__global__ __launch_bounds__(256) void attention_delta(Problem p, Strided dout, Strided o, float *delta) {
+__global__ __launch_bounds__(256) void attention_delta(Problem p, Strided dout, Strided o, float *delta, int64_t first) {
     const int e = threadIdx.x & 15;
-    const int64_t row = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
+    const int64_t row = (first + blockIdx.x) * 16 + (threadIdx.x >> 4);
     if (row >= (int64_t)p.hq * p.tokens) return;
     const int t = (int)(row / p.hq), h = (int)(row - (int64_t)t * p.hq);
     const float *x = dout.p + t * dout.st + h * dout.sh, *y = o.p + t * o.st + h * o.sh;
@@ -906,8 +906,9 @@ __global__ __launch_bounds__(256, DP >= 96 && (RBQ == 2 || RBK == 2) ? 1 : 2) vo
                                                                                               int key_groups) {
     // the waves' turned rows, and in the end what they join
     __shared__ __align__(16) float shared[(DP <= kStagedWidth ? 8 : 4) * 16 * (DP + 4)];
-    if ((int)blockIdx.x < key_groups) backward_dkv<DP, EX, RBK, WS, OWN>(p, a, blockIdx.x, shared);
-    else backward_dq<DP, EX, RBQ, WS, OWN>(p, a, blockIdx.x - key_groups, shared);
+    const int id = p.first + (int)blockIdx.x;
+    if (id < key_groups) backward_dkv<DP, EX, RBK, WS, OWN>(p, a, id, shared);
+    else backward_dq<DP, EX, RBQ, WS, OWN>(p, a, id - key_groups, shared);
 }
 
 // --- host ---
@@ -1117,7 +1118,7 @@ int attn_backward(const attn_backward_args *args, void *stream) {
         if (in_range(res[i], a.lse, row_bytes, T, D) || in_range(res[i], a.p.cu_seqlens, cu_bytes, T, D))
             return GEMM_ERR_ALIAS;
     }
-    const Problem p = device_problem(a.p);
+    Problem p = device_problem(a.p);
     const Plan keys = own ? Plan{1, 4} : plan_keys(a.p), rows = own ? keys : plan_rows(a.p);
     // whole turns of the 8 XCDs, so that the second part's heads keep to theirs
     const int64_t nk = (tiles_of(a.p, keys.rows()) * HK + 7) / 8 * 8, grid = nk + tiles_of(a.p, rows.rows()) * HQ;
@@ -1126,12 +1127,18 @@ int attn_backward(const attn_backward_args *args, void *stream) {
                         strided(a.out, T, HQ),  strided(a.dq, T, HQ), strided(a.dk, T, HK), strided(a.dv, T, HK),
                         a.lse, static_cast<const float *>(a.workspace)};
     hipStream_t hs = static_cast<hipStream_t>(stream);
-    if (!own)
-        hipLaunchKernelGGL(attention_delta, dim3((unsigned)((HQ * T + 15) / 16)), dim3(256), 0, hs, p, b.dout, b.o,
-                           static_cast<float *>(a.workspace));
-#define BWD_AS(DP, EX, RBQ, RBK, WS, OWN)                                                                         \
-    hipLaunchKernelGGL((attention_bwd<DP, EX, RBQ, RBK, WS, OWN>), dim3((unsigned)grid), dim3(256), 0, hs, p, b, \
-                       (int)nk)
+    if (!own) {
+        // the main kernel reads what this one writes
+        st = in_slices((HQ * T + 15) / 16, 256, [&](int64_t first, unsigned count) {
+            hipLaunchKernelGGL(attention_delta, dim3(count), dim3(256), 0, hs, p, b.dout, b.o,
+                               static_cast<float *>(a.workspace), first);
+        });
+        if (st != GEMM_OK) return st;
+    }
+    return in_slices(grid, 256, [&](int64_t first, unsigned count) {
+        p.first = (int)first;
+#define BWD_AS(DP, EX, RBQ, RBK, WS, OWN) \
+    hipLaunchKernelGGL((attention_bwd<DP, EX, RBQ, RBK, WS, OWN>), dim3(count), dim3(256), 0, hs, p, b, (int)nk)
 #define BWD(DP, EX)                                              \
     do {                                                         \
         if (own) BWD_AS(DP, EX, 1, 1, 4, true);                  \
@@ -1140,10 +1147,10 @@ int attn_backward(const attn_backward_args *args, void *stream) {
         else if (rows.rb == 2) BWD_AS(DP, EX, 2, 1, 4, false);   \
         else BWD_AS(DP, EX, 1, 1, 4, false);                     \
     } while (0)
-    ATTN_BY_DIM(BWD);
+        ATTN_BY_DIM(BWD);
 #undef BWD
 #undef BWD_AS
-    return hipGetLastError() == hipSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
+    });
 }
 
 }  // extern "C"
