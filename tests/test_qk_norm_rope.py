@@ -164,6 +164,29 @@ def test_no_tokens():
     assert not grads[2].any() and not grads[3].any()
 
 
+def test_more_tokens_than_one_launch_takes():
+    """A wave a token, past 2^26 tokens: the last ones get the bits of a call
+    of their own."""
+    import torch
+    from tiled_dense_gemm_matmul_amd import binding
+    T, dev = (1 << 26) + 5, device()
+    q, k = (torch.randn((T, 1, 2), device=dev) for _ in range(2))
+    w, freq = torch.ones(2, device=dev), torch.full((1,), 0.25, device=dev)
+    pos = torch.arange(T, dtype=torch.int32, device=dev)
+    common = (w, w * 0.5)
+    out = [torch.full_like(q, SENTINEL) for _ in range(2)]
+    binding.qk_norm_rope(q, k, *common, pos, freq, q_out=out[0], k_out=out[1])
+    grads = binding.qk_norm_rope_backward(q, k, q, k, *common, pos, freq)
+    for a in (0, T // 2, T - 5000):
+        part = [x[a:a + 5000].contiguous() for x in (q, k)]
+        want = binding.qk_norm_rope(*part, *common, pos[a:a + 5000].contiguous(), freq)
+        back = binding.qk_norm_rope_backward(*part, *part, *common, pos[a:a + 5000].contiguous(), freq)
+        for i in range(2):
+            assert torch.equal(out[i][a:a + 5000], want[i]) and torch.equal(grads[i][a:a + 5000], back[i])
+    del q, k, out, grads
+    torch.cuda.empty_cache()
+
+
 def test_repeats_streams_and_graphs():
     import torch
     cases = [Case(7 + i, 700 + i, 6, 2, 64, 64) for i in range(2)]

@@ -28,6 +28,7 @@
 
 #include "attention.h"
 #include "gemm_fwd.h"
+#include "launch.h"
 #include "strided.h"
 
 namespace {
@@ -122,12 +123,14 @@ __device__ __forceinline__ float lanes_sum(float v) {
 }
 
 // NP groups of W pairs a lane, G lanes a head; a wave takes token
-// item / chunks and every (chunks * 64 / G)-th head from its chunk on.
+// item / chunks and every (chunks * 64 / G)-th head from its chunk on; `first`
+// workgroups lie in front of this launch's.
 template <int W, int G, int NP>
-__global__ __launch_bounds__(256) void qk_norm_rope_fwd(Norm n, Strided q, Strided k, Strided yq, Strided yk, int chunks) {
+__global__ __launch_bounds__(256) void qk_norm_rope_fwd(Norm n, Strided q, Strided k, Strided yq, Strided yk, int chunks,
+                                                        int64_t first) {
     constexpr int HW = 64 / G;  // heads at a time
     const int lane = threadIdx.x & 63, part = lane % G, slot = lane / G;
-    const int64_t item = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t item = (first + blockIdx.x) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int t = (int)(item / chunks), chunk = (int)(item % chunks);
     if (t >= n.tokens) return;
     const double pos = position(n, t);
@@ -442,13 +445,14 @@ int attn_qk_norm_rope(const attn_qk_norm_rope_args *args, void *stream) {
 #define FWD(W, G, NP)                                                                                              \
     do {                                                                                                            \
         const int chunks = chunks_of(T, HQ + HK, 64 / G);                                                           \
-        const int64_t grid = (T * chunks + 3) / 4;                                                                  \
-        hipLaunchKernelGGL((qk_norm_rope_fwd<W, G, NP>), dim3((unsigned)grid), dim3(256), 0, hs, n, sq, sk, oq, ok, \
-                           chunks);                                                                                 \
+        st = in_slices((T * chunks + 3) / 4, 256, [&](int64_t first, unsigned count) {                              \
+            hipLaunchKernelGGL((qk_norm_rope_fwd<W, G, NP>), dim3(count), dim3(256), 0, hs, n, sq, sk, oq, ok,      \
+                               chunks, first);                                                                      \
+        });                                                                                                         \
     } while (0)
     NORM_BY_LANES(FWD);
 #undef FWD
-    return hipGetLastError() == hipSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
+    return st;
 }
 
 int64_t attn_qk_norm_rope_workspace_bytes(int64_t tokens, int64_t head_dim) {
