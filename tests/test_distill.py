@@ -175,6 +175,31 @@ def test_degenerate_and_default_norm():
     assert not losses[:, 0].any() and not grad[0].any()
 
 
+@pytest.mark.parametrize("wide", [False, True])
+def test_more_rows_than_one_launch_takes(wide):
+    """A workgroup of 256 threads a row, past 2^24 rows: every array moves on
+    with the rows, and the last ones get the bits of a call of their own."""
+    import torch
+    from tiled_dense_gemm_matmul_amd import binding
+    S, V, K, dev = (1 << 24) + 5, 4, 3, device()
+    g = torch.Generator(device=dev)
+    g.manual_seed(4)
+    l = torch.randn((S, V), generator=g, device=dev)
+    t, ids = (torch.randint(-1, V, s, generator=g, device=dev, dtype=torch.int64 if wide else torch.int32)
+              for s in ((S,), (S, K)))
+    z = torch.randn((S, K), generator=g, device=dev).to(torch.float16 if wide else torch.float32)
+    dl = torch.full_like(l, float("nan"))
+    losses = torch.full((2, S), float("nan"), device=dev)
+    binding.distill_cross_entropy(l, t, ids, z, 2.0, 0.5, 0.1, 1e-3, 0.5, dlogits=dl, losses=losses)
+    for a in (0, S // 2 - 1000, S - 3000):
+        part = slice(a, a + 3000)
+        grad = torch.empty_like(l[part])
+        want = binding.distill_cross_entropy(*(x[part].contiguous() for x in (l, t, ids, z)), 2.0, 0.5, 0.1, 1e-3, 0.5,
+                                             dlogits=grad)
+        assert torch.equal(losses[:, part], want) and torch.equal(dl[part], grad)
+    assert bool(torch.isfinite(dl).all()) and bool(torch.isfinite(losses).all())
+
+
 def test_repeats_and_graphs():
     import torch
     from tiled_dense_gemm_matmul_amd import binding

@@ -38,6 +38,7 @@
 
 #include "distill.h"
 #include "gemm_fwd.h"
+#include "launch.h"
 #include "loss.h"
 
 namespace {
@@ -794,27 +795,31 @@ int loss_distill_cross_entropy(const loss_distill_args *args, void *stream) {
     hipStream_t st = static_cast<hipStream_t>(stream);
     const bool nt = S * V * 4 >= kStreamBytes;
     const bool same_phase = ((reinterpret_cast<uintptr_t>(p.logits) ^ reinterpret_cast<uintptr_t>(p.dlogits)) & 15) == 0;
-#define DISTILL_AS(NT, CAP, T1)                                                                              \
-    do {                                                                                                     \
-        if (nt) hipLaunchKernelGGL((distill_resident<NT, CAP, true, T1>), dim3(a.S), dim3(NT), 0, st, a);    \
-        else hipLaunchKernelGGL((distill_resident<NT, CAP, false, T1>), dim3(a.S), dim3(NT), 0, st, a);      \
-    } while (0)
-#define DISTILL(NT, CAP)                       \
-    do {                                       \
-        if (tau == 1.0f) DISTILL_AS(NT, CAP, true); \
-        else DISTILL_AS(NT, CAP, false);       \
-    } while (0)
-    if (!same_phase) hipLaunchKernelGGL((distill_stream<1024, false>), dim3(a.S), dim3(1024), 0, st, a);
-    else if (V > 1024 * 64) hipLaunchKernelGGL((distill_stream<1024, true>), dim3(a.S), dim3(1024), 0, st, a);
-    else if (V <= 256 * 16) DISTILL(256, 16);
-    else if (V <= 512 * 16) DISTILL(512, 16);
-    else if (V <= 512 * 32) DISTILL(512, 32);
-    else if (V <= 512 * 64) DISTILL(512, 64);
-    else if (V <= 512 * 100) DISTILL(512, 100);
-    else DISTILL(1024, 64);
-#undef DISTILL_AS
+    // a workgroup of `threads` threads a row; S stays the distance between the two rows of losses
+    auto launch = [&](void (*kernel)(Distill), int threads) {
+        return in_slices(S, threads, [&](int64_t first, unsigned count) {
+            Distill b = a;
+            b.logits += first * V;
+            b.grad += first * V;
+            if (p.targets) b.targets = static_cast<const char *>(p.targets) + first * (p.targets64 ? 8 : 4);
+            b.ids = static_cast<const char *>(p.teacher_ids) + first * K * (p.ids64 ? 8 : 4);
+            b.teacher = static_cast<const char *>(p.teacher_logits) + first * K * (p.teacher_f16 ? 2 : 4);
+            b.losses += first;
+            hipLaunchKernelGGL(kernel, dim3(count), dim3(threads), 0, st, b);
+        });
+    };
+#define DISTILL(NT, CAP)                                                                                              \
+    (tau == 1.0f ? launch(nt ? distill_resident<NT, CAP, true, true> : distill_resident<NT, CAP, false, true>, NT)    \
+                 : launch(nt ? distill_resident<NT, CAP, true, false> : distill_resident<NT, CAP, false, false>, NT))
+    if (!same_phase) return launch(distill_stream<1024, false>, 1024);
+    if (V > 1024 * 64) return launch(distill_stream<1024, true>, 1024);
+    if (V <= 256 * 16) return DISTILL(256, 16);
+    if (V <= 512 * 16) return DISTILL(512, 16);
+    if (V <= 512 * 32) return DISTILL(512, 32);
+    if (V <= 512 * 64) return DISTILL(512, 64);
+    if (V <= 512 * 100) return DISTILL(512, 100);
+    return DISTILL(1024, 64);
 #undef DISTILL
-    return hipGetLastError() == hipSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
 }
 
 }  // extern "C"
