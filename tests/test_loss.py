@@ -109,6 +109,25 @@ def test_ignored_and_degenerate():
     assert float(binding.sum_losses(torch.empty(0, device=dev)).item()) == 0.0
 
 
+def test_more_rows_than_one_launch_takes():
+    """A workgroup of 256 threads a row, past 2^24 rows: the last rows get the
+    bits of a call of their own."""
+    import torch
+    from tiled_dense_gemm_matmul_amd import binding
+    S, V, dev = (1 << 24) + 5, 4, device()
+    g = torch.Generator(device=dev)
+    g.manual_seed(4)
+    l = torch.randn((S, V), generator=g, device=dev)
+    t = torch.randint(-1, V, (S,), generator=g, device=dev, dtype=torch.int32)
+    parts = [slice(0, 3000), slice(S // 2 - 1000, S // 2 + 2000), slice(S - 3000, S)]
+    kept = [l[p].clone() for p in parts]
+    losses = binding.cross_entropy(l, t, 0.1, 1e-3, 0.5, losses=torch.full((S,), float("nan"), device=dev))
+    for p, own in zip(parts, kept):
+        want = binding.cross_entropy(own, t[p].contiguous(), 0.1, 1e-3, 0.5)
+        assert torch.equal(losses[p], want) and torch.equal(l[p], own)
+    assert bool(torch.isfinite(losses).all())
+
+
 def test_sum_losses_and_determinism():
     import torch
     from tiled_dense_gemm_matmul_amd import binding

@@ -699,37 +699,27 @@ int loss_cross_entropy(float *logits, const uint32_t *targets, float *losses, in
         return GEMM_ERR_ALIAS;
     if (S == 0) return GEMM_OK;
     hipStream_t st = static_cast<hipStream_t>(stream);
-    const int s = (int)S, v = (int)V;
+    const int v = (int)V;
     const bool vec = V % 4 == 0 && aligned(logits, 16);
     const bool stream_hint = S * V * 4 >= kStreamBytes;
+    // a workgroup of `threads` threads a row
+    auto launch = [&](void (*kernel)(float *, const uint32_t *, float *, int, float, float, float), int threads) {
+        return in_slices(S, threads, [&](int64_t first, unsigned count) {
+            hipLaunchKernelGGL(kernel, dim3(count), dim3(threads), 0, st, logits + first * V, targets + first,
+                               losses + first, v, alpha, beta, inv_norm);
+        });
+    };
     // a resident launch of NT threads holding CAP logits each
-#define LOSS_RESIDENT(NT, CAP)                                                                                   \
-    do {                                                                                                          \
-        if (stream_hint)                                                                                          \
-            hipLaunchKernelGGL((cross_entropy_resident<NT, CAP, true, true>), dim3(s), dim3(NT), 0, st, logits,  \
-                               targets, losses, v, alpha, beta, inv_norm);                                        \
-        else                                                                                                      \
-            hipLaunchKernelGGL((cross_entropy_resident<NT, CAP, true, false>), dim3(s), dim3(NT), 0, st, logits, \
-                               targets, losses, v, alpha, beta, inv_norm);                                        \
-    } while (0)
-    if (vec && V <= 256 * 16) {
-        LOSS_RESIDENT(256, 16);
-    } else if (vec && V <= 512 * 16) {
-        LOSS_RESIDENT(512, 16);
-    } else if (vec && V <= 512 * 32) {
-        LOSS_RESIDENT(512, 32);
-    } else if (vec && V <= 1024 * 32) {
-        LOSS_RESIDENT(1024, 32);
-    } else if (V <= 256 * 64 && !vec) {
-        hipLaunchKernelGGL((cross_entropy_resident<256, 64, false, false>), dim3(s), dim3(256), 0, st, logits, targets, losses, v, alpha, beta, inv_norm);
-    } else if (V <= 1024 * 64 && vec) {
-        if (stream_hint) hipLaunchKernelGGL((cross_entropy_resident<1024, 64, true, true>), dim3(s), dim3(1024), 0, st, logits, targets, losses, v, alpha, beta, inv_norm);
-        else hipLaunchKernelGGL((cross_entropy_resident<1024, 64, true, false>), dim3(s), dim3(1024), 0, st, logits, targets, losses, v, alpha, beta, inv_norm);
-    } else {
-        hipLaunchKernelGGL((cross_entropy_stream<1024>), dim3(s), dim3(1024), 0, st, logits, targets, losses, v, alpha, beta, inv_norm);
-    }
+#define LOSS_RESIDENT(NT, CAP) \
+    launch(stream_hint ? cross_entropy_resident<NT, CAP, true, true> : cross_entropy_resident<NT, CAP, true, false>, NT)
+    if (vec && V <= 256 * 16) return LOSS_RESIDENT(256, 16);
+    if (vec && V <= 512 * 16) return LOSS_RESIDENT(512, 16);
+    if (vec && V <= 512 * 32) return LOSS_RESIDENT(512, 32);
+    if (vec && V <= 1024 * 32) return LOSS_RESIDENT(1024, 32);
+    if (V <= 256 * 64 && !vec) return launch(cross_entropy_resident<256, 64, false, false>, 256);
+    if (V <= 1024 * 64 && vec) return LOSS_RESIDENT(1024, 64);
+    return launch(cross_entropy_stream<1024>, 1024);
 #undef LOSS_RESIDENT
-    return hipGetLastError() == hipSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
 }
 
 int loss_sum_losses(const float *losses, float *out, int64_t S, void *stream) {
