@@ -157,6 +157,43 @@ def test_many_sequences(causal, heads, longest):
     check(Case(4, lengths, tail=3, hq=heads, hk=heads, d=32, causal=causal), "300 sequences")
 
 
+@pytest.mark.parametrize("number", [512, 513, 4095, 4097, 9000])
+@pytest.mark.parametrize("causal", [True, False])
+def test_thousands_of_sequences(number, causal):
+    """On both sides of the number from which a tile's sequence is searched
+    for, and of those at which that search takes another look: sequences of no
+    rows to a few, runs of empty ones, and some of several tiles."""
+    r = np.random.default_rng(number)
+    lengths = r.choice(4, number)
+    lengths[100:300] = 0
+    lengths[[0, 63, 64, 301, number - 2]] = 50, 70, 33, 17, 40
+    lengths[number // 2] = 150
+    check(Case(number, [int(n) for n in lengths], first=5, tail=3, hq=2, hk=1, d=32, causal=causal), f"{number} sequences")
+
+
+@pytest.mark.parametrize("front", [True, False])
+def test_most_sequences(front):
+    """As many entries in cu_seqlens as a call takes, all but a few of them
+    empty, in front of the others or behind them: the bits of the few alone."""
+    import torch
+    from tiled_dense_gemm_matmul_amd import binding
+    g = torch.Generator(device=device())
+    g.manual_seed(6)
+    few = cu_of([300, 1, 40, 500, 97], first=10)
+    T = int(few[-1]) + 12
+    q, k, v, do = (torch.randn((T, 1, 32), generator=g, device=device()) for _ in range(4))
+    n = (1 << 24) - len(few)
+    cu = torch.full((n,), int(few[0] if front else few[-1]), dtype=torch.int32, device=device())
+    cu, few = torch.cat((cu, to_dev(few)) if front else (to_dev(few), cu)), to_dev(few)
+    assert cu.shape[0] - 1 == (1 << 24) - 1
+    out, lse = binding.attention(q, k, v, cu_seqlens=cu)
+    want = binding.attention(q, k, v, cu_seqlens=few)
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    grads = binding.attention_backward(do, q, k, v, out, lse, cu_seqlens=cu)
+    want = binding.attention_backward(do, q, k, v, out, lse, cu_seqlens=few)
+    assert all(torch.equal(a, b) for a, b in zip(grads, want))
+
+
 @pytest.mark.parametrize("gain,scale", [(6.0, None), (1.0, 2.5), (0.01, 1e-4)])
 def test_scales(gain, scale):
     """Scores from nearly equal to ones whose exponentials underflow."""

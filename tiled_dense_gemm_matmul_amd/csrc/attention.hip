@@ -292,6 +292,17 @@ __device__ __forceinline__ int lanes_sum(int v) {
 // last sequence starts when the chip is nearly done: dk and dv of 4 x 2048
 // rows, 2 heads of 128, took 910 us in a launch of their own; without a causal
 // mask, six documents of 1 to 1531 rows took 686 us by level, 560 by length.)
+//
+// That search looks at every sequence, 64 at a time, in every workgroup, which
+// with 2^24 sequences would take hours.  Past kScanned of them sequence b,
+// which starts at row c, has the numbers from c / TILE + b on, of which there
+// are enough up to the next sequence's, and b is found by a search in which
+// the wave looks at 64 bounds at once: two looks up to 4096 sequences, four up
+// to 2^24.  The tiles then come in the order of the sequences (12 heads of 64,
+// sequences of 100 rows, forward and backward: 200 of them 72 and 268 us by
+// level against 78 and 288, 400 of them 161 and 553 against 163 and 572, 1000
+// of them 430 and 1517 against 392 and 1409).
+constexpr int kScanned = 512;
 struct Tile {
     int s0, s1, r0, first, last;
 };
@@ -307,6 +318,26 @@ __device__ __forceinline__ Tile find_tile(const Problem &p, int x, bool back) {
         n = (t.s1 - t.s0 + TILE - 1) / TILE;
         if (x >= n) return t;
         level = n - 1 - x;
+    } else if (p.nseq > kScanned) {
+        const int lane = threadIdx.x & 63;
+        const int c0 = p.cu[0], c1 = p.cu[p.nseq];
+        auto bound = [&](int b) { return min(max(p.cu[b], 0), p.tokens); };
+        int lo = 0, hi = p.nseq, step;
+        do {  // of [lo, hi), the last sequence whose first number is x or less
+            step = (hi - lo + 63) / 64;
+            const int b = lo + lane * step;
+            const int below = __popcll(__ballot(b < hi && bound(min(b, hi)) / TILE + b <= x));
+            lo += max(below - 1, 0) * step;
+            hi = min(lo + step, hi);
+        } while (step > 1);
+        t.first = min(max(uniform(c0), 0), p.tokens);
+        t.last = max(t.first, min(uniform(c1), p.tokens));
+        t.s0 = uniform(bound(lo));
+        t.s1 = max(t.s0, min(uniform(p.cu[lo + 1]), p.tokens));
+        n = (t.s1 - t.s0 + TILE - 1) / TILE;
+        const int at = x - (t.s0 / TILE + lo);
+        if (at < 0 || at >= n) return t;
+        level = n - 1 - at;
     } else {
         const int lane = threadIdx.x & 63;
         const int c0 = p.cu[0], c1 = p.cu[p.nseq];
