@@ -46,7 +46,8 @@
  *
  * where pair p is (p, p + rotated / 2), or (2p, 2p + 1) when interleaved,
  * and y = n from `rotated` on.  The angle is reduced to a part of a
- * turn without loss for positions up to 2^53 in magnitude.
+ * turn without loss for positions up to 2^53 in magnitude, and its sine and
+ * cosine are good to fp32 relative to themselves.
  * The backward pass gives dx from dy, and the weight's gradient summed over
  * tokens and heads:
  *

@@ -133,7 +133,7 @@ def qk_norm_rope(x, weight, positions, inv_freq, eps=1e-6, interleaved=False):
     a, b = _pairs(d, 2 * angle.shape[1], interleaved)
     na, nb = n[..., a], n[..., b]
     y[..., a], y[..., b] = na * c - nb * s, nb * c + na * s
-    # the angle is a part of a turn in fp32 (pi u), sine and cosine 4 u, the combination 3 u
+    # sine and cosine 4 u and the correction by the angle's rest 2 u, the combination 3 u, and 3 u to spare
     err[..., a] = err[..., b] = (np.abs(na) + np.abs(nb)) * (rel + 12 * U)
     return y, err + 1e-37
 

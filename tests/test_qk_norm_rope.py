@@ -111,6 +111,48 @@ def test_far_positions(first, wide):
     verify(c, run(c), run_backward(c), f"from {first}")
 
 
+def turned(pos, freq):
+    """Cosine and sine of pos * freq in 64 bits, however near to their zeros:
+    the angle's distance from the nearest quarter turn is formed in 60 digits."""
+    from decimal import Decimal, getcontext
+    getcontext().prec = 60
+    quarter = Decimal("3.14159265358979323846264338327950288419716939937510582097494459") / 2
+    angle = Decimal(int(pos)) * Decimal(float(freq))
+    n = int((angle / quarter).to_integral_value())
+    rest = float(angle - n * quarter)
+    c, s = np.cos(rest), np.sin(rest)
+    return [(c, s), (-s, c), (-c, -s), (s, -c)][n % 4]
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_angles_near_quarter_turns(interleaved):
+    """Sine and cosine are good to fp32 relative to themselves, next to their
+    zeros too.  Heads hold (a, 0) in every pair, so a result is one product of
+    the normed a, which position 0 gives as it is: u = 2^-24 for that product,
+    4 u for sine and cosine, u each for the product and the sum that correct
+    them by the angle's rest, and one to spare."""
+    import torch
+    from tiled_dense_gemm_matmul_amd import binding
+    r, d = np.random.default_rng(8), 256
+    quarters = r.integers(1, 9, d // 2) * (np.pi / 2)
+    freq = (quarters + r.choice([-1.0, 1.0], d // 2) * 2.0 ** -r.integers(1, 20, d // 2)).astype(np.float32)
+    pos = np.array([0, 1, 3, -5, 1001, -123457, 2 ** 24 + 1, 10 ** 9 + 7, 2 ** 40 + 3], dtype=np.int64)
+    first, second = OA._pairs(d, d, interleaved)
+    x = np.zeros((len(pos), 1, d), np.float32)
+    x[:, :, first] = 1.0 + r.random(d // 2).astype(np.float32)
+    w = torch.ones(d, device=device())
+    y, _ = binding.qk_norm_rope(to_dev(x), to_dev(x), w, w, to_dev(pos), to_dev(freq), interleaved=interleaved)
+    y = y.cpu().numpy().astype(np.float64)[:, 0]
+    n = y[0, first]
+    assert not y[0, second].any()
+    want = np.array([[turned(p, f) for f in freq] for p in pos])
+    for name, got, ref in (("cosine", y[:, first] / n, want[..., 0]), ("sine", y[:, second] / n, want[..., 1])):
+        far = np.abs(got - ref) / np.maximum(np.abs(ref), 1e-300)
+        far[0] = 0.0 if name == "cosine" else np.where(got[0] == 0, 0.0, np.inf)
+        say(f"  {name}: off by up to {far.max() * 2 ** 24:.3g} u")
+        assert far.max() <= 8 * 2.0 ** -24, name
+
+
 @pytest.mark.parametrize("pad", [1, 2, 4])
 @pytest.mark.parametrize("interleaved", [False, True])
 def test_views_in_place_and_neighbours(pad, interleaved):

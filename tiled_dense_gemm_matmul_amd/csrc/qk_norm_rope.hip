@@ -13,8 +13,11 @@
 //  * The dimensions that are not rotated are paired in the same way and turned by
 //    the angle zero, so a head is one kind of pair throughout.
 //  * The angle pos * inv_freq is formed and reduced to a part of a turn in 64
-//    bits, with the rounding errors of both products carried along, so the
-//    part of a turn is good to fp32 at any position up to 2^53.
+//    bits, with the rounding errors of both products carried along.  Sine and
+//    cosine are taken of that part rounded to fp32, and turned by what the
+//    rounding left out (without that they were off by up to 1.1e-7, not
+//    3e-8, and by far more than an ulp near their zeros), so they are good to
+//    fp32 at any position up to 2^53.
 //  * The weight's gradient sums over all tokens and heads: fp32 over a token's
 //    heads in a lane, then 64 bits over tokens, lanes, waves and workgroups,
 //    each in a fixed order; a second small kernel adds the workgroups' parts.
@@ -108,7 +111,12 @@ __device__ __forceinline__ void turn(const Norm &n, double pos, int p, float &c,
         const double angle = pos * f, angle_low = fma(pos, f, -angle);
         const double turns = angle * kTurn;
         const double low = fma(angle, kTurn, -turns) + (angle * kTurnLow + angle_low * kTurn);
-        sincospif(2.0f * (float)((turns - rint(turns)) + low), &s, &c);
+        const double half_turns = 2.0 * ((turns - rint(turns)) + low);
+        const float x = (float)half_turns, rest = (float)((half_turns - (double)x) * M_PI);
+        sincospif(x, &s, &c);
+        const float s0 = s;
+        s = fmaf(c, rest, s);
+        c = fmaf(-s0, rest, c);
     }
 }
 __device__ __forceinline__ double position(const Norm &n, int t) {
