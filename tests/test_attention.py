@@ -560,6 +560,19 @@ def test_refusals_on_the_device():
         binding.attention(q.transpose(1, 2), q.transpose(1, 2), q.transpose(1, 2))
 
 
+def test_both_passes_refuse_a_problem_alike():
+    import torch
+    from tiled_dense_gemm_matmul_amd import binding
+    q = torch.randn((20, 2, 64), device=device())
+    k, v, out, lse = q.clone(), q.clone(), q.clone(), torch.zeros((2, 20), device=device())
+    for kw, width, status in (({"scale": 0.0}, 64, -4), ({"scale": float("inf")}, 64, -4), ({}, 62, -2)):
+        for run in (lambda x: binding.attention(*(t[..., :x] for t in (q, k, v)), **kw),
+                    lambda x: binding.attention_backward(*(t[..., :x] for t in (out, q, k, v, out)), lse, **kw)):
+            with pytest.raises(binding.GemmError) as e:
+                run(width)
+            assert e.value.status == status
+
+
 @pytest.mark.parametrize("heads", [2, 64])
 def test_repeated_calls_give_the_same_bits(heads):
     import torch

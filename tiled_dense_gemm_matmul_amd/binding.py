@@ -788,9 +788,8 @@ def attention_backward(dout, q, k, v, out, lse, cu_seqlens=None, causal=True, wi
     tdq = _heads(dq, "dq", shape_q, device)
     tdk = _heads(dk, "dk", shape_k, device)
     tdv = _heads(dv, "dv", shape_k, device)
-    nbytes = load_library().attn_backward_workspace_bytes(_PROBLEM.pack(*problem))
-    if nbytes < 0:
-        raise GemmError(-2, "attn_backward_workspace_bytes")
+    # less than 0 for a problem that the call below refuses, with the reason
+    nbytes = max(0, load_library().attn_backward_workspace_bytes(_PROBLEM.pack(*problem)))
     # scratch of this call's own: two captured graphs share nothing
     scratch = q.new_empty((nbytes // 4,)) if nbytes else None
     _call_packed("attn_backward",
