@@ -89,7 +89,9 @@ typedef struct attn_tensor {
  * pass. */
 typedef struct attn_problem {
     const int32_t *cu_seqlens; /* [num_seqs + 1] device array, or NULL: one sequence of all tokens */
-    int64_t num_seqs;          /* ignored when cu_seqlens is NULL */
+    int64_t num_seqs;          /* ignored when cu_seqlens is NULL; tokens / num_seqs, empty sequences
+                                  included, is what the host takes for their length when it deals out
+                                  the work (speed only) */
     int64_t tokens;
     int64_t q_heads;
     int64_t kv_heads;          /* divides q_heads */

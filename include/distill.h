@@ -18,6 +18,10 @@
  * [0, V) is padding: both losses 0 and a zero gradient row.  targets may be
  * NULL when mix is 1: then every row counts and its ce is 0.
  *
+ * Probabilities e^x, x <= 0 the logit's distance from the row's maximum (over
+ * tau), are formed in fp32 with x log2(e) rounded once: each is off by about
+ * |x| 2^-24 of itself.
+ *
  * Index arrays hold int32 or int64, teacher logits fp32 or binary16.  Rows
  * of up to 65536 logits are read once when logits and dlogits lie at the same
  * offset from a 16-byte boundary (they do when one call's arrays are both

@@ -8,11 +8,12 @@
 // is 10 D flops, but then dq or dk and dv would be summed by atomics, whose
 // order changes results, or kept as [tokens, tokens] arrays.)
 //
-//  * No operand passes through LDS.  A wave holds 16 or 32 rows (or keys) in
-//    registers and walks over blocks of 16 of the other side, whose operands
-//    it loads from memory straight into the registers that the MFMA reads,
-//    each under one product or more before its own (a load of 4 KiB takes
-//    place of 32 to 64 MFMAs' 1024 to 2048 cycles).
+//  * A wave holds 16 or 32 rows (or keys) in registers and walks over blocks
+//    of 16 of the other side, whose operands it loads from memory straight
+//    into the registers that the MFMA reads, each under one product or more
+//    before its own (a load of 4 KiB takes place of 32 to 64 MFMAs' 1024 to
+//    2048 cycles).  Only the backward pass over heads of up to 64 takes
+//    operands through LDS, where it turns them for their second product.
 //  * The probabilities never leave the registers either.  A 16 x 16 product
 //    leaves lane (g, m) = (lane / 16, lane % 16) with its rows 4g .. 4g + 3
 //    of column m.  That is the B operand of the next product when its
@@ -1012,7 +1013,14 @@ int64_t tiles_of(const attn_problem &p, int64_t tile) {
 //    forward 26 us against 38 joined; backward 110 against 156; 16 x 512 rows:
 //    backward 231 against 261).
 // `many` is the number of 32-row tiles from which two blocks win, `most` the
-// average sequence length (all that the host knows) that counts as short.
+// average sequence length (all that the host knows) that counts as short;
+// from 512 tiles of 128 rows on unjoined waves fill the chip.  Both sides of
+// each bound, causal, heads of 64 unless said otherwise, us:
+//  * short sequences, forward, unjoined against joined: 64 x 128 rows with 4
+//    heads (256 tiles) 14.9 to 14.9, with 8 (512) 22.0 to 27.5; 12 heads of 32 x
+//    256 rows 42.2 to 51.4, of 16 x 512 72 to 74, of 8 x 1024 133 to 119.
+//    Backward: 12 heads of 16 x 512 231 to 263, of 8 x 1024 396 to 423, and of
+//    width 32 131 to 137 and 226 to 219.
 struct Plan {
     int rb, ws;
     int64_t rows() const { return 16 * rb * (4 / ws); }
@@ -1025,9 +1033,22 @@ Plan plan(const attn_problem &p, int64_t heads, int64_t many, int64_t most) {
     if (average_length(p) <= most && p.tokens / 128 * heads >= 512) return {2, 1};
     return {p.tokens / 32 * heads >= many ? 2 : 1, 4};
 }
+// 2048 rows of 8 heads (512 tiles) 51.3 us with one block, 53.2 with two; 4096
+// of 8 (1024) 158 and 163, of 12 (1536) 234 and 208.  Heads of 128: 88 and 97,
+// 308 and 273, 457 and 397; without a causal mask 8 heads of 64 gain from 512
+// tiles on (80 and 72).
 Plan plan_forward(const attn_problem &p) { return plan(p, p.q_heads, 1024, 256); }
 // Keys of the backward pass: a tile of few keys takes all rows of the group's
 // heads, so two blocks pay from fewer tiles where no mask makes tiles uneven.
+// With 8 heads, one block and two, us:
+//  * causal, 64 wide (320 tiles): 1024 rows (256 tiles) 47 and 63, 1280 (320)
+//    70 and 69, 1536 (384) 98 and 84.  2 shared heads gain only from about
+//    512: 5120 rows (320) 731 and 873, 4 of them at 4096 (512) 928 and 912;
+//  * causal, 128 wide (256 tiles): 768 rows (192) 64 and 62, 1024 (256) 100 and
+//    89; 2 shared heads 2816 rows (176) 525 and 728, 4096 (256) 1063 and 1057;
+//  * no mask (192 tiles): 64 wide 768 rows (192) 45 and 50, 1024 (256) 84 and
+//    64, 1280 107 and 140, 16 heads of 1024 (512) 136 and 124; 2 shared heads of
+//    128 at 2816 rows (176) 975 and 1014, at 4096 (256) 1976 and 1871.
 Plan plan_keys(const attn_problem &p) {
     return plan(p, p.kv_heads, !p.causal ? 192 : p.head_dim > 64 ? 256 : 320, 512);
 }
