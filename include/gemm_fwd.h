@@ -67,7 +67,9 @@
  * the 16-byte vector loads, "Önemli Optimizasyonlar" §1):
  *   0 <= M < 2^31;  0 <= K < 2^21;  0 <= N < 2^21;  K % 4 == 0;  N % 4 == 0;
  *   fp32 arrays 16-byte aligned; binary16 W 8-byte aligned;
- *   Y overlaps none of the inputs (R included).
+ *   Y overlaps none of the inputs (R included);
+ *   the output's tiles take fewer than 2^32 threads (GEMM_ERR_SHAPE; with the
+ *   smallest tiles, 16 rows and 256 threads, M from 2^28 on can exceed it).
  * Degenerate shapes: M == 0 or N == 0 enqueues nothing and returns GEMM_OK;
  * K == 0 gives Y = R (or Y = 0 without a residual).  The pointer of an array
  * with no elements (e.g. X and W when K == 0) may be NULL.

@@ -501,3 +501,18 @@ def test_activation_exports_and_validation(lib):
     assert gb(n=-1) == SHAPE and gb(x=None) == NULL and gb(d=Y + 1) == ALIGN and gb(d=W + 4) == ALIAS
     gi = lambda x=X, p=Y, n=64: lib.act_gelu_inplace(x, p, n, None)
     assert gi(x=None) == NULL and gi(p=X) == ALIAS and gi(p=X + 8) == ALIAS and gi(n=0) == 0
+
+
+def test_grids_of_two_to_the_32_threads_are_refused(lib):
+    """The runtime takes them without an error, and their last workgroups
+    never run.  Addresses far enough apart for the arrays."""
+    from tiled_dense_gemm_matmul_amd import binding
+    shape = _status("GEMM_ERR_SHAPE")
+    x, w, r, y = (1 << s for s in (52, 30, 53, 54))
+    M, K, N = (1 << 31) - 1, 4, 1024
+    for config in [-1, *range(lib.gemm_num_configs())]:
+        o = binding.opts(config)
+        if config < 0 or not lib.gemm_config_name(config).decode().count("_ks"):
+            assert lib.gemm_fwd_ex(x, w, r, y, M, K, N, 0, o, None) == shape, config
+    assert lib.gemm_fwd(x, w, None, y, M, K, N, 0, None) == shape
+    assert lib.gemm_matmul_t(x, w, y, M, N, K, 0, None) == shape

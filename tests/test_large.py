@@ -78,3 +78,19 @@ def test_weight_gradient_contraction_past_4gib():
     res = oracle.compare(dW.cpu().numpy(), ref, scale, oracle.TOL_W32)
     say(f"  max err/tol {res['max_ratio']:.3g}, fails {res['fails']} of {res['n']}")
     assert res["fails"] == 0, res
+
+
+def test_empty_contraction_past_one_launch():
+    """K == 0 fills Y with R or zero, also past 2^32 values (17 GB)."""
+    import torch
+    from tiled_dense_gemm_matmul_amd import binding
+    M, N = (1 << 20) + 37, 4100
+    x, w = torch.empty((M, 0), device=device()), torch.empty((0, N), device=device())
+    y = torch.full((M, N), float("nan"), device=device())
+    binding.matmul(x, w, out=y)
+    assert not y.any()
+    r = _randn((M, N), 9)
+    binding.matmul(x, w, R=r, out=y)
+    assert torch.equal(y, r)
+    del y, r
+    torch.cuda.empty_cache()

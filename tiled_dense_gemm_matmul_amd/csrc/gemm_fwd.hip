@@ -1078,8 +1078,8 @@ __global__ __launch_bounds__(C::NT, C::MINB) void gemm_fwd_kernel(Params p) {
 
 // Y = R (or 0) when K == 0: the contraction is empty.
 __global__ void fill_k0_kernel(const float *R, float *Y, int64_t count) {
-    const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    if (i < count) Y[i] = R ? R[i] : 0.0f;
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < count; i += (int64_t)gridDim.x * blockDim.x)
+        Y[i] = R ? R[i] : 0.0f;
 }
 
 // ---------------------------------------------------------------------------
@@ -1782,6 +1782,16 @@ int resolve(const ConfigEntry *table, const Opts &o, int64_t M, int64_t N, Pick 
     return GEMM_OK;
 }
 
+// A grid has to stay below 2^32 threads: from there on it was taken without an
+// error and its last workgroups never ran.
+constexpr int64_t kMaxThreads = (int64_t)1 << 32;
+
+// Workgroups of 256 threads that fill an array of `count` values.
+unsigned fill_groups(int64_t count) {
+    const int64_t groups = ceil_div(count, 256), most = kMaxThreads / 512;
+    return (unsigned)(groups < most ? groups : most);
+}
+
 int run(bool swiglu, const float *A, const float *U, const void *W, bool w16, const float *R, float *Y,
         int64_t M, int64_t K, int64_t N, const Opts &o, void *stream) {
     const int64_t lim = (int64_t)1 << 31;
@@ -1817,7 +1827,7 @@ int run(bool swiglu, const float *A, const float *U, const void *W, bool w16, co
     hipStream_t s = static_cast<hipStream_t>(stream);
     if (K == 0) {
         const int64_t count = M * N;
-        hipExtLaunchKernelGGL(fill_k0_kernel, dim3((unsigned)ceil_div(count, 256)), dim3(256), 0, s,
+        hipExtLaunchKernelGGL(fill_k0_kernel, dim3(fill_groups(count)), dim3(256), 0, s,
                               static_cast<hipEvent_t>(o.start), static_cast<hipEvent_t>(o.stop), 0, R, Y, count);
         return hipGetLastError() == hipSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
     }
@@ -1842,7 +1852,7 @@ int run(bool swiglu, const float *A, const float *U, const void *W, bool w16, co
     p.group_m = p.tiles_m < 4 ? p.tiles_m : 4;
     p.kchunk = (int)(ceil_div(ceil_div(K, e.ks), e.bk) * e.bk);
     const int64_t blocks = (int64_t)p.tiles_m * p.tiles_n * e.ks;
-    if (blocks >= lim) return GEMM_ERR_SHAPE;
+    if (blocks * e.nt >= kMaxThreads) return GEMM_ERR_SHAPE;
     KernelFn fn = e.fn[swiglu ? 1 : 0][w16 ? 1 : 0][R ? 1 : 0];
     if (!fn) return GEMM_ERR_CONFIG;
     // with NULL events this is a plain launch; otherwise the events take the
@@ -1903,16 +1913,16 @@ int run_bwd(int op, bool swiglu, const float *A, const float *U, const float *B,
     hipEvent_t e0 = static_cast<hipEvent_t>(o.start), e1 = static_cast<hipEvent_t>(o.stop);
     if (kk == 0 && fused) {
         // dH = 0: both gradients are zero
-        hipExtLaunchKernelGGL(fill_k0_kernel, dim3((unsigned)ceil_div(km * kn2, 256)), dim3(256), 0, s, e0,
+        hipExtLaunchKernelGGL(fill_k0_kernel, dim3(fill_groups(km * kn2)), dim3(256), 0, s, e0,
                               nullptr, 0, nullptr, Y, km * kn2);
-        hipExtLaunchKernelGGL(fill_k0_kernel, dim3((unsigned)ceil_div(km * kn2, 256)), dim3(256), 0, s, nullptr,
+        hipExtLaunchKernelGGL(fill_k0_kernel, dim3(fill_groups(km * kn2)), dim3(256), 0, s, nullptr,
                               e1, 0, nullptr, Y2, km * kn2);
         return hipGetLastError() == hipSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
     }
     if (kk == 0) {
         if (acc) return GEMM_OK;  // nothing to add
         const int64_t count = km * kn2;
-        hipExtLaunchKernelGGL(fill_k0_kernel, dim3((unsigned)ceil_div(count, 256)), dim3(256), 0, s, e0, e1, 0,
+        hipExtLaunchKernelGGL(fill_k0_kernel, dim3(fill_groups(count)), dim3(256), 0, s, e0, e1, 0,
                               nullptr, Y, count);
         return hipGetLastError() == hipSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
     }
@@ -1931,7 +1941,7 @@ int run_bwd(int op, bool swiglu, const float *A, const float *U, const float *B,
     p.group_m = p.tiles_m < 4 ? p.tiles_m : 4;
     p.kchunk = (int)(ceil_div(ceil_div(kk, e.ks), e.bk) * e.bk);
     const int64_t blocks = (int64_t)p.tiles_m * p.tiles_n * e.ks;
-    if (blocks >= lim) return GEMM_ERR_SHAPE;
+    if (blocks * e.nt >= kMaxThreads) return GEMM_ERR_SHAPE;
     KernelFn fn = e.fn[op == kOpTN ? 1 : 0][swiglu ? 1 : 0][acc ? 1 : 0];
     if (fn == nullptr) return GEMM_ERR_DTYPE;
     hipExtLaunchKernelGGL(fn, dim3((unsigned)blocks), dim3(e.nt), 0, s, e0, e1, 0, p);
