@@ -171,6 +171,16 @@ def test_thousands_of_sequences(number, causal):
     check(Case(number, [int(n) for n in lengths], first=5, tail=3, hq=2, hk=1, d=32, causal=causal), f"{number} sequences")
 
 
+@pytest.mark.parametrize("heads,longest", [(48, 40), (48, 200), (3, 400)])
+@pytest.mark.parametrize("causal,window", [(True, 0), (False, 30)])
+def test_hundreds_of_sequences_on_longer_tiles(heads, longest, causal, window):
+    """The same with tiles of 32 and 128 rows."""
+    r = np.random.default_rng(longest)
+    lengths = [int(n) for n in r.integers(0, longest, 560) * (r.random(560) < (0.9 if longest == 40 else 0.1))]
+    check(Case(longest, lengths, first=2, tail=70, hq=heads, hk=heads, d=32, causal=causal, window=window),
+          f"560 sequences, {heads} heads")
+
+
 @pytest.mark.parametrize("front", [True, False])
 def test_most_sequences(front):
     """As many entries in cu_seqlens as a call takes, all but a few of them
@@ -360,6 +370,20 @@ def test_writes_stay_inside(heads):
     c.q = q
     got, _ = call(c, out=q)
     assert got is q and torch.equal(q, plain[0])
+
+
+@pytest.mark.parametrize("hq,hk,tokens", [(4, 2, 300), (64, 16, 700), (128, 128, 600)])
+def test_out_over_q_inside_the_projection(hq, hk, tokens):
+    """out over the query columns of the buffer that holds the keys and values too."""
+    import torch
+    lengths = [tokens] if hq < 100 else [tokens // 6] * 6
+    c = Case(hq, lengths, tail=5, hq=hq, hk=hk, d=64)
+    want = call(c)
+    keys, values = c.k.clone(), c.v.clone()
+    got = call(c, out=c.q)
+    assert got[0] is c.q and torch.equal(c.q, want[0]) and torch.equal(got[1], want[1])
+    for kept, now in ((keys, c.k), (values, c.v)):
+        assert torch.equal(kept[:tokens], now[:tokens]) and bool(now[tokens:].isnan().all())
 
 
 def test_heads_of_three_tensors_in_turn():

@@ -80,6 +80,17 @@ def test_teachers(K, params):
     check(c, losses, grad, params, 0.5, f"K={K}")
 
 
+@pytest.mark.parametrize("V", [70003, 65537])
+@pytest.mark.parametrize("K", [200, 1024])
+def test_wide_teachers_of_long_rows(V, K):
+    """Rows that are read twice, in place and at every alignment a row of odd
+    length comes to, with more teacher entries than waves."""
+    c = case(V + K, 6, V, K, half=K == 200)
+    for params in PARAMS[1:3]:
+        losses, grad = run(c, *params, 0.5)
+        check(c, losses, grad, params, 0.5, f"V={V} K={K} {params}")
+
+
 @pytest.mark.parametrize("off,apart_off", [(1, None), (2, None), (3, None), (0, 0), (1, 1), (0, 1), (3, 2)])
 def test_alignment(off, apart_off):
     """Logits at every offset from a 16-byte boundary, the gradient over them,
