@@ -8,6 +8,7 @@ Public Python surface (a thin binding over the C-ABI library libgemmfwd.so):
     attention(q, k, v, ...), attention_backward(...)    attention over packed sequences
     qk_norm_rope(...), qk_norm_rope_backward(...)       norm and rotation of query and key heads
     distill_cross_entropy(...)                          cross-entropy mixed with distillation
+    block_norm(...), block_norm_backward(...)           norms around a block, its gate and the residual stream
 
 W may be float32 or float16 ([K, N] row-major); activations are float32.
 The binding (and with it torch and the HIP library) is loaded on first use, so
@@ -18,6 +19,7 @@ _BINDING_NAMES = {
     "status_string", "library_path", "load_library", "GemmError", "kernel_config",
     "num_configs", "config_name",
     "attention", "attention_backward", "qk_norm_rope", "qk_norm_rope_backward", "distill_cross_entropy",
+    "block_norm", "block_norm_backward",
     "GEMM_FLAG_W_F16", "GEMM_W_F32", "GEMM_W_F16",
 }
 

@@ -32,6 +32,7 @@ EXPORTED = (
     "act_ffn_gelu_backward", "act_gelu_inplace", "attn_forward", "attn_backward",
     "attn_backward_workspace_bytes", "attn_qk_norm_rope",
     "attn_qk_norm_rope_backward", "attn_qk_norm_rope_workspace_bytes",
+    "block_norm", "block_norm_backward", "block_norm_backward_workspace_bytes",
     "gemm_timing_event_create", "gemm_timing_event_record", "gemm_timing_elapsed_ms", "gemm_timing_event_destroy",
 )
 
@@ -133,13 +134,15 @@ def _open(path):
     lib.act_gelu_inplace.argtypes = [p, p, i64, p]
     lib.act_gelu_inplace.restype = c_int
     for name in ("attn_forward", "attn_backward", "attn_qk_norm_rope", "attn_qk_norm_rope_backward",
-                 "loss_distill_cross_entropy"):
+                 "loss_distill_cross_entropy", "block_norm", "block_norm_backward"):
         getattr(lib, name).argtypes = [ctypes.c_char_p, p]  # the packed argument struct, the stream
         getattr(lib, name).restype = c_int
     lib.attn_backward_workspace_bytes.argtypes = [ctypes.c_char_p]
     lib.attn_backward_workspace_bytes.restype = i64
     lib.attn_qk_norm_rope_workspace_bytes.argtypes = [i64, i64]
     lib.attn_qk_norm_rope_workspace_bytes.restype = i64
+    lib.block_norm_backward_workspace_bytes.argtypes = [ctypes.c_char_p]
+    lib.block_norm_backward_workspace_bytes.restype = i64
     lib.gemm_timing_event_create.argtypes = [ctypes.POINTER(ctypes.c_void_p)]
     lib.gemm_timing_event_create.restype = c_int
     lib.gemm_timing_event_record.argtypes = [p, p]
@@ -709,6 +712,18 @@ def _row_values(t, name, shape, device):
     return t.data_ptr()
 
 
+def _cu_seqlens(cu_seqlens, device):
+    """(pointer, sequences) of the sequences' bounds; (0, 0) for None."""
+    if cu_seqlens is None:
+        return 0, 0
+    if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 or cu_seqlens.device != device \
+            or cu_seqlens.shape[0] < 1 or not cu_seqlens.is_contiguous():
+        raise ValueError(f"cu_seqlens must be a contiguous 1-D tensor of at least one entry on {device}")
+    if cu_seqlens.dtype != torch.int32:
+        raise TypeError(f"cu_seqlens must be int32, got {cu_seqlens.dtype}")
+    return cu_seqlens.data_ptr(), cu_seqlens.shape[0] - 1
+
+
 def _attn_problem(q, k, cu_seqlens, causal, window, scale):
     """The fields of attn_problem, and the shapes of q and of k and v."""
     for name, t in (("q", q), ("k", k)):
@@ -718,14 +733,7 @@ def _attn_problem(q, k, cu_seqlens, causal, window, scale):
     hkv = k.shape[1]
     if hq < 1 or hkv < 1 or hq % hkv:
         raise ValueError(f"{hq} query heads do not share {hkv} key/value heads evenly")
-    cu, nseq = 0, 0
-    if cu_seqlens is not None:
-        if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 or cu_seqlens.device != q.device \
-                or cu_seqlens.shape[0] < 1 or not cu_seqlens.is_contiguous():
-            raise ValueError(f"cu_seqlens must be a contiguous 1-D tensor of at least one entry on {q.device}")
-        if cu_seqlens.dtype != torch.int32:
-            raise TypeError(f"cu_seqlens must be int32, got {cu_seqlens.dtype}")
-        cu, nseq = cu_seqlens.data_ptr(), cu_seqlens.shape[0] - 1
+    cu, nseq = _cu_seqlens(cu_seqlens, q.device)
     if window < 0:
         raise ValueError(f"window must not be negative, got {window}")
     if scale is None:
@@ -888,3 +896,140 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, positions, i
                  _NORM_BACKWARD_ARGS.pack(*fields, *tgq, *tgk, *tq, *tk, *tdq, *tdk, pqw, pkw, scratch.data_ptr(),
                                           nbytes), device)
     return dq, dk, dq_weight, dk_weight
+
+
+# --- norms around a block (include/block_norm.h) ---
+
+_BLOCK_ARGS = struct.Struct("=8q3d 8q")
+_BLOCK_PROBLEM = struct.Struct("=8q3d")
+_BLOCK_BACKWARD_ARGS = struct.Struct("=8q3d 12q 3q 2q")
+
+
+def _rows(t, name, shape, device):
+    """(pointer, row stride) of the [tokens, width] tensor t; (0, 0) for None."""
+    if t is None:
+        return 0, 0
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda or t.device != device:
+        raise ValueError(f"{name} must live on {device if device.type == 'cuda' else 'a GPU'}, got {t.device}")
+    if t.dtype is not torch.float32:
+        raise TypeError(f"{name} must be float32, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    st, sd = t.stride()
+    if sd != 1 and shape[1] > 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+    return t.data_ptr(), st
+
+
+def _block_problem(rows, name, pre_weight, post_weight, gate, residual_scale, block_scale, cu_seqlens, eps):
+    """The fields of block_norm_problem for the [tokens, width] tensor `rows`, and the gate's shape."""
+    if not isinstance(rows, torch.Tensor) or rows.dim() != 2:
+        raise TypeError(f"{name} must be a 2-D torch.Tensor [tokens, width]")
+    device = rows.device
+    tokens, width = rows.shape
+    cu, nseq = _cu_seqlens(cu_seqlens, device)
+    by_seq, shape_gate, pg = 0, None, 0
+    if gate is not None:
+        if not isinstance(gate, torch.Tensor) or gate.dim() not in (1, 2):
+            raise TypeError("gate must be a torch.Tensor [width] or [sequences, width]")
+        by_seq = gate.dim() - 1
+        if by_seq and cu_seqlens is None:
+            raise ValueError("a gate for each sequence needs cu_seqlens")
+        shape_gate = torch.Size((nseq, width) if by_seq else (width,))
+        if gate.shape != shape_gate or gate.device != device or gate.dtype != torch.float32 \
+                or not gate.is_contiguous():
+            raise ValueError(f"gate must be a contiguous float32 tensor of shape {tuple(shape_gate)} on {device}")
+        pg = gate.data_ptr()
+    fields = (0 if pre_weight is None else _vector(pre_weight, "pre_weight", device, width),
+              0 if post_weight is None else _vector(post_weight, "post_weight", device, width), pg, by_seq, cu, nseq,
+              tokens, width, float(residual_scale), float(block_scale), float(eps))
+    return fields, shape_gate
+
+
+def block_norm(x, y=None, pre_weight=None, post_weight=None, gate=None, residual_scale=1.0, block_scale=1.0,
+               cu_seqlens=None, eps=1e-6, x_out=None, h_out=None):
+    """The norm behind a block, its gate, the update of the residual stream
+    and the norm in front of the next block, in one pass:
+
+        n = norm(y) * post_weight                 (y without post_weight)
+        x_out = residual_scale * x + block_scale * gate * n
+        h = norm(x_out) * pre_weight              (None without pre_weight)
+
+    where norm divides a row by its root mean square.  x, the residual stream,
+    and y, the block's output, are [tokens, width] float32 with contiguous
+    rows at any stride, width up to 8192.  gate is [width], or [sequences,
+    width] with cu_seqlens (int32 [sequences + 1] on the device, as for
+    attention; rows of no sequence get x_out and h 0), or None for 1.  Without
+    y (in front of the first block, behind the last) x_out is x and only the
+    norm is formed.  x_out and h_out may each be x or y.
+    Returns (x_out, h)."""
+    fields, _ = _block_problem(x, "x", pre_weight, post_weight, gate, residual_scale, block_scale, cu_seqlens, eps)
+    device, shape = x.device, x.shape
+    if y is None and (pre_weight is None or x_out is not None or post_weight is not None or gate is not None
+                      or residual_scale != 1 or block_scale != 1):
+        raise ValueError("without y there is only the norm: pre_weight, and no x_out, post_weight, gate or scale")
+    if pre_weight is None and h_out is not None:
+        raise ValueError("h_out needs pre_weight")
+    tx, ty = _rows(x, "x", shape, device), _rows(y, "y", shape, device)
+    if y is not None and x_out is None:
+        x_out = x.new_empty(shape)
+    if pre_weight is not None and h_out is None:
+        h_out = x.new_empty(shape)
+    _call_packed("block_norm", _BLOCK_ARGS.pack(*fields, *tx, *ty, *_rows(x_out, "x_out", shape, device),
+                                                *_rows(h_out, "h_out", shape, device)), device)
+    return x if y is None else x_out, h_out
+
+
+def block_norm_backward(dx_out, dh, x_out, y=None, pre_weight=None, post_weight=None, gate=None, residual_scale=1.0,
+                        block_scale=1.0, cu_seqlens=None, eps=1e-6, dx=None, dy=None, dpre_weight=None,
+                        dpost_weight=None, dgate=None):
+    """Gradients of block_norm, from those of its results, dx_out (of the
+    residual stream, from what reads it later; None counts as zero) and dh,
+    and from x_out and y.  Other arguments as for block_norm; dx and dy may
+    each be dx_out, dh, x_out or y.
+    Returns (dx, dy, dpre_weight, dpost_weight, dgate), None for what the call
+    has none of."""
+    fields, shape_gate = _block_problem(x_out, "x_out", pre_weight, post_weight, gate, residual_scale, block_scale,
+                                        cu_seqlens, eps)
+    device, shape = x_out.device, x_out.shape
+    if y is None and (pre_weight is None or dy is not None or post_weight is not None or gate is not None
+                      or residual_scale != 1 or block_scale != 1):
+        raise ValueError("without y there is only the norm: pre_weight, and no dy, post_weight, gate or scale")
+    if (dh is None) != (pre_weight is None):
+        raise ValueError("dh and pre_weight belong together")
+    if dx_out is None and pre_weight is None:
+        raise ValueError("without pre_weight there is dx_out")
+    if (pre_weight is None and dpre_weight is not None) or (post_weight is None and dpost_weight is not None) \
+            or (gate is None and dgate is not None):
+        raise ValueError("dpre_weight, dpost_weight and dgate need pre_weight, post_weight and gate")
+    inputs = (*_rows(dx_out, "dx_out", shape, device), *_rows(dh, "dh", shape, device),
+              *_rows(x_out, "x_out", shape, device), *_rows(y, "y", shape, device))
+    new = x_out.new_empty
+    if dx is None:
+        dx = new(shape)
+    if dy is None and y is not None:
+        dy = new(shape)
+    width = shape[1]
+    if pre_weight is not None and dpre_weight is None:
+        dpre_weight = new((width,))
+    if post_weight is not None and dpost_weight is None:
+        dpost_weight = new((width,))
+    if gate is not None:
+        dgate = new(shape_gate) if dgate is None else dgate
+        if not isinstance(dgate, torch.Tensor) or dgate.shape != shape_gate or dgate.device != device \
+                or dgate.dtype != torch.float32 or not dgate.is_contiguous():
+            raise ValueError(f"dgate must be a contiguous float32 tensor of shape {tuple(shape_gate)} on {device}")
+    outputs = (*_rows(dx, "dx", shape, device), *_rows(dy, "dy", shape, device),
+               0 if pre_weight is None else _vector(dpre_weight, "dpre_weight", device, width),
+               0 if post_weight is None else _vector(dpost_weight, "dpost_weight", device, width),
+               0 if gate is None else dgate.data_ptr())
+    nbytes = load_library().block_norm_backward_workspace_bytes(_BLOCK_PROBLEM.pack(*fields))
+    # scratch of this call's own: two captured graphs share nothing (none for
+    # a problem that the call below refuses, with the reason)
+    scratch = new((nbytes // 4,)) if nbytes > 0 else None
+    _call_packed("block_norm_backward",
+                 _BLOCK_BACKWARD_ARGS.pack(*fields, *inputs, *outputs, scratch.data_ptr() if nbytes > 0 else 0,
+                                           max(0, nbytes)), device)
+    return dx, dy, dpre_weight, dpost_weight, dgate

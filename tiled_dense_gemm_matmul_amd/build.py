@@ -7,6 +7,8 @@ from __future__ import annotations
 
 import os
 import subprocess
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -15,7 +17,8 @@ LOSS_SRC = os.path.join(PKG, "csrc", "loss.hip")
 ACT_SRC = os.path.join(PKG, "csrc", "activation.hip")
 ATTN_SRC = os.path.join(PKG, "csrc", "attention.hip")
 NORM_SRC = os.path.join(PKG, "csrc", "qk_norm_rope.hip")
-SRCS = [SRC, LOSS_SRC, ACT_SRC, ATTN_SRC, NORM_SRC]
+BLOCK_SRC = os.path.join(PKG, "csrc", "block_norm.hip")
+SRCS = [SRC, LOSS_SRC, ACT_SRC, ATTN_SRC, NORM_SRC, BLOCK_SRC]
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libgemmfwd.so")
 SYNC_LIB = os.path.join(PKG, "libgemmfwd_sync.so")
@@ -23,26 +26,36 @@ PROBE_SRC = os.path.join(PKG, "csrc", "mfma_probe.hip")
 PROBE_LIB = os.path.join(PKG, "libmfmaprobe.so")
 
 HIPCC_FLAGS = [
-    "--offload-arch=gfx950", "-O3", "-std=c++17", "-shared", "-fPIC",
+    "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
 ]
 
 
 def _hipcc(srcs, lib: str, verbose: bool, defines=()) -> str:
+    """Compiles every source to an object, side by side, and links them."""
     hipcc = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
-    tmp = lib + ".tmp"
-    cmd = [hipcc, *HIPCC_FLAGS, *[f"-D{d}" for d in defines], "-I", INCLUDE, *srcs, "-o", tmp]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    subprocess.run(cmd, check=True)
-    os.replace(tmp, lib)
+
+    def run(cmd):
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        subprocess.run(cmd, check=True)
+
+    with tempfile.TemporaryDirectory() as tmp, ThreadPoolExecutor(len(srcs)) as pool:
+        objects = [os.path.join(tmp, os.path.basename(src) + ".o") for src in srcs]
+        jobs = [pool.submit(run, [hipcc, *HIPCC_FLAGS, *[f"-D{d}" for d in defines], "-I", INCLUDE, "-c", src, "-o", o])
+                for src, o in zip(srcs, objects)]
+        for job in jobs:
+            job.result()
+        linked = lib + ".tmp"
+        run([hipcc, "--offload-arch=gfx950", "-shared", *objects, "-o", linked])
+    os.replace(linked, lib)
     return lib
 
 
 def build_library(verbose: bool = False) -> str:
     """The library: the GEMM family (forward and backward), the fused loss, the
-    FFN activation kernels, the attention kernels and the norm and
-    rotation of queries and keys."""
+    FFN activation kernels, the attention kernels, the norm and rotation of
+    queries and keys, and the norms around a block."""
     return _hipcc(SRCS, LIB, verbose)
 
 
