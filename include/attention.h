@@ -45,7 +45,9 @@
  *       angle = positions[t] inv_freq[p]     for pair p < rotated / 2
  *
  * where pair p is (p, p + rotated / 2), or (2p, 2p + 1) when interleaved,
- * and y = n from `rotated` on.  The angle is reduced to a part of a
+ * and y = n from `rotated` on.  With positions of several axes (the time,
+ * height and width of a patch, say) pair p turns by its own axis's position,
+ * angle = positions[pair_axis[p]][t] inv_freq[p].  The angle is reduced to a part of a
  * turn without loss for positions up to 2^53 in magnitude, and its sine and
  * cosine are good to fp32 relative to themselves.
  * The backward pass gives dx from dy, and the weight's gradient summed over
@@ -175,6 +177,20 @@ typedef struct attn_qk_norm_rope_args {
 } attn_qk_norm_rope_args;
 int attn_qk_norm_rope(const attn_qk_norm_rope_args *args, void *stream);
 
+/* Positions of several axes: n.positions is [axes, tokens], dense. */
+typedef struct attn_axes {
+    const int32_t *pair_axis;  /* [rotated / 2] device array; entries outside [0, axes) are clamped to it */
+    int64_t axes;              /* 1 to 65535 */
+} attn_axes;
+
+/* The same by positions of several axes. */
+typedef struct attn_qk_norm_rope_axes_args {
+    attn_norm n;
+    attn_axes x;
+    attn_tensor q, k, q_out, k_out;
+} attn_qk_norm_rope_axes_args;
+int attn_qk_norm_rope_axes(const attn_qk_norm_rope_axes_args *args, void *stream);
+
 /*
  * dq, dk and the weights' gradients [head_dim] from dq_out, dk_out, q and k.
  * dq may be the very same tensor as dq_out or q, dk as dk_out or k.  The
@@ -192,6 +208,17 @@ typedef struct attn_qk_norm_rope_backward_args {
 } attn_qk_norm_rope_backward_args;
 int attn_qk_norm_rope_backward(const attn_qk_norm_rope_backward_args *args, void *stream);
 int64_t attn_qk_norm_rope_workspace_bytes(int64_t tokens, int64_t head_dim);
+
+/* The same by positions of several axes. */
+typedef struct attn_qk_norm_rope_axes_backward_args {
+    attn_norm n;
+    attn_axes x;
+    attn_tensor dq_out, dk_out, q, k, dq, dk;
+    float *dq_weight, *dk_weight;
+    void *workspace;
+    int64_t workspace_bytes;
+} attn_qk_norm_rope_axes_backward_args;
+int attn_qk_norm_rope_axes_backward(const attn_qk_norm_rope_axes_backward_args *args, void *stream);
 
 #ifdef __cplusplus
 }

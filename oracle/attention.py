@@ -108,9 +108,48 @@ def attention_backward(dout, q, k, v, out, lse, cu=None, causal=True, window=0, 
     return (*grads, *[e + 1e-37 for e in errs])
 
 
-def _angles(positions, inv_freq):
-    """positions * inv_freq in extended precision (64-bit mantissa)."""
-    return np.asarray(positions).astype(np.longdouble)[:, None] * np.asarray(inv_freq).astype(np.longdouble)[None, :]
+_BITS = 256
+
+
+def _arctan_inverse(n):
+    """arctan(1 / n) 2^_BITS, by its series."""
+    term = total = (1 << _BITS) // n
+    k = 1
+    while term:
+        term = -term // (n * n)
+        k += 2
+        total += term // k
+    return total
+
+
+def _reduced(positions, inv_freq):
+    """The angles [tokens, pairs] less whole turns, from integers of 256 bits: a position of 2^53 times a frequency of
+    24 bits has 77, so that an extended product is off by up to 2^-11."""
+    turn = 8 * (4 * _arctan_inverse(5) - _arctan_inverse(239))  # Machin's formula for pi / 4
+    out = np.empty((len(positions), len(inv_freq)), dtype=np.longdouble)
+    for p, f in enumerate(inv_freq):
+        top, below = float(f).as_integer_ratio()
+        for t, pos in enumerate(positions):
+            rest = (int(pos) * top << _BITS) // below % turn
+            out[t, p] = np.longdouble(rest if 2 * rest < turn else rest - turn) / np.longdouble(2) ** _BITS
+    return out
+
+
+def _angles(positions, inv_freq, axis=None):
+    """positions * inv_freq in extended precision (64-bit mantissa), of far
+    positions less whole turns; with axis, each pair's own row of positions
+    [axes, tokens]."""
+    if axis is not None and np.abs(np.asarray(positions)).max(initial=0) > 1 << 32:
+        pos = np.asarray(positions)
+        cols = [_reduced(pos[a], np.asarray(inv_freq)[p:p + 1]) for p, a in enumerate(np.asarray(axis))]
+        return np.concatenate(cols, 1)
+    pos, freq = np.asarray(positions).astype(np.longdouble), np.asarray(inv_freq).astype(np.longdouble)
+    if axis is None:
+        return pos[:, None] * freq[None, :]
+    out = np.empty((pos.shape[1], freq.shape[0]), dtype=np.longdouble)
+    for p, a in enumerate(np.asarray(axis)):
+        out[:, p] = pos[a] * freq[p]
+    return out
 
 
 def _pairs(d, rotated, interleaved):
@@ -119,7 +158,7 @@ def _pairs(d, rotated, interleaved):
     return (2 * p, 2 * p + 1) if interleaved else (p, p + rotated // 2)
 
 
-def qk_norm_rope(x, weight, positions, inv_freq, eps=1e-6, interleaved=False):
+def qk_norm_rope(x, weight, positions, inv_freq, eps=1e-6, interleaved=False, axis=None):
     """The norm and rotation of x [T, H, D]: (y, its bound)."""
     x, w = np.asarray(x, dtype=np.float64), np.asarray(weight, dtype=np.float64)
     d = x.shape[2]
@@ -128,7 +167,7 @@ def qk_norm_rope(x, weight, positions, inv_freq, eps=1e-6, interleaved=False):
     # r: a sum of d squares, halved by the root; three products
     rel = ((d + 6) / 2 + 12) * U
     y, err = n.copy(), np.abs(n) * rel
-    angle = _angles(positions, inv_freq)
+    angle = _angles(positions, inv_freq, axis)
     c, s = (f(angle).astype(np.float64)[:, None] for f in (np.cos, np.sin))
     a, b = _pairs(d, 2 * angle.shape[1], interleaved)
     na, nb = n[..., a], n[..., b]
@@ -138,11 +177,11 @@ def qk_norm_rope(x, weight, positions, inv_freq, eps=1e-6, interleaved=False):
     return y, err + 1e-37
 
 
-def qk_norm_rope_backward(dy, x, weight, positions, inv_freq, eps=1e-6, interleaved=False):
+def qk_norm_rope_backward(dy, x, weight, positions, inv_freq, eps=1e-6, interleaved=False, axis=None):
     """(dx, dweight, dx's bound, dweight's bound)."""
     dy, x, w = (np.asarray(v, dtype=np.float64) for v in (dy, x, weight))
     T, H, d = x.shape
-    angle = _angles(positions, inv_freq)
+    angle = _angles(positions, inv_freq, axis)
     c, s = (f(angle).astype(np.float64)[:, None] for f in (np.cos, np.sin))
     a, b = _pairs(d, 2 * angle.shape[1], interleaved)
     dn, e_dn = dy.copy(), np.zeros_like(dy)

@@ -32,6 +32,7 @@ EXPORTED = (
     "act_ffn_gelu_backward", "act_gelu_inplace", "attn_forward", "attn_backward",
     "attn_backward_workspace_bytes", "attn_qk_norm_rope",
     "attn_qk_norm_rope_backward", "attn_qk_norm_rope_workspace_bytes",
+    "attn_qk_norm_rope_axes", "attn_qk_norm_rope_axes_backward",
     "block_norm", "block_norm_backward", "block_norm_backward_workspace_bytes",
     "gemm_timing_event_create", "gemm_timing_event_record", "gemm_timing_elapsed_ms", "gemm_timing_event_destroy",
 )
@@ -134,7 +135,8 @@ def _open(path):
     lib.act_gelu_inplace.argtypes = [p, p, i64, p]
     lib.act_gelu_inplace.restype = c_int
     for name in ("attn_forward", "attn_backward", "attn_qk_norm_rope", "attn_qk_norm_rope_backward",
-                 "loss_distill_cross_entropy", "block_norm", "block_norm_backward"):
+                 "attn_qk_norm_rope_axes", "attn_qk_norm_rope_axes_backward", "loss_distill_cross_entropy",
+                 "block_norm", "block_norm_backward"):
         getattr(lib, name).argtypes = [ctypes.c_char_p, p]  # the packed argument struct, the stream
         getattr(lib, name).restype = c_int
     lib.attn_backward_workspace_bytes.argtypes = [ctypes.c_char_p]
@@ -686,6 +688,8 @@ _PROBLEM = struct.Struct("=8qd")
 _BACKWARD_ARGS = struct.Struct("=8qd 15q q 9q 2q")
 _NORM_ARGS = struct.Struct("=11qd 12q")
 _NORM_BACKWARD_ARGS = struct.Struct("=11qd 18q 4q")
+_NORM_AXES_ARGS = struct.Struct("=11qd 2q 12q")
+_NORM_AXES_BACKWARD_ARGS = struct.Struct("=11qd 2q 18q 4q")
 
 
 def _heads(t, name, shape, device):
@@ -814,17 +818,18 @@ def _vector(t, name, device, n=None):
     return t.data_ptr()
 
 
-def _attn_norm(q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved):
-    """The fields of attn_norm, and the shapes of q and of k."""
+def _attn_norm(q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved, pair_axis):
+    """The fields of attn_norm and, with pair_axis, of attn_axes, and the shapes of q and of k."""
     for name, t in (("q", q), ("k", k)):
         if not isinstance(t, torch.Tensor) or t.dim() != 3:
             raise TypeError(f"{name} must be a 3-D torch.Tensor [tokens, heads, head_dim]")
     device = q.device
     tokens, hq, dim = q.shape
     hk = k.shape[1]
-    if not isinstance(positions, torch.Tensor) or positions.shape != (tokens,) or positions.device != device \
-            or not positions.is_contiguous():
-        raise ValueError(f"positions must be a contiguous [{tokens}] tensor on {device}")
+    by_axis = pair_axis is not None
+    if not isinstance(positions, torch.Tensor) or positions.dim() != (2 if by_axis else 1) \
+            or positions.shape[-1] != tokens or positions.device != device or not positions.is_contiguous():
+        raise ValueError(f"positions must be a contiguous [{'axes, ' if by_axis else ''}{tokens}] tensor on {device}")
     if positions.dtype not in (torch.int32, torch.int64):
         raise TypeError(f"positions must be int32 or int64, got {positions.dtype}")
     pf = _vector(inv_freq, "inv_freq", device)
@@ -834,10 +839,18 @@ def _attn_norm(q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved):
     fields = (positions.data_ptr(), 1 if positions.dtype == torch.int64 else 0, pf,
               _vector(q_weight, "q_weight", device, dim), _vector(k_weight, "k_weight", device, dim), tokens, hq, hk,
               dim, rotated, 1 if interleaved else 0, float(eps))
+    if by_axis:
+        if not isinstance(pair_axis, torch.Tensor) or pair_axis.shape != inv_freq.shape or pair_axis.device != device \
+                or not pair_axis.is_contiguous():
+            raise ValueError(f"pair_axis must be a contiguous [{rotated // 2}] tensor on {device}")
+        if pair_axis.dtype != torch.int32:
+            raise TypeError(f"pair_axis must be int32, got {pair_axis.dtype}")
+        fields += (pair_axis.data_ptr(), positions.shape[0])
     return fields, q.shape, (tokens, hk, dim)
 
 
-def qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, eps=1e-6, interleaved=False, q_out=None, k_out=None):
+def qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, eps=1e-6, interleaved=False, q_out=None, k_out=None,
+                 pair_axis=None):
     """Root-mean-square norm of every query and key head, times a weight, then
     the rotation by the token's position, in one pass over both.
 
@@ -847,8 +860,13 @@ def qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, eps=1e-6, interl
     inv_freq float32 [rotated / 2]: pair p of the first `rotated` dimensions
     turns by positions * inv_freq[p].  Pair p is dimensions p and p + rotated
     / 2, or with interleaved 2p and 2p + 1.  q_out and k_out may be q and k.
+    With pair_axis, int32 [rotated / 2], positions is [axes, tokens] (the
+    time, height and width of a patch, say) and pair p turns by
+    positions[pair_axis[p]] * inv_freq[p]; sections of neighbouring pairs, or
+    axes in turn, are a matter of that array (on the device, its entries in
+    [0, axes)).
     Returns (q_out, k_out)."""
-    fields, shape_q, shape_k = _attn_norm(q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved)
+    fields, shape_q, shape_k = _attn_norm(q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved, pair_axis)
     device = q.device
     tq = _heads(q, "q", shape_q, device)
     tk = _heads(k, "k", shape_k, device)
@@ -858,17 +876,20 @@ def qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, eps=1e-6, interl
         k_out = q.new_empty(shape_k)
     toq = _heads(q_out, "q_out", shape_q, device)
     tok = _heads(k_out, "k_out", shape_k, device)
-    _call_packed("attn_qk_norm_rope", _NORM_ARGS.pack(*fields, *tq, *tk, *toq, *tok), device)
+    if pair_axis is None:
+        _call_packed("attn_qk_norm_rope", _NORM_ARGS.pack(*fields, *tq, *tk, *toq, *tok), device)
+    else:
+        _call_packed("attn_qk_norm_rope_axes", _NORM_AXES_ARGS.pack(*fields, *tq, *tk, *toq, *tok), device)
     return q_out, k_out
 
 
 def qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, positions, inv_freq, eps=1e-6, interleaved=False,
-                          dq=None, dk=None, dq_weight=None, dk_weight=None):
+                          dq=None, dk=None, dq_weight=None, dk_weight=None, pair_axis=None):
     """Gradients of qk_norm_rope, from those of its results and its inputs.
     dq may be dq_out or q, dk may be dk_out or k (which are overwritten).
     Returns (dq, dk, dq_weight, dk_weight); the weights' gradients are sums
     over all tokens and heads."""
-    fields, shape_q, shape_k = _attn_norm(q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved)
+    fields, shape_q, shape_k = _attn_norm(q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved, pair_axis)
     device = q.device
     tgq = _heads(dq_out, "dq_out", shape_q, device)
     tgk = _heads(dk_out, "dk_out", shape_k, device)
@@ -892,9 +913,10 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, positions, i
         raise GemmError(-2, "attn_qk_norm_rope_workspace_bytes")
     # scratch of this call's own: two captured graphs share nothing
     scratch = q.new_empty((nbytes // 4,))
-    _call_packed("attn_qk_norm_rope_backward",
-                 _NORM_BACKWARD_ARGS.pack(*fields, *tgq, *tgk, *tq, *tk, *tdq, *tdk, pqw, pkw, scratch.data_ptr(),
-                                          nbytes), device)
+    name, args = (("attn_qk_norm_rope_backward", _NORM_BACKWARD_ARGS) if pair_axis is None else
+                  ("attn_qk_norm_rope_axes_backward", _NORM_AXES_BACKWARD_ARGS))
+    _call_packed(name, args.pack(*fields, *tgq, *tgk, *tq, *tk, *tdq, *tdk, pqw, pkw, scratch.data_ptr(), nbytes),
+                 device)
     return dq, dk, dq_weight, dk_weight
 
 

@@ -13,7 +13,9 @@
 //  * The dimensions that are not rotated are paired in the same way and turned by
 //    the angle zero, so a head is one kind of pair throughout.
 //  * The angle pos * inv_freq is formed and reduced to a part of a turn in 64
-//    bits, with the rounding errors of both products carried along.  Sine and
+//    bits, with the rounding errors of both products carried along.  With
+//    positions of several axes (AXES) every pair has a position of its own, which
+//    a lane loads by the pair's axis; what follows is the same.  Sine and
 //    cosine are taken of that part rounded to fp32, and turned by what the
 //    rounding left out (without that they were off by up to 1.1e-7, not
 //    3e-8, and by far more than an ulp near their zeros), so they are good to
@@ -41,6 +43,8 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 struct Norm {
     const void *pos;
     const float *inv_freq, *qw, *kw;
+    const int *axis;              // of each rotated pair, with `axes` rows of positions
+    int axes;
     int tokens, hq, hk, d, half;  // half: rotated pairs
     int wide, interleaved;
     float eps, inv_d;
@@ -119,8 +123,15 @@ __device__ __forceinline__ void turn(const Norm &n, double pos, int p, float &c,
         c = fmaf(-s0, rest, c);
     }
 }
-__device__ __forceinline__ double position(const Norm &n, int t) {
+__device__ __forceinline__ double position(const Norm &n, int64_t t) {
     return n.wide ? (double)((const int64_t *)n.pos)[t] : (double)((const int *)n.pos)[t];
+}
+// The row of positions that pair p turns by (the first one past the rotated
+// pairs, which turn by no angle).
+template <bool AXES>
+__device__ __forceinline__ int64_t axis_row(const Norm &n, int p) {
+    if (!AXES || p >= n.half) return 0;
+    return (int64_t)min(max(n.axis[p], 0), n.axes - 1) * n.tokens;
 }
 
 template <int G>
@@ -133,7 +144,7 @@ __device__ __forceinline__ float lanes_sum(float v) {
 // NP groups of W pairs a lane, G lanes a head; a wave takes token
 // item / chunks and every (chunks * 64 / G)-th head from its chunk on; `first`
 // workgroups lie in front of this launch's.
-template <int W, int G, int NP>
+template <int W, int G, int NP, bool AXES>
 __global__ __launch_bounds__(256) void qk_norm_rope_fwd(Norm n, Strided q, Strided k, Strided yq, Strided yk, int chunks,
                                                         int64_t first) {
     constexpr int HW = 64 / G;  // heads at a time
@@ -141,7 +152,7 @@ __global__ __launch_bounds__(256) void qk_norm_rope_fwd(Norm n, Strided q, Strid
     const int64_t item = (first + blockIdx.x) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int t = (int)(item / chunks), chunk = (int)(item % chunks);
     if (t >= n.tokens) return;
-    const double pos = position(n, t);
+    const double pos = AXES ? 0.0 : position(n, t);
     Place at[NP];
     bool in[NP];
     float c[NP][W], s[NP][W];
@@ -151,7 +162,8 @@ __global__ __launch_bounds__(256) void qk_norm_rope_fwd(Norm n, Strided q, Strid
         in[i] = p < n.d / 2;
         at[i] = place(n, p, W);
 #pragma unroll
-        for (int e = 0; e < W; ++e) turn(n, pos, p + e, c[i][e], s[i][e]);
+        for (int e = 0; e < W; ++e)
+            turn(n, AXES ? position(n, axis_row<AXES>(n, p + e) + t) : pos, p + e, c[i][e], s[i][e]);
     }
     const int heads = n.hq + n.hk;
     for (int h = chunk * HW + slot; h < heads; h += chunks * HW) {
@@ -193,7 +205,7 @@ __global__ __launch_bounds__(256) void qk_norm_rope_fwd(Norm n, Strided q, Strid
 constexpr int kWaves = 8;    // of a workgroup of the backward pass
 constexpr int kParts = 512;  // workgroups of the backward pass at most: two a CU
 
-template <int W, int G, int NP>
+template <int W, int G, int NP, bool AXES>
 __global__ __launch_bounds__(64 * kWaves) void qk_norm_rope_bwd(Norm n, Strided gq, Strided gk, Strided q, Strided k, Strided dq,
                                                         Strided dk, double *parts, int chunks) {
     constexpr int HW = 64 / G;
@@ -202,11 +214,14 @@ __global__ __launch_bounds__(64 * kWaves) void qk_norm_rope_bwd(Norm n, Strided 
     Place at[NP];
     bool in[NP];
     double sums[2][NP][2 * W];
+    int64_t row[NP][W];  // of the pairs' positions
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
         const int p = (i * G + part) * W;
         in[i] = p < n.d / 2;
         at[i] = place(n, p, W);
+#pragma unroll
+        for (int e = 0; e < W; ++e) row[i][e] = axis_row<AXES>(n, p + e);
 #pragma unroll
         for (int e = 0; e < 2 * W; ++e) sums[0][i][e] = sums[1][i][e] = 0.0;
     }
@@ -215,14 +230,14 @@ __global__ __launch_bounds__(64 * kWaves) void qk_norm_rope_bwd(Norm n, Strided 
     for (int64_t item = (int64_t)blockIdx.x * kWaves + wave; item < items;
          item += (int64_t)gridDim.x * kWaves) {
         const int t = (int)(item / chunks), chunk = (int)(item % chunks);
-        const double pos = position(n, t);
+        const double pos = AXES ? 0.0 : position(n, t);
         float c[NP][W], s[NP][W];
         float dw[2][NP][2 * W];
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
 #pragma unroll
             for (int e = 0; e < W; ++e) {
-                turn(n, pos, (i * G + part) * W + e, c[i][e], s[i][e]);
+                turn(n, AXES ? position(n, row[i][e] + t) : pos, (i * G + part) * W + e, c[i][e], s[i][e]);
                 dw[0][i][e] = dw[0][i][W + e] = dw[1][i][e] = dw[1][i][W + e] = 0.0f;
             }
         }
@@ -366,15 +381,35 @@ int check_view(const View &v, int64_t tokens, int64_t d) {
     return GEMM_OK;
 }
 
-// Whether an output overlaps what every thread reads: weights, frequencies, positions.
-bool covers_shared(const View &o, const attn_norm &n) {
-    const int64_t T = n.tokens, D = n.head_dim;
-    return in_range(o, n.q_weight, D * 4, T, D) || in_range(o, n.k_weight, D * 4, T, D) ||
-           in_range(o, n.inv_freq, n.rotated * 2, T, D) || in_range(o, n.positions, T * (n.positions64 ? 8 : 4), T, D);
+// One position a token: every pair turns by it.
+constexpr attn_axes kOneAxis = {nullptr, 1};
+
+int check_axes(const attn_norm &n, const attn_axes &x) {
+    if (x.axes < 1 || x.axes > 65535) return GEMM_ERR_SHAPE;
+    if (n.rotated > 0 && x.pair_axis == nullptr) return GEMM_ERR_NULL;
+    return aligned(x.pair_axis, 4) ? GEMM_OK : GEMM_ERR_ALIGN;
 }
 
-Norm device_norm(const attn_norm &a) {
+// What every thread reads: weights, frequencies, positions and the pairs' axes.
+struct Shared {
+    Span part[5];
+    Shared(const attn_norm &n, const attn_axes &x)
+        : part{{n.q_weight, n.head_dim * 4},
+               {n.k_weight, n.head_dim * 4},
+               {n.inv_freq, n.rotated * 2},
+               {n.positions, x.axes * n.tokens * (n.positions64 ? 8 : 4)},
+               {x.pair_axis, n.rotated * 2}} {}
+};
+bool covers_shared(const View &o, const attn_norm &n, const Shared &shared) {
+    for (const Span &s : shared.part)
+        if (in_range(o, s.p, s.bytes, n.tokens, n.head_dim)) return true;
+    return false;
+}
+
+Norm device_norm(const attn_norm &a, const attn_axes &x) {
     Norm n;
+    n.axis = x.pair_axis;
+    n.axes = (int)x.axes;
     n.pos = a.positions;
     n.inv_freq = a.inv_freq;
     n.qw = a.q_weight;
@@ -426,27 +461,27 @@ int64_t backward_groups(int64_t items) { return std::max<int64_t>(1, std::min<in
         }                                                                                                     \
     } while (0)
 
-}  // namespace
+int64_t workspace_bytes(int64_t head_dim) { return kParts * 2 * head_dim * 8; }
 
-extern "C" {
-
-int attn_qk_norm_rope(const attn_qk_norm_rope_args *args, void *stream) {
-    if (args == nullptr) return GEMM_ERR_NULL;
-    const attn_qk_norm_rope_args &a = *args;
+// `a` has n, q, k, q_out and k_out, with or without the axes x beside them.
+template <bool AXES, class Args>
+int forward(const Args &a, const attn_axes &x, void *stream) {
     const int64_t T = a.n.tokens, D = a.n.head_dim, HQ = a.n.q_heads, HK = a.n.k_heads;
     int st = check_norm(a.n);
+    if (st == GEMM_OK && AXES) st = check_axes(a.n, x);
     if (st != GEMM_OK) return st;
     if (T == 0) return GEMM_OK;
     const View q = {&a.q, HQ, false}, k = {&a.k, HK, false}, yq = {&a.q_out, HQ, true}, yk = {&a.k_out, HK, true};
-    for (const View *x : {&q, &k, &yq, &yk})
-        if ((st = check_view(*x, T, D)) != GEMM_OK) return st;
+    for (const View *v : {&q, &k, &yq, &yk})
+        if ((st = check_view(*v, T, D)) != GEMM_OK) return st;
+    const Shared shared(a.n, x);
     if ((!same_tensor(a.q_out, a.q) && overlap(yq, q, T, D)) || (!same_tensor(a.k_out, a.k) && overlap(yk, k, T, D)) ||
-        overlap(yq, k, T, D) || overlap(yk, q, T, D) || overlap(yq, yk, T, D) || covers_shared(yq, a.n) ||
-        covers_shared(yk, a.n))
+        overlap(yq, k, T, D) || overlap(yk, q, T, D) || overlap(yq, yk, T, D) || covers_shared(yq, a.n, shared) ||
+        covers_shared(yk, a.n, shared))
         return GEMM_ERR_ALIAS;
     const attn_tensor *all[4] = {&a.q, &a.k, &a.q_out, &a.k_out};
     const bool vec = vector_access(a.n, all, 4);
-    const Norm n = device_norm(a.n);
+    const Norm n = device_norm(a.n, x);
     const Strided sq = strided(a.q, T, HQ), sk = strided(a.k, T, HK), oq = strided(a.q_out, T, HQ),
                   ok = strided(a.k_out, T, HK);
     hipStream_t hs = static_cast<hipStream_t>(stream);
@@ -454,7 +489,7 @@ int attn_qk_norm_rope(const attn_qk_norm_rope_args *args, void *stream) {
     do {                                                                                                            \
         const int chunks = chunks_of(T, HQ + HK, 64 / G);                                                           \
         st = in_slices((T * chunks + 3) / 4, 256, [&](int64_t first, unsigned count) {                              \
-            hipLaunchKernelGGL((qk_norm_rope_fwd<W, G, NP>), dim3(count), dim3(256), 0, hs, n, sq, sk, oq, ok,      \
+            hipLaunchKernelGGL((qk_norm_rope_fwd<W, G, NP, AXES>), dim3(count), dim3(256), 0, hs, n, sq, sk, oq, ok,      \
                                chunks, first);                                                                      \
         });                                                                                                         \
     } while (0)
@@ -463,23 +498,19 @@ int attn_qk_norm_rope(const attn_qk_norm_rope_args *args, void *stream) {
     return st;
 }
 
-int64_t attn_qk_norm_rope_workspace_bytes(int64_t tokens, int64_t head_dim) {
-    if (tokens < 0 || tokens >= ((int64_t)1 << 30) || head_dim < 2 || head_dim > 256) return -1;
-    return kParts * 2 * head_dim * 8;
-}
-
-int attn_qk_norm_rope_backward(const attn_qk_norm_rope_backward_args *args, void *stream) {
-    if (args == nullptr) return GEMM_ERR_NULL;
-    const attn_qk_norm_rope_backward_args &a = *args;
+template <bool AXES, class Args>
+int backward(const Args &a, const attn_axes &axes, void *stream) {
     const int64_t T = a.n.tokens, D = a.n.head_dim, HQ = a.n.q_heads, HK = a.n.k_heads;
     int st = check_norm(a.n);
+    if (st == GEMM_OK && AXES) st = check_axes(a.n, axes);
     if (st != GEMM_OK) return st;
     if (a.dq_weight == nullptr || a.dk_weight == nullptr || a.workspace == nullptr) return GEMM_ERR_NULL;
     if (!aligned(a.dq_weight, 4) || !aligned(a.dk_weight, 4) || !aligned(a.workspace, 8)) return GEMM_ERR_ALIGN;
-    const int64_t need = attn_qk_norm_rope_workspace_bytes(T, D);
+    const int64_t need = workspace_bytes(D);
     if (a.workspace_bytes < need) return GEMM_ERR_WORKSPACE;
     const View gq = {&a.dq_out, HQ, false}, gk = {&a.dk_out, HK, false}, q = {&a.q, HQ, false}, k = {&a.k, HK, false},
                dq = {&a.dq, HQ, true}, dk = {&a.dk, HK, true};
+    const Shared shared(a.n, axes);
     if (T > 0) {
         for (const View *x : {&gq, &gk, &q, &k, &dq, &dk})
             if ((st = check_view(*x, T, D)) != GEMM_OK) return st;
@@ -489,25 +520,23 @@ int attn_qk_norm_rope_backward(const attn_qk_norm_rope_backward_args *args, void
                                  ((o == &dq) == (x == &gq || x == &q));
                 if (!own && overlap(*o, *x, T, D)) return GEMM_ERR_ALIAS;
             }
-            if (covers_shared(*o, a.n)) return GEMM_ERR_ALIAS;
+            if (covers_shared(*o, a.n, shared)) return GEMM_ERR_ALIAS;
         }
         if (overlap(dq, dk, T, D)) return GEMM_ERR_ALIAS;
     }
     // the weights' gradients and the scratch apart from everything else
     const Span small[3] = {{a.dq_weight, D * 4}, {a.dk_weight, D * 4}, {a.workspace, need}};
-    const Span shared[4] = {{a.n.q_weight, D * 4}, {a.n.k_weight, D * 4}, {a.n.inv_freq, a.n.rotated * 2},
-                            {a.n.positions, T * (a.n.positions64 ? 8 : 4)}};
     for (int i = 0; i < 3; ++i) {
         for (int j = 0; j < i; ++j)
             if (spans_overlap(small[i], small[j])) return GEMM_ERR_ALIAS;
-        for (const Span &x : shared)
+        for (const Span &x : shared.part)
             if (spans_overlap(small[i], x)) return GEMM_ERR_ALIAS;
         for (const View *x : {&gq, &gk, &q, &k, &dq, &dk})
             if (T > 0 && in_range(*x, small[i].p, small[i].bytes, T, D)) return GEMM_ERR_ALIAS;
     }
     const attn_tensor *all[6] = {&a.dq_out, &a.dk_out, &a.q, &a.k, &a.dq, &a.dk};
     const bool vec = vector_access(a.n, all, 6);
-    const Norm n = device_norm(a.n);
+    const Norm n = device_norm(a.n, axes);
     const Strided g0 = strided(a.dq_out, T, HQ), g1 = strided(a.dk_out, T, HK), sq = strided(a.q, T, HQ),
                   sk = strided(a.k, T, HK), o0 = strided(a.dq, T, HQ), o1 = strided(a.dk, T, HK);
     hipStream_t hs = static_cast<hipStream_t>(stream);
@@ -517,7 +546,7 @@ int attn_qk_norm_rope_backward(const attn_qk_norm_rope_backward_args *args, void
     do {                                                                                                                \
         const int chunks = T > 0 ? chunks_of(T, HQ + HK, 64 / G) : 1;                                                   \
         grid = (int)backward_groups(T * chunks);                                                                        \
-        hipLaunchKernelGGL((qk_norm_rope_bwd<W, G, NP>), dim3(grid), dim3(64 * kWaves), 0, hs, n, g0, g1, sq, sk, o0,  \
+        hipLaunchKernelGGL((qk_norm_rope_bwd<W, G, NP, AXES>), dim3(grid), dim3(64 * kWaves), 0, hs, n, g0, g1, sq, sk, o0,  \
                            o1, parts, chunks);                                                                          \
     } while (0)
     NORM_BY_LANES(BWD);
@@ -525,6 +554,31 @@ int attn_qk_norm_rope_backward(const attn_qk_norm_rope_backward_args *args, void
     hipLaunchKernelGGL(weight_grads, dim3((unsigned)((2 * D + 15) / 16)), dim3(1024), 0, hs, parts, grid, a.dq_weight,
                        a.dk_weight, (int)D);
     return hipGetLastError() == hipSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
+}
+
+}  // namespace
+
+extern "C" {
+
+int attn_qk_norm_rope(const attn_qk_norm_rope_args *args, void *stream) {
+    return args == nullptr ? GEMM_ERR_NULL : forward<false>(*args, kOneAxis, stream);
+}
+
+int attn_qk_norm_rope_axes(const attn_qk_norm_rope_axes_args *args, void *stream) {
+    return args == nullptr ? GEMM_ERR_NULL : forward<true>(*args, args->x, stream);
+}
+
+int attn_qk_norm_rope_backward(const attn_qk_norm_rope_backward_args *args, void *stream) {
+    return args == nullptr ? GEMM_ERR_NULL : backward<false>(*args, kOneAxis, stream);
+}
+
+int attn_qk_norm_rope_axes_backward(const attn_qk_norm_rope_axes_backward_args *args, void *stream) {
+    return args == nullptr ? GEMM_ERR_NULL : backward<true>(*args, args->x, stream);
+}
+
+int64_t attn_qk_norm_rope_workspace_bytes(int64_t tokens, int64_t head_dim) {
+    if (tokens < 0 || tokens >= ((int64_t)1 << 30) || head_dim < 2 || head_dim > 256) return -1;
+    return workspace_bytes(head_dim);
 }
 
 }  // extern "C"
