@@ -12,7 +12,7 @@
  * row sees itself).  Query head h reads key/value head h / (q_heads /
  * kv_heads).  For every row i and query head:
  *
- *   s_ij   = scale q_i . k_j                 over the visible j
+ *   s_ij   = scale q_i . k_j                 over the visible j (or as below)
  *   lse_i  = log sum_j exp(s_ij)             (natural logarithm)
  *   out_i  = sum_j exp(s_ij - lse_i) v_j
  *
@@ -141,6 +141,55 @@ typedef struct attn_backward_args {
 } attn_backward_args;
 int64_t attn_backward_workspace_bytes(const attn_problem *problem);
 int attn_backward(const attn_backward_args *args, void *stream);
+
+/*
+ * Scores of other forms, in any combination (attn_scored_*):
+ *
+ *   s_ij = softcap tanh(scale q_i . k_j / softcap) - slopes[h] |i - j|
+ *
+ * for query head h, and with prefix_lens row i sees, beside the keys j <= i,
+ * the first prefix_lens[b] keys of its sequence b (entries below 0 and past
+ * the sequence's length are clamped), less than `window` away as ever.  The
+ * backward pass is that of the final scores,
+ *
+ *   dslopes[h] = - sum_{i,j} ds_ij |i - j|,
+ *
+ * with ds_ij (1 - tanh^2) in the place of ds_ij in dq and dk.  Distances are
+ * fp32, slopes finite (others spread NaN over their head).
+ */
+typedef struct attn_scores {
+    double softcap;             /* 0: none; 1e-6 to 1e6, with scale / softcap normal in fp32 */
+    const float *slopes;        /* [q_heads], or NULL */
+    const int32_t *prefix_lens; /* [num_seqs] ([1] without cu_seqlens) device array, or NULL; only with causal */
+} attn_scores;
+
+/* As attn_forward; out and lse overlap neither slopes nor prefix_lens.
+ * GEMM_ERR_DTYPE also for a softcap outside the above or prefix_lens without
+ * causal. */
+typedef struct attn_scored_forward_args {
+    attn_problem p;
+    attn_scores s;
+    attn_tensor q, k, v, out;
+    float *lse;
+} attn_scored_forward_args;
+int attn_scored_forward(const attn_scored_forward_args *args, void *stream);
+
+/* As attn_backward, and dslopes [q_heads], or NULL where it is not wanted
+ * (GEMM_ERR_NULL for dslopes without slopes); it may not overlap another array
+ * of the call, and with tokens == 0 it is zero.  With dslopes the workspace is
+ * 8-byte aligned, and its size is the one for a slopes_gradient other than 0. */
+typedef struct attn_scored_backward_args {
+    attn_problem p;
+    attn_scores s;
+    attn_tensor dout, q, k, v, out;
+    const float *lse;
+    attn_tensor dq, dk, dv;
+    float *dslopes;
+    void *workspace;
+    int64_t workspace_bytes;
+} attn_scored_backward_args;
+int64_t attn_scored_backward_workspace_bytes(const attn_problem *problem, int slopes_gradient);
+int attn_scored_backward(const attn_scored_backward_args *args, void *stream);
 
 /* The sizes of a norm and rotation and what all rows share. */
 typedef struct attn_norm {

@@ -215,3 +215,108 @@ def compare(y, ref, bound):
     ratio = np.where(np.isnan(ratio), np.inf, ratio)
     return {"max_ratio": float(ratio.max()) if ratio.size else 0.0,
             "fails": int((ratio > 1).sum()) + (0 if same else 1), "n": int(ref.size)}
+
+
+# --- scores that are capped, biased by distance, or masked with a prefix ---
+
+
+def scored_visible(n, causal, window, prefix=0):
+    see = visible(n, causal, 0)
+    see[:, :max(0, min(prefix, n))] = True
+    return see & visible(n, False, window)
+
+
+def _final_scores(q, k, scale, softcap, slope):
+    """The final scores of one head, the derivative of the cap, the distances,
+    and how far a score may be off in fp32."""
+    n, d = q.shape
+    raw = scale * (q @ k.T)
+    err = scale * (d + 4) * U * (np.abs(q) @ np.abs(k).T) + 2 * U * np.abs(raw)
+    away = np.abs(np.arange(n)[:, None] - np.arange(n)[None, :]).astype(np.float64)
+    s, steep = raw, np.ones((n, n))
+    if softcap:
+        t = np.tanh(raw / softcap)
+        s, steep = softcap * t, 1.0 - t * t
+        # what the argument is off by, which the cap's slope shrinks, and the tanh's own 8 u
+        err = steep * (err + 2 * U * np.abs(raw)) + 8 * U * np.abs(s) + err * err / softcap
+    if slope:
+        s = s - slope * away
+        err = err + 4 * U * np.abs(slope) * away
+    return s, steep, away, err + 8 * U * np.abs(s)
+
+
+def scored_attention(q, k, v, cu=None, causal=True, window=0, scale=None, softcap=0.0, slopes=None, prefix=None):
+    """As attention, with scores of the other forms; prefix: a length for each sequence."""
+    q, k, v = (np.asarray(x, dtype=np.float64) for x in (q, k, v))
+    T, hq, d = q.shape
+    group = hq // k.shape[1]
+    scale = d ** -0.5 if scale is None else scale
+    out, out_err = np.zeros((T, hq, d)), np.zeros((T, hq, d))
+    lse, lse_err = np.full((hq, T), -np.inf), np.zeros((hq, T))
+    for b, (a, e) in enumerate(sequences(cu, T)):
+        n = e - a
+        if n == 0:
+            continue
+        see = scored_visible(n, causal, window, 0 if prefix is None else int(prefix[b]))
+        for h in range(hq):
+            vs = v[a:e, h // group]
+            s, _, _, ds = _final_scores(q[a:e, h], k[a:e, h // group], scale, softcap,
+                                        0.0 if slopes is None else float(slopes[h]))
+            s = np.where(see, s, -np.inf)
+            top = s.max(1, keepdims=True)
+            p = np.exp(s - top)
+            total = p.sum(1, keepdims=True)
+            p = p / total
+            # a score's error moves its own probability and, through the sum, all others by the probable one's
+            own = np.where(see, ds, 0.0) + 8 * U * np.abs(top)
+            mean = (p * own).sum(1, keepdims=True)
+            out[a:e, h] = p @ vs
+            rel = own + mean + (2 * n + 24) * U + 8 * U * np.where(see, np.abs(s - top), 0.0)
+            out_err[a:e, h] = (p * rel) @ np.abs(vs) + 1e-37
+            lse[h, a:e] = (top + np.log(total))[:, 0]
+            lse_err[h, a:e] = (mean + (n + 16) * U + 8 * U * np.abs(top) + 8 * U * np.abs(np.log(total)))[:, 0]
+    return out, lse, out_err, lse_err
+
+
+def scored_attention_backward(dout, q, k, v, out, lse, cu=None, causal=True, window=0, scale=None, softcap=0.0,
+                              slopes=None, prefix=None):
+    """(dq, dk, dv, dslopes) and their bounds, from the given out and lse."""
+    dout, q, k, v, out, lse = (np.asarray(x, dtype=np.float64) for x in (dout, q, k, v, out, lse))
+    T, hq, d = q.shape
+    group = hq // k.shape[1]
+    scale = d ** -0.5 if scale is None else scale
+    grads = [np.zeros(q.shape), np.zeros(k.shape), np.zeros(k.shape), np.zeros(hq)]
+    errs = [np.zeros(q.shape), np.zeros(k.shape), np.zeros(k.shape), np.zeros(hq)]
+    for b, (a, e) in enumerate(sequences(cu, T)):
+        n = e - a
+        if n == 0:
+            continue
+        see = scored_visible(n, causal, window, 0 if prefix is None else int(prefix[b]))
+        rows = n * group
+        for h in range(hq):
+            hk = h // group
+            qs, ks, vs, gs, os_ = q[a:e, h], k[a:e, hk], v[a:e, hk], dout[a:e, h], out[a:e, h]
+            s, steep, away, e_s = _final_scores(qs, ks, scale, softcap, 0.0 if slopes is None else float(slopes[h]))
+            l = lse[h, a:e][:, None]
+            p = np.where(see, np.exp(np.where(see, s - l, 0.0)), 0.0)
+            dp, delta = gs @ vs.T, (gs * os_).sum(1, keepdims=True)
+            ds = p * (dp - delta)
+            rel = np.where(see, e_s + 8 * U * np.abs(l) + 8 * U, 0.0)
+            e_dp = (d + 2) * U * (np.abs(gs) @ np.abs(vs).T)
+            e_delta = (d + 2) * U * (np.abs(gs) * np.abs(os_)).sum(1, keepdims=True)
+            e_ds = p * ((rel + 4 * U) * np.abs(dp - delta) + (1 + rel) * (e_dp + e_delta))
+            grads[3][h] -= (ds * away).sum()
+            # fp32 over 4 keys, 64 bits from there
+            errs[3][h] += ((e_ds + 8 * U * np.abs(ds)) * away).sum()
+            grads[2][a:e, hk] += p.T @ gs
+            errs[2][a:e, hk] += (p * (rel + (rows + 6) * U)).T @ np.abs(gs)
+            # the cap's derivative: its tanh is off by what the score is off by, over the cap
+            e_ds = steep * e_ds + np.abs(ds) * (6 * U * np.minimum(1.0, steep + 4 * U)
+                                                + (2 * e_s / softcap + 4 * U if softcap else 0.0))
+            ds = ds * steep
+            grads[0][a:e, h] += scale * (ds @ ks)
+            errs[0][a:e, h] += scale * ((e_ds + (n + 6) * U * np.abs(ds)) @ np.abs(ks))
+            grads[1][a:e, hk] += scale * (ds.T @ qs)
+            errs[1][a:e, hk] += scale * ((e_ds + (rows + 6) * U * np.abs(ds)).T @ np.abs(qs))
+    errs[3] += U * np.abs(grads[3])
+    return (*grads, *[x + 1e-37 for x in errs])

@@ -33,6 +33,7 @@ EXPORTED = (
     "attn_backward_workspace_bytes", "attn_qk_norm_rope",
     "attn_qk_norm_rope_backward", "attn_qk_norm_rope_workspace_bytes",
     "attn_qk_norm_rope_axes", "attn_qk_norm_rope_axes_backward",
+    "attn_scored_forward", "attn_scored_backward", "attn_scored_backward_workspace_bytes",
     "block_norm", "block_norm_backward", "block_norm_backward_workspace_bytes",
     "gemm_timing_event_create", "gemm_timing_event_record", "gemm_timing_elapsed_ms", "gemm_timing_event_destroy",
 )
@@ -136,13 +137,15 @@ def _open(path):
     lib.act_gelu_inplace.restype = c_int
     for name in ("attn_forward", "attn_backward", "attn_qk_norm_rope", "attn_qk_norm_rope_backward",
                  "attn_qk_norm_rope_axes", "attn_qk_norm_rope_axes_backward", "loss_distill_cross_entropy",
-                 "block_norm", "block_norm_backward"):
+                 "attn_scored_forward", "attn_scored_backward", "block_norm", "block_norm_backward"):
         getattr(lib, name).argtypes = [ctypes.c_char_p, p]  # the packed argument struct, the stream
         getattr(lib, name).restype = c_int
     lib.attn_backward_workspace_bytes.argtypes = [ctypes.c_char_p]
     lib.attn_backward_workspace_bytes.restype = i64
     lib.attn_qk_norm_rope_workspace_bytes.argtypes = [i64, i64]
     lib.attn_qk_norm_rope_workspace_bytes.restype = i64
+    lib.attn_scored_backward_workspace_bytes.argtypes = [ctypes.c_char_p, c_int]
+    lib.attn_scored_backward_workspace_bytes.restype = i64
     lib.block_norm_backward_workspace_bytes.argtypes = [ctypes.c_char_p]
     lib.block_norm_backward_workspace_bytes.restype = i64
     lib.gemm_timing_event_create.argtypes = [ctypes.POINTER(ctypes.c_void_p)]
@@ -686,6 +689,8 @@ def gelu_inplace(x, pre_gelu=None):
 _FORWARD_ARGS = struct.Struct("=8qd 12q q")
 _PROBLEM = struct.Struct("=8qd")
 _BACKWARD_ARGS = struct.Struct("=8qd 15q q 9q 2q")
+_SCORED_ARGS = struct.Struct("=8qd d2q 12q q")
+_SCORED_BACKWARD_ARGS = struct.Struct("=8qd d2q 15q q 9q q 2q")
 _NORM_ARGS = struct.Struct("=11qd 12q")
 _NORM_BACKWARD_ARGS = struct.Struct("=11qd 18q 4q")
 _NORM_AXES_ARGS = struct.Struct("=11qd 2q 12q")
@@ -745,7 +750,27 @@ def _attn_problem(q, k, cu_seqlens, causal, window, scale):
     return (cu, nseq, tokens, hq, hkv, dim, 1 if causal else 0, int(window), float(scale)), shape_q, (tokens, hkv, dim)
 
 
-def attention(q, k, v, cu_seqlens=None, causal=True, window=0, scale=None, out=None, lse=None):
+def _attn_scores(problem, softcap, slopes, prefix_lens, device):
+    """The fields of attn_scores, or None for plain scores."""
+    if softcap == 0 and slopes is None and prefix_lens is None:
+        return None
+    _, nseq, _, hq, _, _, causal, _, _ = problem
+    pp = 0
+    if prefix_lens is not None:
+        n = nseq if problem[0] else 1
+        if not isinstance(prefix_lens, torch.Tensor) or prefix_lens.shape != (n,) or prefix_lens.device != device \
+                or not prefix_lens.is_contiguous():
+            raise ValueError(f"prefix_lens must be a contiguous [{n}] tensor on {device}")
+        if prefix_lens.dtype != torch.int32:
+            raise TypeError(f"prefix_lens must be int32, got {prefix_lens.dtype}")
+        if not causal:
+            raise ValueError("prefix_lens needs causal: without it all keys are seen anyway")
+        pp = prefix_lens.data_ptr()
+    return float(softcap), 0 if slopes is None else _vector(slopes, "slopes", device, hq), pp
+
+
+def attention(q, k, v, cu_seqlens=None, causal=True, window=0, scale=None, out=None, lse=None, softcap=0.0, slopes=None,
+              prefix_lens=None):
     """Attention over packed sequences: out = softmax(scale q k^T over the
     visible keys) v, and lse, the logarithm of each row's sum of exponentials,
     which attention_backward needs.
@@ -759,6 +784,12 @@ def attention(q, k, v, cu_seqlens=None, causal=True, window=0, scale=None, out=N
     sequence get out 0 and lse -inf.  A row sees the rows of its sequence, up
     to itself with causal, less than `window` away with window > 0.  scale
     defaults to head_dim ** -0.5.  out may be q itself.
+
+    Scores of other forms, in any combination: softcap > 0 (1e-6 to 1e6)
+    bends them to softcap * tanh(score / softcap); slopes, float32 [q_heads],
+    takes slopes[head] * |i - j| from them; prefix_lens, int32 [sequences] on
+    the device ([1] without cu_seqlens), lets every row of sequence b see its
+    first prefix_lens[b] rows too (with causal).
     Returns (out like q, lse [q_heads, tokens])."""
     problem, shape_q, shape_k = _attn_problem(q, k, cu_seqlens, causal, window, scale)
     device = q.device
@@ -772,17 +803,22 @@ def attention(q, k, v, cu_seqlens=None, causal=True, window=0, scale=None, out=N
     if lse is None:
         lse = q.new_empty((hq, tokens))
     pl = _row_values(lse, "lse", (hq, tokens), device)
-    _call_packed("attn_forward", _FORWARD_ARGS.pack(*problem, *tq, *tk, *tv, *to, pl), device)
+    scores = _attn_scores(problem, softcap, slopes, prefix_lens, device)
+    if scores is None:
+        _call_packed("attn_forward", _FORWARD_ARGS.pack(*problem, *tq, *tk, *tv, *to, pl), device)
+    else:
+        _call_packed("attn_scored_forward", _SCORED_ARGS.pack(*problem, *scores, *tq, *tk, *tv, *to, pl), device)
     return out, lse
 
 
 def attention_backward(dout, q, k, v, out, lse, cu_seqlens=None, causal=True, window=0, scale=None, dq=None, dk=None,
-                       dv=None):
+                       dv=None, softcap=0.0, slopes=None, prefix_lens=None, dslopes=None):
     """Gradients of attention: dq, dk, dv from dout, its inputs, and the out
     and lse it returned (the probabilities are formed again from lse).
     Arguments as for attention; dq, dk and dv may be views of one buffer, but
     may not overlap an input.  Rows of no sequence get zero gradients.
-    Returns (dq, dk, dv)."""
+    dslopes, float32 [q_heads], gets the gradient of slopes where it is given.
+    Returns (dq, dk, dv), and dslopes behind them where it is given."""
     problem, shape_q, shape_k = _attn_problem(q, k, cu_seqlens, causal, window, scale)
     device = q.device
     tg = _heads(dout, "dout", shape_q, device)
@@ -800,14 +836,26 @@ def attention_backward(dout, q, k, v, out, lse, cu_seqlens=None, causal=True, wi
     tdq = _heads(dq, "dq", shape_q, device)
     tdk = _heads(dk, "dk", shape_k, device)
     tdv = _heads(dv, "dv", shape_k, device)
+    scores = _attn_scores(problem, softcap, slopes, prefix_lens, device)
+    if dslopes is not None and slopes is None:
+        raise ValueError("dslopes needs slopes")
     # less than 0 for a problem that the call below refuses, with the reason
-    nbytes = max(0, load_library().attn_backward_workspace_bytes(_PROBLEM.pack(*problem)))
+    if scores is None:
+        nbytes = max(0, load_library().attn_backward_workspace_bytes(_PROBLEM.pack(*problem)))
+    else:
+        pd = 0 if dslopes is None else _vector(dslopes, "dslopes", device, shape_q[1])
+        nbytes = max(0, load_library().attn_scored_backward_workspace_bytes(_PROBLEM.pack(*problem), 1 if pd else 0))
     # scratch of this call's own: two captured graphs share nothing
     scratch = q.new_empty((nbytes // 4,)) if nbytes else None
-    _call_packed("attn_backward",
-                 _BACKWARD_ARGS.pack(*problem, *tg, *tq, *tk, *tv, *to, pl, *tdq, *tdk, *tdv,
-                                     scratch.data_ptr() if nbytes else 0, nbytes), device)
-    return dq, dk, dv
+    ps = scratch.data_ptr() if nbytes else 0
+    if scores is None:
+        _call_packed("attn_backward",
+                     _BACKWARD_ARGS.pack(*problem, *tg, *tq, *tk, *tv, *to, pl, *tdq, *tdk, *tdv, ps, nbytes), device)
+        return dq, dk, dv
+    _call_packed("attn_scored_backward",
+                 _SCORED_BACKWARD_ARGS.pack(*problem, *scores, *tg, *tq, *tk, *tv, *to, pl, *tdq, *tdk, *tdv, pd, ps,
+                                            nbytes), device)
+    return (dq, dk, dv) if dslopes is None else (dq, dk, dv, dslopes)
 
 
 def _vector(t, name, device, n=None):
