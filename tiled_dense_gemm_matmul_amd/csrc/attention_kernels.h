@@ -82,12 +82,10 @@ struct Problem {
     int first;       // workgroups in front of this launch's
     float scale, c;  // c = scale log2(e): scores go through exp2
     float factor;    // of dq and dk: the call's scale
-    // SC: the scores are final before the softmax, and scale is 1
-    const float *slopes;  // [hq], or NULL
-    const int *prefix;    // [nseq], or NULL
-    float bend;           // raw scores to the argument of the tanh, or to the score without a cap
-    float cap, per_cap;   // 0: none; 1 / cap
-    float tanh[5];        // cap tanh(x) / x in powers of x^2, |x| <= kSmall
+    // SC: with a cap the raw scores are tanh(bend q.k) and scale is the cap
+    const int *prefix;  // [nseq], or NULL
+    float bend;         // the call's scale over its cap; 0: no cap
+    float per_scale;    // 1 / scale: slopes in units of the raw scores
 };
 
 // A row's lse from the sum of exp2(s c - top) over its raw scores s and the
@@ -107,68 +105,89 @@ __device__ __forceinline__ float lse_of(const Problem &p, float sum, float top, 
 // The probability of a raw score in the backward pass.  The score is rounded
 // as in lse_of before lse is taken from it: two instructions a score more than
 // one multiply-add with scale log2(e).
-template <bool SC>
 __device__ __forceinline__ float probability(const Problem &p, float s, float lse) {
 #pragma clang fp contract(off)
-    const float score = SC ? s : s * p.scale;
+    const float score = s * p.scale;
     return __builtin_amdgcn_exp2f((score - lse) * kLog2e);
 }
 
-// cap tanh(x) for |x| up to kSmall is x times a polynomial in x^2, whose
-// coefficients (a minimax fit, off by a quarter of fp32's rounding) carry the
-// cap: 7 instructions with x itself.  A block of scores that all lie in there,
-// as most do under a cap of a few times their size, takes no exponential; in
-// others the rest of the scores take 1 - 2 / (1 + exp(2 |x|)), good to 3
-// roundings from there on.  `steep` gets the derivative 1 - tanh(x)^2.
+// tanh(x) for |x| up to kSmall is x times a polynomial in x^2 (a minimax fit,
+// off by a quarter of fp32's rounding).  A block of scores that all lie in
+// there, as most do under a cap of a few times their size, takes no
+// exponential; in others the rest of the scores take 1 - 2 / (1 + exp(2 |x|)),
+// good to 3 roundings from there on.
 constexpr float kSmall = 0.5f;
-constexpr double kTanh[5] = {1.0, -0.33333143893843536, 0.13325878887208747, -0.053045488615601204,
-                             0.0172414780429774};
+__device__ __forceinline__ float small_tanh(float x) {
+    const float y = x * x;
+    const float f = fmaf(fmaf(fmaf(0.0172414780429774f, y, -0.053045488615601204f), y, 0.13325878887208747f), y,
+                         -0.33333143893843536f);
+    return x * fmaf(f, y, 1.0f);
+}
 
-// The final scores of the 16 x 16 blocks s, whose lane holds keys (or rows)
-// at the distances |away[b] - i| from its row (or key).  Both passes form
-// them by the same instructions, so they agree to the bit.
+// a where mask is -1, b where it is 0, without a branch over a's exponential.
+__device__ __forceinline__ float choose(int mask, float a, float b) {
+    return __builtin_bit_cast(float, (__builtin_bit_cast(int, a) & mask) | (__builtin_bit_cast(int, b) & ~mask));
+}
+
+// Bends the 16 x 16 blocks s of q.k by the cap and takes the bias from them,
+// all in units of scale, so that what follows is the same for every form: a
+// score costs 7 instructions with a cap and 2 with a bias.  A lane holds keys
+// (or rows) at the distances |away[b] - i| from its row (or key); `slope` is
+// in units of scale too, and `steep` gets the derivative 1 - tanh^2.  Both
+// passes take the same steps, so their scores agree to the bit.
 template <int RB, bool GRAD>
-__device__ __forceinline__ void final_scores(const Problem &p, float slope, const float (&away)[RB], f32x4 (&s)[RB],
-                                             f32x4 (&steep)[RB]) {
+__device__ __forceinline__ void bend_scores(float bend, bool biased, float slope, const float (&away)[RB],
+                                            f32x4 (&s)[RB], f32x4 (&steep)[RB]) {
 #pragma clang fp contract(off)
-    float most = 0.0f;
+    if (bend > 0.0f) {
+        float most = 0.0f;
 #pragma unroll
-    for (int b = 0; b < RB; ++b)
+        for (int b = 0; b < RB; ++b) {
+            s[b] *= bend;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            s[b][i] *= p.bend;
-            most = fmaxf(most, fabsf(s[b][i]));
+            for (int i = 0; i < 4; ++i) most = fmaxf(most, fabsf(s[b][i]));
         }
-    if (p.cap > 0.0f) {
-        const bool small = !__any(most > kSmall);
+        if (!__any(most > kSmall)) {
 #pragma unroll
-        for (int b = 0; b < RB; ++b)
+            for (int b = 0; b < RB; ++b)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float x = s[b][i], y = x * x;
-                const float f = fmaf(fmaf(fmaf(fmaf(p.tanh[4], y, p.tanh[3]), y, p.tanh[2]), y, p.tanh[1]), y, p.tanh[0]);
-                float t = x * f, d = 0.0f;
-                if (GRAD) {
-                    const float u = t * p.per_cap;
-                    d = fmaf(-u, u, 1.0f);
+                for (int i = 0; i < 4; ++i) {
+                    const float t = small_tanh(s[b][i]);
+                    s[b][i] = t;
+                    if (GRAD) steep[b][i] = fmaf(-t, t, 1.0f);
                 }
-                if (!small) {
+        } else {
+#pragma unroll
+            for (int b = 0; b < RB; ++b) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float x = s[b][i];
+                    // an unknown value from here on, or both sides would be
+                    // computed for every block and one of them chosen
+                    asm volatile("" : "+v"(x));
+                    const float t = small_tanh(x);
                     const float e = __builtin_amdgcn_exp2f(fabsf(x) * (-2.0f * kLog2e));
                     const float r = __builtin_amdgcn_rcpf(1.0f + e);
-                    const bool far = fabsf(x) > kSmall;
-                    t = far ? copysignf((1.0f - e) * r * p.cap, x) : t;
-                    if (GRAD) d = far ? 4.0f * e * r * r : d;
+                    const int far = fabsf(x) > kSmall ? -1 : 0;
+                    s[b][i] = choose(far, copysignf((1.0f - e) * r, x), t);
+                    if (GRAD) steep[b][i] = choose(far, 4.0f * e * r * r, fmaf(-t, t, 1.0f));
                 }
-                s[b][i] = t;
-                if (GRAD) steep[b][i] = d;
+                __builtin_amdgcn_sched_barrier(0);  // one block's temporaries at a time
             }
+        }
     }
-    if (p.slopes) {
+    if (biased) {
 #pragma unroll
         for (int b = 0; b < RB; ++b)
 #pragma unroll
             for (int i = 0; i < 4; ++i) s[b][i] = fmaf(-slope, fabsf(away[b] - (float)i), s[b][i]);
     }
+}
+// What no kernel of a call writes, for scalar loads at uniform places.
+template <class T>
+using Constant = const __attribute__((address_space(4))) T *;
+__device__ __forceinline__ float slope_of(const float *slopes, float per_scale, int h) {
+    return slopes ? ((Constant<float>)slopes)[h] * per_scale : 0.0f;
 }
 
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
@@ -489,7 +508,7 @@ struct Range {
 // The row behind the prefix of a tile's sequence, whose keys all of its rows see.
 template <bool SC>
 __device__ __forceinline__ int prefix_end(const Problem &p, const Tile &t) {
-    return SC && p.prefix ? t.s0 + min(max(uniform(p.prefix[t.seq]), 0), t.s1 - t.s0) : t.s0;
+    return SC && p.prefix ? t.s0 + min(max(((Constant<int>)p.prefix)[t.seq], 0), t.s1 - t.s0) : t.s0;
 }
 template <bool SC>
 __device__ __forceinline__ Range keys_of(const Problem &p, int s0, int s1, int pe, int r, int n) {
@@ -531,7 +550,7 @@ __device__ __forceinline__ bool all_see(const Problem &p, int s1, int pe, int r,
 // the rescaling.
 template <int DP, bool EX, int RB, int WS, bool SC>
 __global__ __launch_bounds__(256, DP <= 64 ? 4 : 2) void attention_fwd(Problem p, Strided q, Strided k, Strided v, Strided o,
-                                                        float *lse) {
+                                                        float *lse, const float *slopes) {
     constexpr int WROWS = 16 * RB, WR = 4 / WS, TILE = WR * WROWS;
     const int lane = threadIdx.x & 63, g = lane >> 4, m = lane & 15;
     const int wave = uniform(threadIdx.x >> 6);
@@ -562,7 +581,8 @@ __global__ __launch_bounds__(256, DP <= 64 ? 4 : 2) void attention_fwd(Problem p
     const Range kr = keys_of<SC>(p, s0, s1, pe, r0, WROWS);
     const int step = 16 * WS;
     int kb = kr.lo + 16 * part_of;
-    const float slope = SC && p.slopes ? p.slopes[h] : 0.0f;
+    const float bend = p.bend, slope = SC ? slope_of(slopes, p.per_scale, h) : 0.0f;
+    const bool biased = slopes != nullptr;
     // The values of a block are asked for when its scores begin, the keys of
     // the next one when they are done, so each load has a product to arrive under.
     Rows<DP> K;
@@ -582,7 +602,7 @@ __global__ __launch_bounds__(256, DP <= 64 ? 4 : 2) void attention_fwd(Problem p
             f32x4 steep[RB];
 #pragma unroll
             for (int b = 0; b < RB; ++b) away[b] = (float)(r0 + 16 * b + m - kb - 4 * g);
-            final_scores<RB, false>(p, slope, away, s, steep);
+            bend_scores<RB, false>(bend, biased, slope, away, s, steep);
         }
         if (!all_see<SC>(p, s1, pe, r0, WROWS, kb, 16)) {
 #pragma unroll
@@ -711,6 +731,9 @@ __device__ __forceinline__ void join_rows(const Acc<DP> &acc, float *part, const
 // keys, the rest dq of a tile of rows, longest tiles first in both, so that
 // the shorter dq tiles fill what the others leave of the chip.
 //
+// The slopes (SC) come as [hq], or NULL, and the sums for their gradient go to
+// slope_parts, [hq, tiles of rows, 4 waves], or NULL.
+//
 // delta = dout . out of every row is needed by both parts.  A kernel in front
 // writes it to memory once, or, where a launch counts for more, each part
 // forms it for itself (OWN), which costs the walk over rows a quarter more
@@ -729,7 +752,6 @@ constexpr int kStagedWidth = 64;
 struct Backward {
     Strided dout, q, k, v, o, dq, dk, dv;
     const float *lse, *delta;
-    double *slope_parts;  // SC: [hq, tiles of rows, 4 waves] sums for the slopes' gradient, or NULL
 };
 
 // dout . out of 16 rows: row m's in lanes (g, m).
@@ -760,7 +782,8 @@ __global__ __launch_bounds__(256) void attention_delta(Problem p, Strided dout, 
 }
 
 template <int DP, bool EX, int RB, int WS, bool OWN, bool SC>
-__device__ __forceinline__ void backward_dq(const Problem &p, const Backward &a, int id, int tiles, float *shared) {
+__device__ __forceinline__ void backward_dq(const Problem &p, const Backward &a, int id, float *shared, int tiles,
+                                            const float *slopes, double *slope_parts) {
     const Strided &dout = a.dout, &q = a.q, &k = a.k, &v = a.v, &o = a.o, &dq = a.dq;
     const float *lse = a.lse;
     constexpr int WROWS = 16 * RB, WR = 4 / WS, TILE = WR * WROWS;
@@ -770,13 +793,14 @@ __device__ __forceinline__ void backward_dq(const Problem &p, const Backward &a,
     head_and_tile(id, p.hq, p.group, h, x);
     const Tile t = find_tile<TILE>(p, x, p.causal);
     outside_rows<TILE>(p, t, x, [&](int r) { zero_row(dq.p + r * dq.st + h * dq.sh, p.d); });
-    double *slope_part = SC && a.slope_parts ? a.slope_parts + ((int64_t)h * tiles + x) * 4 + wave : nullptr;
+    double *slope_part = SC && slope_parts ? slope_parts + ((int64_t)h * tiles + x) * 4 + wave : nullptr;
     if (SC && slope_part && lane == 0) *slope_part = 0.0;
     if (t.r0 < 0) return;
     const int s0 = t.s0, s1 = t.s1, t0 = t.r0, pe = prefix_end<SC>(p, t);
     const int part_of = wave / WR, r0 = t0 + wave % WR * WROWS;
     if (WS == 1 && r0 >= s1) return;
-    const float slope = SC && p.slopes ? p.slopes[h] : 0.0f;
+    const float bend = p.bend, slope = SC ? slope_of(slopes, p.per_scale, h) : 0.0f;
+    const bool biased = slopes != nullptr;
     double slope_sum = 0.0;
     const float *kp = k.p + (h / p.group) * k.sh, *vp = v.p + (h / p.group) * v.sh;
 
@@ -828,18 +852,18 @@ __device__ __forceinline__ void backward_dq(const Problem &p, const Backward &a,
         if (SC) {
 #pragma unroll
             for (int b = 0; b < RB; ++b) away[b] = (float)(r0 + 16 * b + m - kb - 4 * g);
-            final_scores<RB, true>(p, slope, away, s, steep);
+            bend_scores<RB, true>(bend, biased, slope, away, s, steep);
         }
 #pragma unroll
         for (int b = 0; b < RB; ++b) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                s[b][i] = probability<SC>(p, s[b][i], l[b]) * (dp[b][i] - del[b]);
+                s[b][i] = probability(p, s[b][i], l[b]) * (dp[b][i] - del[b]);
             if (!whole) {
                 const Range seen = keys_of<SC>(p, s0, s1, pe, r0 + 16 * b + m, 1);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) s[b][i] = inside(seen, kb + 4 * g + i) ? s[b][i] : 0.0f;
-                if (SC && p.cap > 0.0f) {
+                if (SC && bend > 0.0f) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) steep[b][i] = inside(seen, kb + 4 * g + i) ? steep[b][i] : 0.0f;
                 }
@@ -850,7 +874,7 @@ __device__ __forceinline__ void backward_dq(const Problem &p, const Backward &a,
                 for (int i = 0; i < 4; ++i) sum = fmaf(s[b][i], fabsf(away[b] - (float)i), sum);
                 slope_sum += r0 + 16 * b + m < s1 ? (double)sum : 0.0;  // rows past the sequence hold anything
             }
-            if (SC && p.cap > 0.0f) s[b] *= steep[b];
+            if (SC && bend > 0.0f) s[b] *= steep[b];
             A[b].add(T, s[b]);
         }
         if (!STAGED) {
@@ -883,7 +907,8 @@ __device__ __forceinline__ void backward_dq(const Problem &p, const Backward &a,
 // dk and dv: the keys are held fixed and the blocks of 16 rows of every query
 // head of the group are walked over.
 template <int DP, bool EX, int RB, int WS, bool OWN, bool SC>
-__device__ __forceinline__ void backward_dkv(const Problem &p, const Backward &a, int id, float *shared) {
+__device__ __forceinline__ void backward_dkv(const Problem &p, const Backward &a, int id, float *shared,
+                                             const float *slopes) {
     const Strided &dout = a.dout, &q = a.q, &k = a.k, &v = a.v, &o = a.o, &dk = a.dk, &dv = a.dv;
     const float *lse = a.lse;
     constexpr int WROWS = 16 * RB, WR = 4 / WS, TILE = WR * WROWS;
@@ -926,10 +951,10 @@ __device__ __forceinline__ void backward_dkv(const Problem &p, const Backward &a
     f32x4 l4, d4;
     const float *qp, *gp, *op;
     int r;
-    float slope = 0.0f;
+    const float bend = p.bend, per_scale = p.per_scale;
+    const bool biased = slopes != nullptr;
     auto at = [&]() {
         const int head = h * p.group + qh;
-        if (SC && p.slopes) slope = p.slopes[head];
         const bool in = n < total;
         qp = q.p + head * q.sh;
         gp = dout.p + head * dout.sh;
@@ -953,7 +978,7 @@ __device__ __forceinline__ void backward_dkv(const Problem &p, const Backward &a
     while (n < total) {
         const int row = r;
         const float *qc = qp, *gc = gp;
-        const float slope_c = slope;
+        const float slope = SC ? slope_of(slopes, per_scale, h * p.group + uniform(qh)) : 0.0f;
         if (STAGED) {
             Q.stage(staged);
             G.stage(staged_g);
@@ -996,16 +1021,16 @@ __device__ __forceinline__ void backward_dkv(const Problem &p, const Backward &a
             float away[RB];
 #pragma unroll
             for (int b = 0; b < RB; ++b) away[b] = (float)(k0 + 16 * b + m - row - 4 * g);
-            final_scores<RB, true>(p, slope_c, away, s, steep);
+            bend_scores<RB, true>(bend, biased, slope, away, s, steep);
         }
 #pragma unroll
         for (int b = 0; b < RB; ++b) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                s[b][i] = probability<SC>(p, s[b][i], l4[i]);
+                s[b][i] = probability(p, s[b][i], l4[i]);
                 dp[b][i] = s[b][i] * (dp[b][i] - d4[i]);
             }
-            if (SC && p.cap > 0.0f) dp[b] *= steep[b];
+            if (SC && bend > 0.0f) dp[b] *= steep[b];
             if (!whole) {
                 const Range seen = rows_of<SC>(p, s0, s1, pe, k0 + 16 * b + m, 1);
 #pragma unroll
@@ -1064,12 +1089,13 @@ __device__ __forceinline__ void backward_dkv(const Problem &p, const Backward &a
 
 template <int DP, bool EX, int RBQ, int RBK, int WS, bool OWN, bool SC>
 __global__ __launch_bounds__(256, DP >= 96 && (RBQ == 2 || RBK == 2) ? 1 : 2) void attention_bwd(Problem p, Backward a,
-                                                                                              int key_groups, int tiles) {
+                                                                                              int key_groups, int tiles, const float *slopes,
+                                                                                              double *slope_parts) {
     // the waves' turned rows, and in the end what they join
     __shared__ __align__(16) float shared[(DP <= kStagedWidth ? 8 : 4) * 16 * (DP + 4)];
     const int id = p.first + (int)blockIdx.x;
-    if (id < key_groups) backward_dkv<DP, EX, RBK, WS, OWN, SC>(p, a, id, shared);
-    else backward_dq<DP, EX, RBQ, WS, OWN, SC>(p, a, id - key_groups, tiles, shared);
+    if (id < key_groups) backward_dkv<DP, EX, RBK, WS, OWN, SC>(p, a, id, shared, slopes);
+    else backward_dq<DP, EX, RBQ, WS, OWN, SC>(p, a, id - key_groups, shared, tiles, slopes, slope_parts);
 }
 
 // The slopes' gradients: a workgroup adds a head's parts, a thread every 256th
@@ -1129,6 +1155,8 @@ int check_scores(const attn_problem &p, const attn_scores &s) {
         const float bend = (float)(p.scale / s.softcap);
         if (!(bend >= 0x1p-126f) || !std::isfinite(bend)) return GEMM_ERR_DTYPE;
     }
+    // a bias is taken in units of scale: one of up to 2^30 stays finite
+    if (s.softcap == 0.0 && s.slopes && !(p.scale >= 1e-20)) return GEMM_ERR_DTYPE;
     if (s.prefix_lens && !p.causal) return GEMM_ERR_DTYPE;
     return aligned(s.slopes, 4) && aligned(s.prefix_lens, 4) ? GEMM_OK : GEMM_ERR_ALIGN;
 }
@@ -1152,7 +1180,7 @@ struct Shared {
     }
 };
 
-Problem device_problem(const attn_problem &a, const attn_scores &s, bool scored) {
+Problem device_problem(const attn_problem &a, const attn_scores &s) {
     Problem p;
     p.cu = a.cu_seqlens;
     p.nseq = a.cu_seqlens ? (int)a.num_seqs : 1;
@@ -1164,14 +1192,12 @@ Problem device_problem(const attn_problem &a, const attn_scores &s, bool scored)
     p.window = a.window < a.tokens ? (int)a.window : 0;  // a wider window hides nothing
     p.first = 0;
     p.factor = (float)a.scale;
-    p.scale = scored ? 1.0f : p.factor;
-    p.c = folded(scored ? 1.0 : a.scale);
-    p.slopes = s.slopes;
+    const double scale = s.softcap > 0.0 ? s.softcap : a.scale;
+    p.scale = (float)scale;
+    p.c = folded(scale);
     p.prefix = s.prefix_lens;
-    p.cap = (float)s.softcap;
-    p.bend = (float)(s.softcap > 0.0 ? a.scale / s.softcap : a.scale);
-    p.per_cap = s.softcap > 0.0 ? (float)(1.0 / s.softcap) : 0.0f;
-    for (int i = 0; i < 5; ++i) p.tanh[i] = (float)(s.softcap * kTanh[i]);
+    p.bend = s.softcap > 0.0 ? (float)(a.scale / s.softcap) : 0.0f;
+    p.per_scale = (float)(1.0 / scale);
     return p;
 }
 
@@ -1287,7 +1313,7 @@ int forward(const Args &a, const attn_scores &scores, void *stream) {
         in_range(k, a.lse, lse_bytes, T, D) || in_range(v, a.lse, lse_bytes, T, D) ||
         shared.meets(o, a.p) || shared.meets({a.lse, lse_bytes}))
         return GEMM_ERR_ALIAS;
-    Problem p = device_problem(a.p, scores, SC);
+    Problem p = device_problem(a.p, scores);
     const Plan how = plan_forward(a.p);
     const int64_t grid = tiles_of(a.p, how.rows()) * a.p.q_heads;
     if (grid >= ((int64_t)1 << 31)) return GEMM_ERR_SHAPE;
@@ -1297,7 +1323,8 @@ int forward(const Args &a, const attn_scores &scores, void *stream) {
     return in_slices(grid, 256, [&](int64_t first, unsigned count) {
         p.first = (int)first;
 #define FWD_AS(DP, EX, RB, WS) \
-    hipLaunchKernelGGL((attention_fwd<DP, EX, RB, WS, SC>), dim3(count), dim3(256), 0, hs, p, sq, sk, sv, so, a.lse)
+    hipLaunchKernelGGL((attention_fwd<DP, EX, RB, WS, SC>), dim3(count), dim3(256), 0, hs, p, sq, sk, sv, so, a.lse, \
+                       scores.slopes)
 #define FWD(DP, EX)                           \
     do {                                      \
         if (how.ws == 1) FWD_AS(DP, EX, 2, 1); \
@@ -1377,7 +1404,7 @@ int backward(const Args &a, const attn_scores &scores, float *dslopes, void *str
             if (overlap(res[i], res[j], T, D)) return GEMM_ERR_ALIAS;
         if (in_range(res[i], a.lse, row_bytes, T, D) || shared.meets(res[i], a.p)) return GEMM_ERR_ALIAS;
     }
-    Problem p = device_problem(a.p, scores, SC);
+    Problem p = device_problem(a.p, scores);
     const Plan keys = own ? Plan{1, 4} : plan_keys(a.p), rows = own ? keys : plan_rows(a.p);
     // whole turns of the 8 XCDs, so that the second part's heads keep to theirs
     const int64_t nk = (tiles_of(a.p, keys.rows()) * HK + 7) / 8 * 8, tiles = tiles_of(a.p, rows.rows()),
@@ -1385,9 +1412,9 @@ int backward(const Args &a, const attn_scores &scores, float *dslopes, void *str
     if (grid >= ((int64_t)1 << 31) || (HQ * T + 15) / 16 >= ((int64_t)1 << 31)) return GEMM_ERR_SHAPE;
     const Backward b = {strided(a.dout, T, HQ), strided(a.q, T, HQ),  strided(a.k, T, HK),  strided(a.v, T, HK),
                         strided(a.out, T, HQ),  strided(a.dq, T, HQ), strided(a.dk, T, HK), strided(a.dv, T, HK),
-                        a.lse, static_cast<const float *>(a.workspace),
-                        need.parts > 0 ? reinterpret_cast<double *>(static_cast<char *>(a.workspace) + need.delta_bytes)
-                                       : nullptr};
+                        a.lse, static_cast<const float *>(a.workspace)};
+    double *parts = need.parts > 0 ? reinterpret_cast<double *>(static_cast<char *>(a.workspace) + need.delta_bytes)
+                                   : nullptr;
     if (!own) {
         // the main kernel reads what this one writes
         st = in_slices((HQ * T + 15) / 16, 256, [&](int64_t first, unsigned count) {
@@ -1399,7 +1426,8 @@ int backward(const Args &a, const attn_scores &scores, float *dslopes, void *str
     st = in_slices(grid, 256, [&](int64_t first, unsigned count) {
         p.first = (int)first;
 #define BWD_AS(DP, EX, RBQ, RBK, WS, OWN) \
-    hipLaunchKernelGGL((attention_bwd<DP, EX, RBQ, RBK, WS, OWN, SC>), dim3(count), dim3(256), 0, hs, p, b, (int)nk, (int)tiles)
+    hipLaunchKernelGGL((attention_bwd<DP, EX, RBQ, RBK, WS, OWN, SC>), dim3(count), dim3(256), 0, hs, p, b, (int)nk, (int)tiles, \
+                       scores.slopes, parts)
 #define BWD(DP, EX)                                              \
     do {                                                         \
         if (own) BWD_AS(DP, EX, 1, 1, 4, true);                  \
@@ -1413,7 +1441,7 @@ int backward(const Args &a, const attn_scores &scores, float *dslopes, void *str
 #undef BWD_AS
     });
     if (st != GEMM_OK || need.parts == 0) return st;
-    hipLaunchKernelGGL(attention_slopes, dim3((unsigned)HQ), dim3(256), 0, hs, b.slope_parts, need.parts, dslopes);
+    hipLaunchKernelGGL(attention_slopes, dim3((unsigned)HQ), dim3(256), 0, hs, parts, need.parts, dslopes);
     return hipGetLastError() == hipSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
 }
 
