@@ -16,10 +16,10 @@ SRC = os.path.join(PKG, "csrc", "gemm_fwd.hip")
 LOSS_SRC = os.path.join(PKG, "csrc", "loss.hip")
 ACT_SRC = os.path.join(PKG, "csrc", "activation.hip")
 ATTN_SRC = os.path.join(PKG, "csrc", "attention.hip")
-SCORES_SRC = os.path.join(PKG, "csrc", "attention_scores.hip")
+SCORES_SRCS = [os.path.join(PKG, "csrc", f"attention_{form}.hip") for form in ("scores", "bias", "cap", "cap_bias")]
 NORM_SRC = os.path.join(PKG, "csrc", "qk_norm_rope.hip")
 BLOCK_SRC = os.path.join(PKG, "csrc", "block_norm.hip")
-SRCS = [SRC, LOSS_SRC, ACT_SRC, ATTN_SRC, SCORES_SRC, NORM_SRC, BLOCK_SRC]
+SRCS = [SRC, LOSS_SRC, ACT_SRC, ATTN_SRC, *SCORES_SRCS, NORM_SRC, BLOCK_SRC]
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libgemmfwd.so")
 SYNC_LIB = os.path.join(PKG, "libgemmfwd_sync.so")

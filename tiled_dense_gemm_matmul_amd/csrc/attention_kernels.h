@@ -42,10 +42,13 @@
 // rate of a large fp32 product on this card, with the MFMAs busy 83% of the
 // time.
 //
-// The same kernels serve both forms of attention: attention.hip builds them as
-// they are (SC false), attention_scores.hip with scores that are capped,
-// biased by distance or masked with a prefix (SC true), which only changes
-// what is between the two products of a block.
+// The same kernels serve every form of scores: FORM 0 is plain, kPrefix the
+// mask with a prefix, kBias the bias by distance and kCap the cap, the latter
+// two with or without a prefix.  They only change what is between the two
+// products of a block.  The form is a template argument because each of these
+// steps behind a branch made the compiler copy a block's scores from register
+// to register: 16 x 512 tokens, 12 heads of 64, backward, prefixes of no rows,
+// took 256 us that way and 230 as FORM 0.
 #ifndef ATTENTION_KERNELS_H
 #define ATTENTION_KERNELS_H
 
@@ -69,6 +72,8 @@ typedef unsigned int u32x2v __attribute__((vector_size(8)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef __amdgpu_buffer_rsrc_t Rsrc;
 
+constexpr int kPrefix = 1, kBias = 2, kCap = 4;  // bits of FORM
+
 constexpr int kOOB = (int)0x80000000u;  // past every descriptor's end (they end below 2^31)
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
@@ -82,9 +87,9 @@ struct Problem {
     int first;       // workgroups in front of this launch's
     float scale, c;  // c = scale log2(e): scores go through exp2
     float factor;    // of dq and dk: the call's scale
-    // SC: with a cap the raw scores are tanh(bend q.k) and scale is the cap
+    // kCap: the raw scores are tanh(bend q.k) and scale is the cap
     const int *prefix;  // [nseq], or NULL
-    float bend;         // the call's scale over its cap; 0: no cap
+    float bend;         // the call's scale over its cap
     float per_scale;    // 1 / scale: slopes in units of the raw scores
 };
 
@@ -135,11 +140,11 @@ __device__ __forceinline__ float choose(int mask, float a, float b) {
 // (or rows) at the distances |away[b] - i| from its row (or key); `slope` is
 // in units of scale too, and `steep` gets the derivative 1 - tanh^2.  Both
 // passes take the same steps, so their scores agree to the bit.
-template <int RB, bool GRAD>
-__device__ __forceinline__ void bend_scores(float bend, bool biased, float slope, const float (&away)[RB],
-                                            f32x4 (&s)[RB], f32x4 (&steep)[RB]) {
+template <int FORM, int RB, bool GRAD>
+__device__ __forceinline__ void bend_scores(float bend, float slope, const float (&away)[RB], f32x4 (&s)[RB],
+                                            f32x4 (&steep)[RB]) {
 #pragma clang fp contract(off)
-    if (bend > 0.0f) {
+    if constexpr (FORM & kCap) {
         float most = 0.0f;
 #pragma unroll
         for (int b = 0; b < RB; ++b) {
@@ -171,12 +176,12 @@ __device__ __forceinline__ void bend_scores(float bend, bool biased, float slope
                     const int far = fabsf(x) > kSmall ? -1 : 0;
                     s[b][i] = choose(far, copysignf((1.0f - e) * r, x), t);
                     if (GRAD) steep[b][i] = choose(far, 4.0f * e * r * r, fmaf(-t, t, 1.0f));
+                    if (i % 2) __builtin_amdgcn_sched_barrier(0);  // two scores' temporaries at a time
                 }
-                __builtin_amdgcn_sched_barrier(0);  // one block's temporaries at a time
             }
         }
     }
-    if (biased) {
+    if constexpr (FORM & kBias) {
 #pragma unroll
         for (int b = 0; b < RB; ++b)
 #pragma unroll
@@ -187,7 +192,7 @@ __device__ __forceinline__ void bend_scores(float bend, bool biased, float slope
 template <class T>
 using Constant = const __attribute__((address_space(4))) T *;
 __device__ __forceinline__ float slope_of(const float *slopes, float per_scale, int h) {
-    return slopes ? ((Constant<float>)slopes)[h] * per_scale : 0.0f;
+    return ((Constant<float>)slopes)[h] * per_scale;
 }
 
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
@@ -506,11 +511,11 @@ struct Range {
     int lo, hi;
 };
 // The row behind the prefix of a tile's sequence, whose keys all of its rows see.
-template <bool SC>
+template <bool PREFIX>
 __device__ __forceinline__ int prefix_end(const Problem &p, const Tile &t) {
-    return SC && p.prefix ? t.s0 + min(max(((Constant<int>)p.prefix)[t.seq], 0), t.s1 - t.s0) : t.s0;
+    return PREFIX && p.prefix ? t.s0 + min(max(((Constant<int>)p.prefix)[t.seq], 0), t.s1 - t.s0) : t.s0;
 }
-template <bool SC>
+template <bool PREFIX>
 __device__ __forceinline__ Range keys_of(const Problem &p, int s0, int s1, int pe, int r, int n) {
     const int last = min(r + n, s1) - 1;
     Range k = {s0, s1};
@@ -518,10 +523,10 @@ __device__ __forceinline__ Range keys_of(const Problem &p, int s0, int s1, int p
         k.lo = max(s0, r - p.window + 1);
         if (s1 - last > p.window) k.hi = last + p.window;
     }
-    if (p.causal) k.hi = SC ? min(k.hi, max(last + 1, pe)) : last + 1;
+    if (p.causal) k.hi = PREFIX ? min(k.hi, max(last + 1, pe)) : last + 1;
     return k;
 }
-template <bool SC>
+template <bool PREFIX>
 __device__ __forceinline__ Range rows_of(const Problem &p, int s0, int s1, int pe, int k, int n) {
     const int last = min(k + n, s1) - 1;
     Range r = {s0, s1};
@@ -529,15 +534,15 @@ __device__ __forceinline__ Range rows_of(const Problem &p, int s0, int s1, int p
         r.lo = max(s0, k - p.window + 1);
         if (s1 - last > p.window) r.hi = last + p.window;
     }
-    if (p.causal && !(SC && k < pe)) r.lo = k;
+    if (p.causal && !(PREFIX && k < pe)) r.lo = k;
     return r;
 }
 __device__ __forceinline__ bool inside(Range r, int x) { return (unsigned)(x - r.lo) < (unsigned)(r.hi - r.lo); }
 // Whether rows [r, r + n) of the sequence all see keys [k, k + m), both whole inside it.
-template <bool SC>
+template <bool PREFIX>
 __device__ __forceinline__ bool all_see(const Problem &p, int s1, int pe, int r, int n, int k, int m) {
     if (r + n > s1 || k + m > s1) return false;
-    if (p.causal && k + m - 1 > (SC ? max(r, pe - 1) : r)) return false;
+    if (p.causal && k + m - 1 > (PREFIX ? max(r, pe - 1) : r)) return false;
     return !p.window || ((int64_t)r + n - 1 - k < p.window && (int64_t)k + m - 1 - r < p.window);
 }
 
@@ -548,8 +553,15 @@ __device__ __forceinline__ bool all_see(const Problem &p, int s1, int pe, int r,
 // probabilities then stay below 2^8 of the reference, which fp32 holds
 // without loss, and most blocks need neither the maximum across lanes nor
 // the rescaling.
-template <int DP, bool EX, int RB, int WS, bool SC>
-__global__ __launch_bounds__(256, DP <= 64 ? 4 : 2) void attention_fwd(Problem p, Strided q, Strided k, Strided v, Strided o,
+//
+// Four waves a SIMD leave each 128 registers, which two blocks of rows of
+// heads of 64 fill; the cap's steps spill some of the loads' offsets then, and
+// loading these again waits for the keys in flight.  With a cap those kernels
+// run three waves (cap 50, 12 heads of 64, us with three and with four: 16 x 512
+// tokens 79.6 and 85.5, 64 x 128 tokens 28.3 and 35.2; with a bias too 87.2
+// and 98.3).
+template <int DP, bool EX, int RB, int WS, int FORM>
+__global__ __launch_bounds__(256, DP > 64 ? 2 : DP == 64 && RB == 2 && (FORM & kCap) ? 3 : 4) void attention_fwd(Problem p, Strided q, Strided k, Strided v, Strided o,
                                                         float *lse, const float *slopes) {
     constexpr int WROWS = 16 * RB, WR = 4 / WS, TILE = WR * WROWS;
     const int lane = threadIdx.x & 63, g = lane >> 4, m = lane & 15;
@@ -562,7 +574,7 @@ __global__ __launch_bounds__(256, DP <= 64 ? 4 : 2) void attention_fwd(Problem p
         if (lane == 0) lse[(int64_t)h * p.tokens + r] = -INFINITY;
     });
     if (t.r0 < 0) return;
-    const int s0 = t.s0, s1 = t.s1, pe = prefix_end<SC>(p, t);
+    const int s0 = t.s0, s1 = t.s1, pe = prefix_end<FORM != 0>(p, t);
     const int part_of = wave / WR, r0 = t.r0 + wave % WR * WROWS;
     if (WS == 1 && r0 >= s1) return;
     const float *kp = k.p + (h / p.group) * k.sh, *vp = v.p + (h / p.group) * v.sh;
@@ -578,11 +590,10 @@ __global__ __launch_bounds__(256, DP <= 64 ? 4 : 2) void attention_fwd(Problem p
         sum[b] = 0.0f;
         largest[b] = -INFINITY;
     }
-    const Range kr = keys_of<SC>(p, s0, s1, pe, r0, WROWS);
+    const Range kr = keys_of<FORM != 0>(p, s0, s1, pe, r0, WROWS);
     const int step = 16 * WS;
     int kb = kr.lo + 16 * part_of;
-    const float bend = p.bend, slope = SC ? slope_of(slopes, p.per_scale, h) : 0.0f;
-    const bool biased = slopes != nullptr;
+    const float slope = FORM & kBias ? slope_of(slopes, p.per_scale, h) : 0.0f;
     // The values of a block are asked for when its scores begin, the keys of
     // the next one when they are done, so each load has a product to arrive under.
     Rows<DP> K;
@@ -597,17 +608,17 @@ __global__ __launch_bounds__(256, DP <= 64 ? 4 : 2) void attention_fwd(Problem p
         __builtin_amdgcn_sched_barrier(0);
         K.template load<EX>(rows_rsrc(kp, k.st, kb + step, s1, p.d), k.st, p.d);
         __builtin_amdgcn_sched_barrier(0);
-        if (SC) {
+        if constexpr (FORM & (kBias | kCap)) {
             float away[RB];
             f32x4 steep[RB];
 #pragma unroll
             for (int b = 0; b < RB; ++b) away[b] = (float)(r0 + 16 * b + m - kb - 4 * g);
-            bend_scores<RB, false>(bend, biased, slope, away, s, steep);
+            bend_scores<FORM, RB, false>(p.bend, slope, away, s, steep);
         }
-        if (!all_see<SC>(p, s1, pe, r0, WROWS, kb, 16)) {
+        if (!all_see<FORM != 0>(p, s1, pe, r0, WROWS, kb, 16)) {
 #pragma unroll
             for (int b = 0; b < RB; ++b) {
-                const Range seen = keys_of<SC>(p, s0, s1, pe, r0 + 16 * b + m, 1);
+                const Range seen = keys_of<FORM != 0>(p, s0, s1, pe, r0 + 16 * b + m, 1);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) s[b][i] = inside(seen, kb + 4 * g + i) ? s[b][i] : -INFINITY;
             }
@@ -731,7 +742,7 @@ __device__ __forceinline__ void join_rows(const Acc<DP> &acc, float *part, const
 // keys, the rest dq of a tile of rows, longest tiles first in both, so that
 // the shorter dq tiles fill what the others leave of the chip.
 //
-// The slopes (SC) come as [hq], or NULL, and the sums for their gradient go to
+// The slopes (kBias) come as [hq], or NULL, and the sums for their gradient go to
 // slope_parts, [hq, tiles of rows, 4 waves], or NULL.
 //
 // delta = dout . out of every row is needed by both parts.  A kernel in front
@@ -781,7 +792,7 @@ __global__ __launch_bounds__(256) void attention_delta(Problem p, Strided dout, 
     if (e == 0) delta[(int64_t)h * p.tokens + t] = sum;
 }
 
-template <int DP, bool EX, int RB, int WS, bool OWN, bool SC>
+template <int DP, bool EX, int RB, int WS, bool OWN, int FORM>
 __device__ __forceinline__ void backward_dq(const Problem &p, const Backward &a, int id, float *shared, int tiles,
                                             const float *slopes, double *slope_parts) {
     const Strided &dout = a.dout, &q = a.q, &k = a.k, &v = a.v, &o = a.o, &dq = a.dq;
@@ -793,14 +804,13 @@ __device__ __forceinline__ void backward_dq(const Problem &p, const Backward &a,
     head_and_tile(id, p.hq, p.group, h, x);
     const Tile t = find_tile<TILE>(p, x, p.causal);
     outside_rows<TILE>(p, t, x, [&](int r) { zero_row(dq.p + r * dq.st + h * dq.sh, p.d); });
-    double *slope_part = SC && slope_parts ? slope_parts + ((int64_t)h * tiles + x) * 4 + wave : nullptr;
-    if (SC && slope_part && lane == 0) *slope_part = 0.0;
+    double *slope_part = (FORM & kBias) && slope_parts ? slope_parts + ((int64_t)h * tiles + x) * 4 + wave : nullptr;
+    if ((FORM & kBias) && slope_part && lane == 0) *slope_part = 0.0;
     if (t.r0 < 0) return;
-    const int s0 = t.s0, s1 = t.s1, t0 = t.r0, pe = prefix_end<SC>(p, t);
+    const int s0 = t.s0, s1 = t.s1, t0 = t.r0, pe = prefix_end<FORM != 0>(p, t);
     const int part_of = wave / WR, r0 = t0 + wave % WR * WROWS;
     if (WS == 1 && r0 >= s1) return;
-    const float bend = p.bend, slope = SC ? slope_of(slopes, p.per_scale, h) : 0.0f;
-    const bool biased = slopes != nullptr;
+    const float slope = FORM & kBias ? slope_of(slopes, p.per_scale, h) : 0.0f;
     double slope_sum = 0.0;
     const float *kp = k.p + (h / p.group) * k.sh, *vp = v.p + (h / p.group) * v.sh;
 
@@ -823,7 +833,7 @@ __device__ __forceinline__ void backward_dq(const Problem &p, const Backward &a,
         l[b] = r + m < s1 ? lse[at] : 0.0f;
         A[b].clear();
     }
-    const Range kr = keys_of<SC>(p, s0, s1, pe, r0, WROWS);
+    const Range kr = keys_of<FORM != 0>(p, s0, s1, pe, r0, WROWS);
     const int step = 16 * WS;
     int kb = kr.lo + 16 * part_of;
     constexpr bool STAGED = DP <= kStagedWidth, EARLY = RB == 1;
@@ -846,35 +856,34 @@ __device__ __forceinline__ void backward_dq(const Problem &p, const Backward &a,
         V.template load<EX>(rows_rsrc(vp, v.st, kb + step, s1, p.d), v.st, p.d);
         if (STAGED && !EARLY) T.take(staged);
         __builtin_amdgcn_sched_barrier(0);
-        const bool whole = all_see<SC>(p, s1, pe, r0, WROWS, kb, 16);
+        const bool whole = all_see<FORM != 0>(p, s1, pe, r0, WROWS, kb, 16);
         float away[RB];
         f32x4 steep[RB];
-        if (SC) {
+        if constexpr (FORM & (kBias | kCap)) {
 #pragma unroll
             for (int b = 0; b < RB; ++b) away[b] = (float)(r0 + 16 * b + m - kb - 4 * g);
-            bend_scores<RB, true>(bend, biased, slope, away, s, steep);
+            bend_scores<FORM, RB, true>(p.bend, slope, away, s, steep);
         }
 #pragma unroll
         for (int b = 0; b < RB; ++b) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 s[b][i] = probability(p, s[b][i], l[b]) * (dp[b][i] - del[b]);
+            const f32x4 ds = s[b];  // of the final scores
+            if (FORM & kCap) s[b] *= steep[b];
             if (!whole) {
-                const Range seen = keys_of<SC>(p, s0, s1, pe, r0 + 16 * b + m, 1);
+                const Range seen = keys_of<FORM != 0>(p, s0, s1, pe, r0 + 16 * b + m, 1);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) s[b][i] = inside(seen, kb + 4 * g + i) ? s[b][i] : 0.0f;
-                if (SC && bend > 0.0f) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) steep[b][i] = inside(seen, kb + 4 * g + i) ? steep[b][i] : 0.0f;
-                }
             }
-            if (SC && slope_part) {
+            if ((FORM & kBias) && slope_part) {
+                const Range seen = keys_of<FORM != 0>(p, s0, s1, pe, r0 + 16 * b + m, 1);
                 float sum = 0.0f;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) sum = fmaf(s[b][i], fabsf(away[b] - (float)i), sum);
+                for (int i = 0; i < 4; ++i)
+                    sum += whole || inside(seen, kb + 4 * g + i) ? ds[i] * fabsf(away[b] - (float)i) : 0.0f;
                 slope_sum += r0 + 16 * b + m < s1 ? (double)sum : 0.0;  // rows past the sequence hold anything
             }
-            if (SC && bend > 0.0f) s[b] *= steep[b];
             A[b].add(T, s[b]);
         }
         if (!STAGED) {
@@ -883,7 +892,7 @@ __device__ __forceinline__ void backward_dq(const Problem &p, const Backward &a,
         }
     }
 
-    if (SC && slope_part) {
+    if ((FORM & kBias) && slope_part) {
 #pragma unroll
         for (int i = 1; i < 64; i <<= 1) slope_sum += __shfl_xor(slope_sum, i, 64);
         if (lane == 0) *slope_part = slope_sum;
@@ -906,7 +915,7 @@ __device__ __forceinline__ void backward_dq(const Problem &p, const Backward &a,
 
 // dk and dv: the keys are held fixed and the blocks of 16 rows of every query
 // head of the group are walked over.
-template <int DP, bool EX, int RB, int WS, bool OWN, bool SC>
+template <int DP, bool EX, int RB, int WS, bool OWN, int FORM>
 __device__ __forceinline__ void backward_dkv(const Problem &p, const Backward &a, int id, float *shared,
                                              const float *slopes) {
     const Strided &dout = a.dout, &q = a.q, &k = a.k, &v = a.v, &o = a.o, &dk = a.dk, &dv = a.dv;
@@ -922,7 +931,7 @@ __device__ __forceinline__ void backward_dkv(const Problem &p, const Backward &a
         zero_row(dv.p + r * dv.st + h * dv.sh, p.d);
     });
     if (t.r0 < 0) return;
-    const int s0 = t.s0, s1 = t.s1, t0 = t.r0, pe = prefix_end<SC>(p, t);
+    const int s0 = t.s0, s1 = t.s1, t0 = t.r0, pe = prefix_end<FORM != 0>(p, t);
     const int part_of = wave / WR, k0 = t0 + wave % WR * WROWS;
     if (WS == 1 && k0 >= s1) return;
 
@@ -935,7 +944,7 @@ __device__ __forceinline__ void backward_dkv(const Problem &p, const Backward &a
         DK[b].clear();
         DV[b].clear();
     }
-    const Range rr = rows_of<SC>(p, s0, s1, pe, k0, WROWS);
+    const Range rr = rows_of<FORM != 0>(p, s0, s1, pe, k0, WROWS);
     const int blocks = (rr.hi - rr.lo + 15) / 16, total = blocks * p.group;
     // Block n of the walk: head n % group of the group, and the n / group-th
     // block of rows from the last one on.  Workgroups that start together then
@@ -951,8 +960,6 @@ __device__ __forceinline__ void backward_dkv(const Problem &p, const Backward &a
     f32x4 l4, d4;
     const float *qp, *gp, *op;
     int r;
-    const float bend = p.bend, per_scale = p.per_scale;
-    const bool biased = slopes != nullptr;
     auto at = [&]() {
         const int head = h * p.group + qh;
         const bool in = n < total;
@@ -978,7 +985,7 @@ __device__ __forceinline__ void backward_dkv(const Problem &p, const Backward &a
     while (n < total) {
         const int row = r;
         const float *qc = qp, *gc = gp;
-        const float slope = SC ? slope_of(slopes, per_scale, h * p.group + uniform(qh)) : 0.0f;
+        const float slope = FORM & kBias ? slope_of(slopes, p.per_scale, h * p.group + uniform(qh)) : 0.0f;
         if (STAGED) {
             Q.stage(staged);
             G.stage(staged_g);
@@ -1015,13 +1022,13 @@ __device__ __forceinline__ void backward_dkv(const Problem &p, const Backward &a
             QT.template load<EX>(rows_rsrc(qc, q.st, row, s1, p.d), q.st, p.d);
         }
         __builtin_amdgcn_sched_barrier(0);
-        const bool whole = all_see<SC>(p, s1, pe, row, 16, k0, WROWS);
+        const bool whole = all_see<FORM != 0>(p, s1, pe, row, 16, k0, WROWS);
         f32x4 steep[RB];
-        if (SC) {
+        if constexpr (FORM & (kBias | kCap)) {
             float away[RB];
 #pragma unroll
             for (int b = 0; b < RB; ++b) away[b] = (float)(k0 + 16 * b + m - row - 4 * g);
-            bend_scores<RB, true>(bend, biased, slope, away, s, steep);
+            bend_scores<FORM, RB, true>(p.bend, slope, away, s, steep);
         }
 #pragma unroll
         for (int b = 0; b < RB; ++b) {
@@ -1030,9 +1037,9 @@ __device__ __forceinline__ void backward_dkv(const Problem &p, const Backward &a
                 s[b][i] = probability(p, s[b][i], l4[i]);
                 dp[b][i] = s[b][i] * (dp[b][i] - d4[i]);
             }
-            if (SC && bend > 0.0f) dp[b] *= steep[b];
+            if (FORM & kCap) dp[b] *= steep[b];
             if (!whole) {
-                const Range seen = rows_of<SC>(p, s0, s1, pe, k0 + 16 * b + m, 1);
+                const Range seen = rows_of<FORM != 0>(p, s0, s1, pe, k0 + 16 * b + m, 1);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const bool in = inside(seen, row + 4 * g + i);
@@ -1087,15 +1094,15 @@ __device__ __forceinline__ void backward_dkv(const Problem &p, const Backward &a
     }
 }
 
-template <int DP, bool EX, int RBQ, int RBK, int WS, bool OWN, bool SC>
+template <int DP, bool EX, int RBQ, int RBK, int WS, bool OWN, int FORM>
 __global__ __launch_bounds__(256, DP >= 96 && (RBQ == 2 || RBK == 2) ? 1 : 2) void attention_bwd(Problem p, Backward a,
                                                                                               int key_groups, int tiles, const float *slopes,
                                                                                               double *slope_parts) {
     // the waves' turned rows, and in the end what they join
     __shared__ __align__(16) float shared[(DP <= kStagedWidth ? 8 : 4) * 16 * (DP + 4)];
     const int id = p.first + (int)blockIdx.x;
-    if (id < key_groups) backward_dkv<DP, EX, RBK, WS, OWN, SC>(p, a, id, shared, slopes);
-    else backward_dq<DP, EX, RBQ, WS, OWN, SC>(p, a, id - key_groups, shared, tiles, slopes, slope_parts);
+    if (id < key_groups) backward_dkv<DP, EX, RBK, WS, OWN, FORM>(p, a, id, shared, slopes);
+    else backward_dq<DP, EX, RBQ, WS, OWN, FORM>(p, a, id - key_groups, shared, tiles, slopes, slope_parts);
 }
 
 // The slopes' gradients: a workgroup adds a head's parts, a thread every 256th
@@ -1292,11 +1299,11 @@ bool own_delta(const attn_problem &p) {
     } while (0)
 
 // `a` has p, q, k, v, out and lse.
-template <bool SC, class Args>
+template <int FORM, class Args>
 int forward(const Args &a, const attn_scores &scores, void *stream) {
     const int64_t T = a.p.tokens, D = a.p.head_dim;
     int st = check_problem(a.p);
-    if (st == GEMM_OK && SC) st = check_scores(a.p, scores);
+    if (st == GEMM_OK && FORM) st = check_scores(a.p, scores);
     if (st != GEMM_OK) return st;
     if (T == 0) return GEMM_OK;
     const View q = {&a.q, a.p.q_heads, false}, k = {&a.k, a.p.kv_heads, false}, v = {&a.v, a.p.kv_heads, false},
@@ -1323,7 +1330,7 @@ int forward(const Args &a, const attn_scores &scores, void *stream) {
     return in_slices(grid, 256, [&](int64_t first, unsigned count) {
         p.first = (int)first;
 #define FWD_AS(DP, EX, RB, WS) \
-    hipLaunchKernelGGL((attention_fwd<DP, EX, RB, WS, SC>), dim3(count), dim3(256), 0, hs, p, sq, sk, sv, so, a.lse, \
+    hipLaunchKernelGGL((attention_fwd<DP, EX, RB, WS, FORM>), dim3(count), dim3(256), 0, hs, p, sq, sk, sv, so, a.lse, \
                        scores.slopes)
 #define FWD(DP, EX)                           \
     do {                                      \
@@ -1341,11 +1348,10 @@ int forward(const Args &a, const attn_scores &scores, void *stream) {
 struct Scratch {
     int64_t delta_bytes, parts, bytes;  // parts: doubles of one head
 };
-template <bool SC>
 Scratch scratch_of(const attn_problem &p, bool slopes) {
     Scratch s = {own_delta(p) ? 0 : p.q_heads * p.tokens * 4, 0, 0};
     s.bytes = s.delta_bytes;
-    if (SC && slopes) {
+    if (slopes) {
         const Plan rows = own_delta(p) ? Plan{1, 4} : plan_rows(p);
         s.parts = tiles_of(p, rows.rows()) * 4;
         s.delta_bytes = (s.delta_bytes + 7) / 8 * 8;
@@ -1355,17 +1361,17 @@ Scratch scratch_of(const attn_problem &p, bool slopes) {
 }
 
 // `a` has p, dout, q, k, v, out, lse, dq, dk, dv, workspace and workspace_bytes.
-template <bool SC, class Args>
+template <int FORM, class Args>
 int backward(const Args &a, const attn_scores &scores, float *dslopes, void *stream) {
     const int64_t T = a.p.tokens, D = a.p.head_dim, HQ = a.p.q_heads, HK = a.p.kv_heads;
     hipStream_t hs = static_cast<hipStream_t>(stream);
     int st = check_problem(a.p);
-    if (st == GEMM_OK && SC) st = check_scores(a.p, scores);
+    if (st == GEMM_OK && FORM) st = check_scores(a.p, scores);
     if (st != GEMM_OK) return st;
-    if (SC && dslopes && !scores.slopes) return GEMM_ERR_NULL;
+    if (dslopes && !scores.slopes) return GEMM_ERR_NULL;
     if (!aligned(dslopes, 4)) return GEMM_ERR_ALIGN;
     const Shared shared(a.p, scores);
-    if (SC && shared.meets({dslopes, HQ * 4})) return GEMM_ERR_ALIAS;
+    if (shared.meets({dslopes, HQ * 4})) return GEMM_ERR_ALIAS;
     if (T == 0) {
         if (!dslopes) return GEMM_OK;
         hipLaunchKernelGGL(attention_slopes, dim3((unsigned)HQ), dim3(256), 0, hs, nullptr, (int64_t)0, dslopes);
@@ -1381,7 +1387,7 @@ int backward(const Args &a, const attn_scores &scores, float *dslopes, void *str
     if (!aligned(a.lse, 4)) return GEMM_ERR_ALIGN;
     const int64_t row_bytes = HQ * T * 4;
     const bool own = own_delta(a.p);
-    const Scratch need = scratch_of<SC>(a.p, dslopes != nullptr);
+    const Scratch need = scratch_of(a.p, dslopes != nullptr);
     const Span scratch = {a.workspace, need.bytes}, rows_lse = {a.lse, row_bytes}, slopes = {dslopes, HQ * 4};
     if (need.bytes > 0) {
         if (a.workspace == nullptr || a.workspace_bytes < need.bytes) return GEMM_ERR_WORKSPACE;
@@ -1426,7 +1432,7 @@ int backward(const Args &a, const attn_scores &scores, float *dslopes, void *str
     st = in_slices(grid, 256, [&](int64_t first, unsigned count) {
         p.first = (int)first;
 #define BWD_AS(DP, EX, RBQ, RBK, WS, OWN) \
-    hipLaunchKernelGGL((attention_bwd<DP, EX, RBQ, RBK, WS, OWN, SC>), dim3(count), dim3(256), 0, hs, p, b, (int)nk, (int)tiles, \
+    hipLaunchKernelGGL((attention_bwd<DP, EX, RBQ, RBK, WS, OWN, FORM>), dim3(count), dim3(256), 0, hs, p, b, (int)nk, (int)tiles, \
                        scores.slopes, parts)
 #define BWD(DP, EX)                                              \
     do {                                                         \
