@@ -361,17 +361,19 @@ __device__ __forceinline__ float group_max(float v) {
     return across_groups(v, [](float x, float y) { return fmaxf(x, y); });
 }
 
-// Sum over the wave's lanes, the same in every lane: shifts within rows of 16
-// lanes, then broadcasts into the next rows.
-__device__ __forceinline__ int lanes_sum(int v) {
+// Sum over the wave's lanes up to each one, itself included: shifts within
+// rows of 16 lanes, then broadcasts into the next rows.
+__device__ __forceinline__ int lanes_scan(int v) {
     v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, true);   // row_shr:1
     v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, true);   // row_shr:2
     v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, true);   // row_shr:4
     v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, true);   // row_shr:8
     v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);  // row_bcast:15 into rows 1 and 3
     v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);  // row_bcast:31 into rows 2 and 3
-    return __builtin_amdgcn_readlane(v, 63);
+    return v;
 }
+// Sum over all of them, the same in every lane.
+__device__ __forceinline__ int lanes_sum(int v) { return __builtin_amdgcn_readlane(lanes_scan(v), 63); }
 
 // What a workgroup finds in cu_seqlens for its x-th tile of TILE rows, each
 // sequence being cut into tiles by itself: the sequence [s0, s1) and the
@@ -390,6 +392,14 @@ __device__ __forceinline__ int lanes_sum(int v) {
 // rows, 2 heads of 128, took 910 us in a launch of their own; without a causal
 // mask, six documents of 1 to 1531 rows took 686 us by level, 560 by length.)
 //
+// A prefix of G tiles (PREFIX) makes its tiles alike: G tiles of rows see at
+// least its keys and have level G - 1, or G tiles of keys are seen by all rows
+// and have level n - 1; the others keep theirs, and the tiles of one level are
+// found by a sum over the lanes.  (With the levels of a plain causal mask, the
+// last tiles to start were those of the longest prefixes: 7 documents of 1 to
+// 4096 tokens, a third of them prefixes, 16 heads on 4 of 128, forward, took
+// 1119 us, and take 1001.)
+//
 // That search looks at every sequence, 64 at a time, in every workgroup, which
 // with 2^24 sequences would take hours.  Past kScanned of them sequence b,
 // which starts at row c, has the numbers from c / TILE + b on, of which there
@@ -403,7 +413,7 @@ constexpr int kScanned = 512;
 struct Tile {
     int s0, s1, r0, first, last, seq;
 };
-template <int TILE>
+template <int TILE, bool PREFIX>
 __device__ __forceinline__ Tile find_tile(const Problem &p, int x, bool back) {
     Tile t = {0, p.tokens, -1, 0, p.tokens, 0};
     int n = 0, level = 0;
@@ -449,20 +459,36 @@ __device__ __forceinline__ Tile find_tile(const Problem &p, int x, bool back) {
                 x -= total;
                 continue;
             }
-            auto tiles_from = [&](int l) {  // S(l)
-                return lanes_sum(p.causal ? max(0, mine - l) : mine > l ? mine : 0);
+            int alike = 1;  // tiles of the prefix
+            if (PREFIX && p.prefix)
+                alike = max(1, (min(p.prefix[min(b + lane, p.nseq - 1)], hi - lo) + TILE - 1) / TILE);
+            auto own_from = [&](int l) {  // the lane's sequence's part of S(l)
+                if (!p.causal) return mine > l ? mine : 0;
+                if (PREFIX && l < (back ? alike : mine)) return back ? mine : max(mine - l, alike);
+                return max(0, mine - l);
             };
+            auto tiles_from = [&](int l) { return lanes_sum(own_from(l)); };  // S(l)
             for (int bit = 1 << (31 - __builtin_clz(total)); bit > 0; bit >>= 1) {
                 if (!__any(mine > level + bit)) continue;
                 if (tiles_from(level + bit) > x) level += bit;
             }
             x -= tiles_from(level + 1);
-            const int each = p.causal ? 1 : level + 1;  // tiles of a sequence in a row
-            const bool has = p.causal ? mine > level : mine == level + 1;
-            const uint64_t all = __ballot(has);
-            const int rank = __builtin_amdgcn_mbcnt_hi((unsigned)(all >> 32), __builtin_amdgcn_mbcnt_lo((unsigned)all, 0));
-            const int at = __builtin_ctzll(__ballot(has && rank == x / each));
-            if (!p.causal) level = x % each;
+            int at;
+            if (PREFIX && p.prefix) {
+                const int here = own_from(level) - own_from(level + 1), sum = lanes_scan(here);
+                at = __builtin_ctzll(__ballot(sum > x));
+                const int rank = x - __builtin_amdgcn_readlane(sum - here, at);
+                const int n_at = __builtin_amdgcn_readlane(mine, at);
+                if (level == (back ? __builtin_amdgcn_readlane(alike, at) : n_at) - 1) level = back ? rank : n_at - 1 - rank;
+            } else {
+                const int each = p.causal ? 1 : level + 1;  // tiles of a sequence in a row
+                const bool has = p.causal ? mine > level : mine == level + 1;
+                const uint64_t all = __ballot(has);
+                const int rank =
+                    __builtin_amdgcn_mbcnt_hi((unsigned)(all >> 32), __builtin_amdgcn_mbcnt_lo((unsigned)all, 0));
+                at = __builtin_ctzll(__ballot(has && rank == x / each));
+                if (!p.causal) level = x % each;
+            }
             t.seq = b + at;
             t.s0 = __builtin_amdgcn_readlane(lo, at);
             t.s1 = __builtin_amdgcn_readlane(hi, at);
@@ -568,7 +594,7 @@ __global__ __launch_bounds__(256, DP > 64 ? 2 : DP == 64 && RB == 2 && (FORM & k
     const int wave = uniform(threadIdx.x >> 6);
     int h, x;
     head_and_tile(p.first + (int)blockIdx.x, p.hq, p.group, h, x);
-    const Tile t = find_tile<TILE>(p, x, p.causal);
+    const Tile t = find_tile<TILE, FORM != 0>(p, x, p.causal);
     outside_rows<TILE>(p, t, x, [&](int r) {
         zero_row(o.p + r * o.st + h * o.sh, p.d);
         if (lane == 0) lse[(int64_t)h * p.tokens + r] = -INFINITY;
@@ -802,7 +828,7 @@ __device__ __forceinline__ void backward_dq(const Problem &p, const Backward &a,
     const int wave = uniform(threadIdx.x >> 6);
     int h, x;
     head_and_tile(id, p.hq, p.group, h, x);
-    const Tile t = find_tile<TILE>(p, x, p.causal);
+    const Tile t = find_tile<TILE, FORM != 0>(p, x, p.causal);
     outside_rows<TILE>(p, t, x, [&](int r) { zero_row(dq.p + r * dq.st + h * dq.sh, p.d); });
     double *slope_part = (FORM & kBias) && slope_parts ? slope_parts + ((int64_t)h * tiles + x) * 4 + wave : nullptr;
     if ((FORM & kBias) && slope_part && lane == 0) *slope_part = 0.0;
@@ -925,7 +951,7 @@ __device__ __forceinline__ void backward_dkv(const Problem &p, const Backward &a
     const int wave = uniform(threadIdx.x >> 6);
     int h, x;
     head_and_tile(id, p.hq / p.group, 1, h, x);
-    const Tile t = find_tile<TILE>(p, x, false);
+    const Tile t = find_tile<TILE, FORM != 0>(p, x, false);
     outside_rows<TILE>(p, t, x, [&](int r) {
         zero_row(dk.p + r * dk.st + h * dk.sh, p.d);
         zero_row(dv.p + r * dv.st + h * dv.sh, p.d);
