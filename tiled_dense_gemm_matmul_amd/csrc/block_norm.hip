@@ -3,11 +3,15 @@
 //
 // The work is bound by memory: every value is read and written once (forward:
 // x and y in, x_out and h out; backward: dx_out, dh, x_out and y in, dx and dy
-// out), and a row stays in registers between its sums.  LANES lanes own a row,
+// out), and a row stays in registers between its sums.  7992 rows of 4096
+// forward run at 5.3 TB/s, where a large copy on this card reaches 5.1; 8192
+// rows of 768 backward take 30 us, 5.0 TB/s with the kernel behind it.  LANES lanes own a row,
 // each NV groups of 4 consecutive values: a wave rows of up to 1024 values,
 // four rows a workgroup, and a workgroup of 256 or 512 threads wider ones.
 //  * Accesses are 16 bytes wide at any 4-byte alignment; where the width is no
-//    multiple of 4, one lane takes a row's last values one by one (EX false).
+//    multiple of 4, one lane takes a row's last values one by one (EX false),
+//    behind the loads of all others (8192 rows of 1150 backward 49 us; 69 with
+//    the choice inside every load).
 //  * The backward pass sums over rows for the weights and the gate.  A
 //    workgroup owns a run of rows and keeps its sums in registers (fp32, 64
 //    rows a lane at most), the gate's until the sequence ends; it writes them
@@ -101,32 +105,30 @@ struct Row {
 #pragma unroll
         for (int i = 0; i < NV; ++i) x[i] = f32x4{v, v, v, v};
     }
-    // zeros past the row's end
+    // zeros past the row's end; a last group of 1 to 3 values (not EX) is
+    // always one of the lanes' last groups, and is taken behind all others
     __device__ __forceinline__ void load(const float *row, int width) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = at(i);
             x[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-            if (c + 4 <= width) {
-                x[i] = *(const f32x4u *)(row + c);
-            } else if (!EX && c < width) {
-                x[i][0] = row[c];
-                if (c + 1 < width) x[i][1] = row[c + 1];
-                if (c + 2 < width) x[i][2] = row[c + 2];
-            }
+            if (at(i) + 4 <= width) x[i] = *(const f32x4u *)(row + at(i));
+        }
+        const int c = at(NV - 1);
+        if (!EX && c < width && c + 4 > width) {
+            x[NV - 1][0] = row[c];
+            if (c + 1 < width) x[NV - 1][1] = row[c + 1];
+            if (c + 2 < width) x[NV - 1][2] = row[c + 2];
         }
     }
     __device__ __forceinline__ void store(float *row, int width) const {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = at(i);
-            if (c + 4 <= width) {
-                *(f32x4u *)(row + c) = x[i];
-            } else if (!EX && c < width) {
-                row[c] = x[i][0];
-                if (c + 1 < width) row[c + 1] = x[i][1];
-                if (c + 2 < width) row[c + 2] = x[i][2];
-            }
+        for (int i = 0; i < NV; ++i)
+            if (at(i) + 4 <= width) *(f32x4u *)(row + at(i)) = x[i];
+        const int c = at(NV - 1);
+        if (!EX && c < width && c + 4 > width) {
+            row[c] = x[NV - 1][0];
+            if (c + 1 < width) row[c + 1] = x[NV - 1][1];
+            if (c + 2 < width) row[c + 2] = x[NV - 1][2];
         }
     }
 };
@@ -154,6 +156,31 @@ __device__ __forceinline__ int sequence_of(const Problem &p, int t) {
     } while (step > 1);
     return uniform(lo);
 }
+
+// The sequences that a run of rows meets, one after the other: the wave holds
+// the next 64 bounds, so that only every 64th sequence is searched for.
+struct Sequences {
+    int first = 0, bounds = 0x7fffffff;  // of sequence first + lane; none is known yet
+
+    __device__ __forceinline__ void look(const Problem &p, int t) {
+        first = sequence_of(p, t);
+        bounds = bound(p, min(first + (int)(threadIdx.x & 63), p.nseq));
+    }
+    // The sequence of row t, which is no less than the last one's, and the row
+    // behind it.
+    __device__ __forceinline__ void find(const Problem &p, int t, int &seq, int &end) {
+        auto below = [&]() {
+            return __popcll(__ballot(first + (int)(threadIdx.x & 63) < p.nseq && bounds <= t));
+        };
+        int n = below();
+        if (n == 0 || n == 64) {
+            look(p, t);
+            n = below();
+        }
+        seq = first + max(n - 1, 0);
+        end = n < 64 ? __builtin_amdgcn_readlane(bounds, n) : uniform(bound(p, seq + 1));
+    }
+};
 
 // The rows that belong to sequences.
 struct Used {
@@ -273,6 +300,7 @@ __global__ __launch_bounds__(LANES < 256 ? 256 : LANES, 2) void block_norm_bwd(P
     if (p.pre) pre.load(p.pre, p.width);
     if (p.post) post.load(p.post, p.width);
     if (p.gate && !by_seq) gate.load(p.gate, p.width);
+    Sequences sequences;
     for (int row = t0; row < t1;) {
         int end = t1, seq = 0;
         const bool in = row >= used.first && row < used.last;
@@ -281,8 +309,9 @@ __global__ __launch_bounds__(LANES < 256 ? 256 : LANES, 2) void block_norm_bwd(P
         } else {
             end = min(t1, used.last);
             if (by_seq) {
-                seq = sequence_of(p, row);
-                end = min(end, max(row + 1, uniform(bound(p, seq + 1))));
+                int behind;
+                sequences.find(p, row, seq, behind);
+                end = min(end, max(row + 1, behind));
                 gate.load(p.gate + (int64_t)seq * p.width, p.width);
             }
         }
@@ -362,14 +391,15 @@ __global__ __launch_bounds__(LANES < 256 ? 256 : LANES, 2) void block_norm_bwd(P
 }
 
 // The parts' sums: a workgroup takes 64 columns of one result, a thread 4 of
-// them over every 16th part, joined in order.  Results are numbered dpre_weight,
+// them over every EACH-th part, joined in order.  Results are numbered dpre_weight,
 // dpost_weight, then the gate's rows, those that the call has.
 struct Sums {
     const float *pre_parts, *post_parts, *gate_parts;
     float *dpre, *dpost, *dgate;
     int pitch, groups, chunk;
 };
-__global__ __launch_bounds__(256) void block_norm_sums(Problem p, Sums a, int tiles, int64_t first) {
+template <int EACH>
+__global__ __launch_bounds__(16 * EACH) void block_norm_sums(Problem p, Sums a, int tiles, int64_t first) {
     const int64_t id = first + blockIdx.x;
     int64_t job = id / tiles;
     const int c = (int)(id % tiles) * 64 + 4 * (threadIdx.x & 15), part = threadIdx.x >> 4;
@@ -393,14 +423,14 @@ __global__ __launch_bounds__(256) void block_norm_sums(Problem p, Sums a, int ti
     }
     double s[4] = {0.0, 0.0, 0.0, 0.0};
     if (c < p.width) {
-#pragma unroll 4
-        for (int64_t i = lo + part; i < hi; i += 16) {
+#pragma unroll EACH == 64 ? 8 : 4
+        for (int64_t i = lo + part; i < hi; i += EACH) {
             const f32x4 v = *(const f32x4 *)(parts + i * a.pitch + c);
 #pragma unroll
             for (int e = 0; e < 4; ++e) s[e] += (double)v[e];
         }
     }
-    __shared__ double meet[16][64];
+    __shared__ double meet[EACH][64];
 #pragma unroll
     for (int e = 0; e < 4; ++e) meet[part][4 * (threadIdx.x & 15) + e] = s[e];
     __syncthreads();
@@ -408,7 +438,7 @@ __global__ __launch_bounds__(256) void block_norm_sums(Problem p, Sums a, int ti
     if (mine < 64 && col < p.width) {
         double v = meet[0][mine];
 #pragma unroll
-        for (int w = 1; w < 16; ++w) v += meet[w][mine];
+        for (int w = 1; w < EACH; ++w) v += meet[w][mine];
         to[col] = (float)v;
     }
 }
@@ -484,15 +514,23 @@ Problem device_problem(const block_norm_problem &a) {
     return p;
 }
 
-// Lanes of a row: as few as hold it, 16 values each.
+// Lanes of a row: as few as hold it, 16 values each.  More values a lane were
+// a little faster over many rows and slower over few (a wave of 5 or 6 groups
+// a lane against 256 lanes of 2, us: 8192 rows of 1152 forward 23.3 and 24.4,
+// backward 42.5 and 43.3; 1001 rows of 1150 forward 6.8 and 5.9; 2000 rows of
+// 1536 backward 29.4 and 21.4).
 int lanes_of(int64_t width) { return width <= 1024 ? 64 : width <= 4096 ? 256 : 512; }
 
 // Rows of a workgroup of the backward pass.  Enough workgroups to fill the
 // chip, but no more than that, as each writes parts that are read again; and
-// 64 rows a lane at most, which bounds the fp32 sums.
+// 64 rows a lane at most, which bounds the fp32 sums.  Narrow rows take more of
+// them, wide ones, of 512 threads, fewer: us with 256, 512 and 1024, 16384 rows
+// of 128: -, 18.5, 16.6 (2048: 20.0); 8192 rows of 768: -, 30.2, 32.8; 4096
+// rows of 8192: 172, 182, -.
 int64_t chunk_of(const block_norm_problem &p) {
     const int64_t rows = std::max<int64_t>(1, 256 / lanes_of(p.width));
-    const int64_t each = (p.tokens + 512 * rows - 1) / (512 * rows);
+    const int64_t most = p.width <= 256 ? 1024 : p.width <= 4096 ? 512 : 256;
+    const int64_t each = (p.tokens + most * rows - 1) / (most * rows);
     return rows * std::min<int64_t>(std::max<int64_t>(each, 1), 64);
 }
 
@@ -645,8 +683,15 @@ int block_norm_backward(const block_norm_backward_args *args, void *stream) {
     const Sums s = {b.pre_parts, b.post_parts, b.gate_parts, a.dpre_weight, a.dpost_weight, a.dgate,
                     (int)parts.pitch, (int)parts.groups, (int)parts.chunk};
     const int64_t jobs = (p.pre ? 1 : 0) + (p.post ? 1 : 0) + gates / (W * 4), tiles = (W + 63) / 64;
+    // Many parts of few results: four times the threads, each with its loads in
+    // flight at once (8192 rows of 768: 30.2 us for the whole pass and 31.3; 512
+    // rows, 128 parts: 9.0 and 8.5; gates of 2048 sequences: 132 and 56).
+    if (parts.groups >= 256 && jobs * tiles <= 512)
+        return in_slices(jobs * tiles, 1024, [&](int64_t first, unsigned count) {
+            hipLaunchKernelGGL(block_norm_sums<64>, dim3(count), dim3(1024), 0, hs, p, s, (int)tiles, first);
+        });
     return in_slices(jobs * tiles, 256, [&](int64_t first, unsigned count) {
-        hipLaunchKernelGGL(block_norm_sums, dim3(count), dim3(256), 0, hs, p, s, (int)tiles, first);
+        hipLaunchKernelGGL(block_norm_sums<16>, dim3(count), dim3(256), 0, hs, p, s, (int)tiles, first);
     });
 }
 
