@@ -560,7 +560,7 @@ def _call_packed(name, args, device):
     fn = getattr(load_library(), name)
     # the handle alone: a torch stream object around it costs 1.8 us a call
     stream = torch._C._cuda_getCurrentRawStream(device.index)
-    if device.index == torch.cuda.current_device():
+    if device.index == torch._C._cuda_getDevice():
         st = fn(args, stream)
     else:
         with torch.cuda.device(device):
@@ -713,6 +713,23 @@ def _heads(t, name, shape, device):
     return t.data_ptr(), st, sh
 
 
+def _out_heads(t, name, shape, like):
+    """A result and its fields as of _heads: t itself, checked, or where that
+    is None a new dense one on `like`'s device, which needs no check."""
+    if t is not None:
+        return t, _heads(t, name, shape, like.device)
+    t = like.new_empty(shape)
+    return t, (t.data_ptr(), shape[1] * shape[2], shape[2])
+
+
+def _out_vector(t, name, n, like):
+    """The same for a vector of n values and its pointer."""
+    if t is not None:
+        return t, _vector(t, name, like.device, n)
+    t = like.new_empty((n,))
+    return t, t.data_ptr()
+
+
 def _row_values(t, name, shape, device):
     """Pointer of a dense float32 [heads, tokens] tensor."""
     if not isinstance(t, torch.Tensor) or t.device != device or t.dtype != torch.float32 or t.shape != shape \
@@ -797,12 +814,12 @@ def attention(q, k, v, cu_seqlens=None, causal=True, window=0, scale=None, out=N
     tk = _heads(k, "k", shape_k, device)
     tv = _heads(v, "v", shape_k, device)
     tokens, hq, _ = shape_q
-    if out is None:
-        out = q.new_empty(shape_q)
-    to = _heads(out, "out", shape_q, device)
+    out, to = _out_heads(out, "out", shape_q, q)
     if lse is None:
         lse = q.new_empty((hq, tokens))
-    pl = _row_values(lse, "lse", (hq, tokens), device)
+        pl = lse.data_ptr()
+    else:
+        pl = _row_values(lse, "lse", (hq, tokens), device)
     scores = _attn_scores(problem, softcap, slopes, prefix_lens, device)
     if scores is None:
         _call_packed("attn_forward", _FORWARD_ARGS.pack(*problem, *tq, *tk, *tv, *to, pl), device)
@@ -827,15 +844,9 @@ def attention_backward(dout, q, k, v, out, lse, cu_seqlens=None, causal=True, wi
     tv = _heads(v, "v", shape_k, device)
     to = _heads(out, "out", shape_q, device)
     pl = _row_values(lse, "lse", (shape_q[1], shape_q[0]), device)
-    if dq is None:
-        dq = q.new_empty(shape_q)
-    if dk is None:
-        dk = q.new_empty(shape_k)
-    if dv is None:
-        dv = q.new_empty(shape_k)
-    tdq = _heads(dq, "dq", shape_q, device)
-    tdk = _heads(dk, "dk", shape_k, device)
-    tdv = _heads(dv, "dv", shape_k, device)
+    dq, tdq = _out_heads(dq, "dq", shape_q, q)
+    dk, tdk = _out_heads(dk, "dk", shape_k, q)
+    dv, tdv = _out_heads(dv, "dv", shape_k, q)
     scores = _attn_scores(problem, softcap, slopes, prefix_lens, device)
     if dslopes is not None and slopes is None:
         raise ValueError("dslopes needs slopes")
@@ -918,12 +929,8 @@ def qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, eps=1e-6, interl
     device = q.device
     tq = _heads(q, "q", shape_q, device)
     tk = _heads(k, "k", shape_k, device)
-    if q_out is None:
-        q_out = q.new_empty(shape_q)
-    if k_out is None:
-        k_out = q.new_empty(shape_k)
-    toq = _heads(q_out, "q_out", shape_q, device)
-    tok = _heads(k_out, "k_out", shape_k, device)
+    q_out, toq = _out_heads(q_out, "q_out", shape_q, q)
+    k_out, tok = _out_heads(k_out, "k_out", shape_k, q)
     if pair_axis is None:
         _call_packed("attn_qk_norm_rope", _NORM_ARGS.pack(*fields, *tq, *tk, *toq, *tok), device)
     else:
@@ -943,19 +950,11 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, positions, i
     tgk = _heads(dk_out, "dk_out", shape_k, device)
     tq = _heads(q, "q", shape_q, device)
     tk = _heads(k, "k", shape_k, device)
-    if dq is None:
-        dq = q.new_empty(shape_q)
-    if dk is None:
-        dk = q.new_empty(shape_k)
-    tdq = _heads(dq, "dq", shape_q, device)
-    tdk = _heads(dk, "dk", shape_k, device)
+    dq, tdq = _out_heads(dq, "dq", shape_q, q)
+    dk, tdk = _out_heads(dk, "dk", shape_k, q)
     tokens, _, dim = shape_q
-    if dq_weight is None:
-        dq_weight = q.new_empty((dim,))
-    if dk_weight is None:
-        dk_weight = q.new_empty((dim,))
-    pqw = _vector(dq_weight, "dq_weight", device, dim)
-    pkw = _vector(dk_weight, "dk_weight", device, dim)
+    dq_weight, pqw = _out_vector(dq_weight, "dq_weight", dim, q)
+    dk_weight, pkw = _out_vector(dk_weight, "dk_weight", dim, q)
     nbytes = load_library().attn_qk_norm_rope_workspace_bytes(tokens, dim)
     if nbytes < 0:
         raise GemmError(-2, "attn_qk_norm_rope_workspace_bytes")
@@ -991,6 +990,14 @@ def _rows(t, name, shape, device):
     if sd != 1 and shape[1] > 1:
         raise ValueError(f"{name}'s last dimension must be contiguous")
     return t.data_ptr(), st
+
+
+def _out_rows(t, name, shape, like):
+    """As _out_heads for [tokens, width]."""
+    if t is not None:
+        return t, _rows(t, name, shape, like.device)
+    t = like.new_empty(shape)
+    return t, (t.data_ptr(), shape[1])
 
 
 def _block_problem(rows, name, pre_weight, post_weight, gate, residual_scale, block_scale, cu_seqlens, eps):
@@ -1043,12 +1050,12 @@ def block_norm(x, y=None, pre_weight=None, post_weight=None, gate=None, residual
     if pre_weight is None and h_out is not None:
         raise ValueError("h_out needs pre_weight")
     tx, ty = _rows(x, "x", shape, device), _rows(y, "y", shape, device)
-    if y is not None and x_out is None:
-        x_out = x.new_empty(shape)
-    if pre_weight is not None and h_out is None:
-        h_out = x.new_empty(shape)
-    _call_packed("block_norm", _BLOCK_ARGS.pack(*fields, *tx, *ty, *_rows(x_out, "x_out", shape, device),
-                                                *_rows(h_out, "h_out", shape, device)), device)
+    txo = th = (0, 0)
+    if y is not None:
+        x_out, txo = _out_rows(x_out, "x_out", shape, x)
+    if pre_weight is not None:
+        h_out, th = _out_rows(h_out, "h_out", shape, x)
+    _call_packed("block_norm", _BLOCK_ARGS.pack(*fields, *tx, *ty, *txo, *th), device)
     return x if y is None else x_out, h_out
 
 
@@ -1076,30 +1083,27 @@ def block_norm_backward(dx_out, dh, x_out, y=None, pre_weight=None, post_weight=
         raise ValueError("dpre_weight, dpost_weight and dgate need pre_weight, post_weight and gate")
     inputs = (*_rows(dx_out, "dx_out", shape, device), *_rows(dh, "dh", shape, device),
               *_rows(x_out, "x_out", shape, device), *_rows(y, "y", shape, device))
-    new = x_out.new_empty
-    if dx is None:
-        dx = new(shape)
-    if dy is None and y is not None:
-        dy = new(shape)
+    tdy, ppre, ppost, pgate = (0, 0), 0, 0, 0
+    dx, tdx = _out_rows(dx, "dx", shape, x_out)
+    if y is not None:
+        dy, tdy = _out_rows(dy, "dy", shape, x_out)
     width = shape[1]
-    if pre_weight is not None and dpre_weight is None:
-        dpre_weight = new((width,))
-    if post_weight is not None and dpost_weight is None:
-        dpost_weight = new((width,))
+    if pre_weight is not None:
+        dpre_weight, ppre = _out_vector(dpre_weight, "dpre_weight", width, x_out)
+    if post_weight is not None:
+        dpost_weight, ppost = _out_vector(dpost_weight, "dpost_weight", width, x_out)
     if gate is not None:
-        dgate = new(shape_gate) if dgate is None else dgate
-        if not isinstance(dgate, torch.Tensor) or dgate.shape != shape_gate or dgate.device != device \
+        if dgate is None:
+            dgate = x_out.new_empty(shape_gate)
+        elif not isinstance(dgate, torch.Tensor) or dgate.shape != shape_gate or dgate.device != device \
                 or dgate.dtype != torch.float32 or not dgate.is_contiguous():
             raise ValueError(f"dgate must be a contiguous float32 tensor of shape {tuple(shape_gate)} on {device}")
-    outputs = (*_rows(dx, "dx", shape, device), *_rows(dy, "dy", shape, device),
-               0 if pre_weight is None else _vector(dpre_weight, "dpre_weight", device, width),
-               0 if post_weight is None else _vector(dpost_weight, "dpost_weight", device, width),
-               0 if gate is None else dgate.data_ptr())
+        pgate = dgate.data_ptr()
     nbytes = load_library().block_norm_backward_workspace_bytes(_BLOCK_PROBLEM.pack(*fields))
     # scratch of this call's own: two captured graphs share nothing (none for
     # a problem that the call below refuses, with the reason)
-    scratch = new((nbytes // 4,)) if nbytes > 0 else None
+    scratch = x_out.new_empty((nbytes // 4,)) if nbytes > 0 else None
     _call_packed("block_norm_backward",
-                 _BLOCK_BACKWARD_ARGS.pack(*fields, *inputs, *outputs, scratch.data_ptr() if nbytes > 0 else 0,
-                                           max(0, nbytes)), device)
+                 _BLOCK_BACKWARD_ARGS.pack(*fields, *inputs, *tdx, *tdy, ppre, ppost, pgate,
+                                           scratch.data_ptr() if nbytes > 0 else 0, max(0, nbytes)), device)
     return dx, dy, dpre_weight, dpost_weight, dgate
