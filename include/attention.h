@@ -155,19 +155,17 @@ int attn_backward(const attn_backward_args *args, void *stream);
  *   dslopes[h] = - sum_{i,j} ds_ij |i - j|,
  *
  * with ds_ij (1 - tanh^2) in the place of ds_ij in dq and dk.  Distances are
- * fp32 and slopes are taken in units of softcap, or of scale without one, so
- * a bias is off by up to 2^-22 of itself; slopes are finite (others spread NaN
- * over their head).
+ * fp32, slopes finite (others spread NaN over their head).
  */
 typedef struct attn_scores {
     double softcap;             /* 0: none; 1e-6 to 1e6, with scale / softcap normal in fp32 */
-    const float *slopes;        /* [q_heads], or NULL; without softcap only with a scale of 1e-20 or more */
+    const float *slopes;        /* [q_heads], or NULL */
     const int32_t *prefix_lens; /* [num_seqs] ([1] without cu_seqlens) device array, or NULL; only with causal */
 } attn_scores;
 
 /* As attn_forward; out and lse overlap neither slopes nor prefix_lens.
- * GEMM_ERR_DTYPE also for a softcap or scale outside the above or prefix_lens
- * without causal. */
+ * GEMM_ERR_DTYPE also for a softcap outside the above or prefix_lens without
+ * causal. */
 typedef struct attn_scored_forward_args {
     attn_problem p;
     attn_scores s;

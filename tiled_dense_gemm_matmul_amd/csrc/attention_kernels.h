@@ -87,10 +87,9 @@ struct Problem {
     int first;       // workgroups in front of this launch's
     float scale, c;  // c = scale log2(e): scores go through exp2
     float factor;    // of dq and dk: the call's scale
-    // kCap: the raw scores are tanh(bend q.k) and scale is the cap
     const int *prefix;  // [nseq], or NULL
-    float bend;         // the call's scale over its cap
-    float per_scale;    // 1 / scale: slopes in units of the raw scores
+    float bend;         // kCap: the raw scores are tanh(bend q.k), and scale is the cap
+    float times;        // kBias: of the raw scores, before the bias; scale is 1
 };
 
 // A row's lse from the sum of exp2(s c - top) over its raw scores s and the
@@ -110,9 +109,10 @@ __device__ __forceinline__ float lse_of(const Problem &p, float sum, float top, 
 // The probability of a raw score in the backward pass.  The score is rounded
 // as in lse_of before lse is taken from it: two instructions a score more than
 // one multiply-add with scale log2(e).
+template <int FORM>
 __device__ __forceinline__ float probability(const Problem &p, float s, float lse) {
 #pragma clang fp contract(off)
-    const float score = s * p.scale;
+    const float score = FORM & kBias ? s : s * p.scale;
     return __builtin_amdgcn_exp2f((score - lse) * kLog2e);
 }
 
@@ -134,14 +134,16 @@ __device__ __forceinline__ float choose(int mask, float a, float b) {
     return __builtin_bit_cast(float, (__builtin_bit_cast(int, a) & mask) | (__builtin_bit_cast(int, b) & ~mask));
 }
 
-// Bends the 16 x 16 blocks s of q.k by the cap and takes the bias from them,
-// all in units of scale, so that what follows is the same for every form: a
-// score costs 7 instructions with a cap and 2 with a bias.  A lane holds keys
-// (or rows) at the distances |away[b] - i| from its row (or key); `slope` is
-// in units of scale too, and `steep` gets the derivative 1 - tanh^2.  Both
-// passes take the same steps, so their scores agree to the bit.
+// Bends the 16 x 16 blocks s of q.k by the cap, 7 instructions a score, and
+// takes the bias from them, 3 (without a bias the cap stays a factor for the
+// exponent to take in).  A lane holds keys (or rows) at the distances |away[b]
+// - i| from its row (or key); `steep` gets the derivative 1 - tanh^2.  Both
+// passes take the same steps, so their scores agree to the bit.  (A bias in
+// units of the raw scores took one instruction less, but rounded the slopes:
+// that moves all of a head's scores one way, and the slopes' gradient, which
+// sums over them, came out up to twice as far off.)
 template <int FORM, int RB, bool GRAD>
-__device__ __forceinline__ void bend_scores(float bend, float slope, const float (&away)[RB], f32x4 (&s)[RB],
+__device__ __forceinline__ void bend_scores(float bend, float times, float slope, const float (&away)[RB], f32x4 (&s)[RB],
                                             f32x4 (&steep)[RB]) {
 #pragma clang fp contract(off)
     if constexpr (FORM & kCap) {
@@ -185,15 +187,13 @@ __device__ __forceinline__ void bend_scores(float bend, float slope, const float
 #pragma unroll
         for (int b = 0; b < RB; ++b)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) s[b][i] = fmaf(-slope, fabsf(away[b] - (float)i), s[b][i]);
+            for (int i = 0; i < 4; ++i) s[b][i] = fmaf(-slope, fabsf(away[b] - (float)i), s[b][i] * times);
     }
 }
 // What no kernel of a call writes, for scalar loads at uniform places.
 template <class T>
 using Constant = const __attribute__((address_space(4))) T *;
-__device__ __forceinline__ float slope_of(const float *slopes, float per_scale, int h) {
-    return ((Constant<float>)slopes)[h] * per_scale;
-}
+__device__ __forceinline__ float slope_of(const float *slopes, int h) { return ((Constant<float>)slopes)[h]; }
 
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
@@ -339,6 +339,30 @@ __device__ __forceinline__ f32x4 dots(const Rows<DP> &a, const Rows<DP> &b) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) s = mfma(a.x[j][e], b.x[j][e], s);
     return s;
+}
+
+// The same products as four sums of DP / 4, added in pairs: a partial sum
+// that is rounded at every step is half as large, over a quarter of the steps.
+// For scores with a bias (3 instructions a score): the slopes' gradient sums
+// ds_ij |i - j| over a head, terms of both signs that all but cancel, and is
+// off by the scores' roundings more than by all others together.  Over 40
+// drawn problems it was as far off as an elementary torch implementation with
+// single sums, a third of that with four.
+template <int DP>
+__device__ __forceinline__ f32x4 split_dots(const Rows<DP> &a, const Rows<DP> &b) {
+    f32x4 s[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        s[c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int i = c * DP / 16; i < (c + 1) * DP / 16; ++i) s[c] = mfma(a.x[i / 4][i % 4], b.x[i / 4][i % 4], s[c]);
+    }
+    return (s[0] + s[1]) + (s[2] + s[3]);
+}
+template <int DP, int FORM>
+__device__ __forceinline__ f32x4 scores(const Rows<DP> &a, const Rows<DP> &b) {
+    if constexpr (FORM & kBias) return split_dots<DP>(a, b);
+    else return dots<DP>(a, b);
 }
 
 // A value of the four lane groups (lanes of one m) combined in all of them.
@@ -581,13 +605,13 @@ __device__ __forceinline__ bool all_see(const Problem &p, int s1, int pe, int r,
 // the rescaling.
 //
 // Four waves a SIMD leave each 128 registers, which two blocks of rows of
-// heads of 64 fill; the cap's steps spill some of the loads' offsets then, and
-// loading these again waits for the keys in flight.  With a cap those kernels
-// run three waves (cap 50, 12 heads of 64, us with three and with four: 16 x 512
-// tokens 79.6 and 85.5, 64 x 128 tokens 28.3 and 35.2; with a bias too 87.2
-// and 98.3).
+// heads of 64 fill; the cap's and the bias's steps spill some of the loads'
+// offsets then, and loading these again waits for the keys in flight.  Those
+// kernels run three waves (12 heads of 64, us with three and with four: cap 50,
+// 16 x 512 tokens 79.6 and 85.5, 64 x 128 tokens 28.3 and 35.2; biases 81.3 and
+// 118, 28.6 and 46.1).
 template <int DP, bool EX, int RB, int WS, int FORM>
-__global__ __launch_bounds__(256, DP > 64 ? 2 : DP == 64 && RB == 2 && (FORM & kCap) ? 3 : 4) void attention_fwd(Problem p, Strided q, Strided k, Strided v, Strided o,
+__global__ __launch_bounds__(256, DP > 64 ? 2 : DP == 64 && RB == 2 && FORM > kPrefix ? 3 : 4) void attention_fwd(Problem p, Strided q, Strided k, Strided v, Strided o,
                                                         float *lse, const float *slopes) {
     constexpr int WROWS = 16 * RB, WR = 4 / WS, TILE = WR * WROWS;
     const int lane = threadIdx.x & 63, g = lane >> 4, m = lane & 15;
@@ -619,7 +643,7 @@ __global__ __launch_bounds__(256, DP > 64 ? 2 : DP == 64 && RB == 2 && (FORM & k
     const Range kr = keys_of<FORM != 0>(p, s0, s1, pe, r0, WROWS);
     const int step = 16 * WS;
     int kb = kr.lo + 16 * part_of;
-    const float slope = FORM & kBias ? slope_of(slopes, p.per_scale, h) : 0.0f;
+    const float slope = FORM & kBias ? slope_of(slopes, h) : 0.0f;
     // The values of a block are asked for when its scores begin, the keys of
     // the next one when they are done, so each load has a product to arrive under.
     Rows<DP> K;
@@ -630,7 +654,7 @@ __global__ __launch_bounds__(256, DP > 64 ? 2 : DP == 64 && RB == 2 && (FORM & k
         V.template load<EX>(rows_rsrc(vp, v.st, kb, s1, p.d), v.st, p.d);
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int b = 0; b < RB; ++b) s[b] = dots<DP>(K, Q[b]);
+        for (int b = 0; b < RB; ++b) s[b] = scores<DP, FORM>(K, Q[b]);
         __builtin_amdgcn_sched_barrier(0);
         K.template load<EX>(rows_rsrc(kp, k.st, kb + step, s1, p.d), k.st, p.d);
         __builtin_amdgcn_sched_barrier(0);
@@ -639,7 +663,7 @@ __global__ __launch_bounds__(256, DP > 64 ? 2 : DP == 64 && RB == 2 && (FORM & k
             f32x4 steep[RB];
 #pragma unroll
             for (int b = 0; b < RB; ++b) away[b] = (float)(r0 + 16 * b + m - kb - 4 * g);
-            bend_scores<FORM, RB, false>(p.bend, slope, away, s, steep);
+            bend_scores<FORM, RB, false>(p.bend, p.times, slope, away, s, steep);
         }
         if (!all_see<FORM != 0>(p, s1, pe, r0, WROWS, kb, 16)) {
 #pragma unroll
@@ -836,7 +860,7 @@ __device__ __forceinline__ void backward_dq(const Problem &p, const Backward &a,
     const int s0 = t.s0, s1 = t.s1, t0 = t.r0, pe = prefix_end<FORM != 0>(p, t);
     const int part_of = wave / WR, r0 = t0 + wave % WR * WROWS;
     if (WS == 1 && r0 >= s1) return;
-    const float slope = FORM & kBias ? slope_of(slopes, p.per_scale, h) : 0.0f;
+    const float slope = FORM & kBias ? slope_of(slopes, h) : 0.0f;
     double slope_sum = 0.0;
     const float *kp = k.p + (h / p.group) * k.sh, *vp = v.p + (h / p.group) * v.sh;
 
@@ -873,7 +897,7 @@ __device__ __forceinline__ void backward_dq(const Problem &p, const Backward &a,
         f32x4 s[RB], dp[RB];
         if (STAGED) K.stage(staged);
 #pragma unroll
-        for (int b = 0; b < RB; ++b) s[b] = dots<DP>(K, Q[b]);
+        for (int b = 0; b < RB; ++b) s[b] = scores<DP, FORM>(K, Q[b]);
         K.template load<EX>(rows_rsrc(kp, k.st, kb + step, s1, p.d), k.st, p.d);
         if (STAGED && EARLY) T.take(staged);
         __builtin_amdgcn_sched_barrier(0);
@@ -888,13 +912,13 @@ __device__ __forceinline__ void backward_dq(const Problem &p, const Backward &a,
         if constexpr (FORM & (kBias | kCap)) {
 #pragma unroll
             for (int b = 0; b < RB; ++b) away[b] = (float)(r0 + 16 * b + m - kb - 4 * g);
-            bend_scores<FORM, RB, true>(p.bend, slope, away, s, steep);
+            bend_scores<FORM, RB, true>(p.bend, p.times, slope, away, s, steep);
         }
 #pragma unroll
         for (int b = 0; b < RB; ++b) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                s[b][i] = probability(p, s[b][i], l[b]) * (dp[b][i] - del[b]);
+                s[b][i] = probability<FORM>(p, s[b][i], l[b]) * (dp[b][i] - del[b]);
             const f32x4 ds = s[b];  // of the final scores
             if (FORM & kCap) s[b] *= steep[b];
             if (!whole) {
@@ -1011,7 +1035,7 @@ __device__ __forceinline__ void backward_dkv(const Problem &p, const Backward &a
     while (n < total) {
         const int row = r;
         const float *qc = qp, *gc = gp;
-        const float slope = FORM & kBias ? slope_of(slopes, p.per_scale, h * p.group + uniform(qh)) : 0.0f;
+        const float slope = FORM & kBias ? slope_of(slopes, h * p.group + uniform(qh)) : 0.0f;
         if (STAGED) {
             Q.stage(staged);
             G.stage(staged_g);
@@ -1025,7 +1049,7 @@ __device__ __forceinline__ void backward_dkv(const Problem &p, const Backward &a
         at();
         f32x4 s[RB], dp[RB];
 #pragma unroll
-        for (int b = 0; b < RB; ++b) s[b] = dots<DP>(Q, K[b]);
+        for (int b = 0; b < RB; ++b) s[b] = scores<DP, FORM>(Q, K[b]);
         if (OWN) {
             const float del = row_dots<DP>(G, out);
 #pragma unroll
@@ -1054,13 +1078,13 @@ __device__ __forceinline__ void backward_dkv(const Problem &p, const Backward &a
             float away[RB];
 #pragma unroll
             for (int b = 0; b < RB; ++b) away[b] = (float)(k0 + 16 * b + m - row - 4 * g);
-            bend_scores<FORM, RB, true>(p.bend, slope, away, s, steep);
+            bend_scores<FORM, RB, true>(p.bend, p.times, slope, away, s, steep);
         }
 #pragma unroll
         for (int b = 0; b < RB; ++b) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                s[b][i] = probability(p, s[b][i], l4[i]);
+                s[b][i] = probability<FORM>(p, s[b][i], l4[i]);
                 dp[b][i] = s[b][i] * (dp[b][i] - d4[i]);
             }
             if (FORM & kCap) dp[b] *= steep[b];
@@ -1188,8 +1212,6 @@ int check_scores(const attn_problem &p, const attn_scores &s) {
         const float bend = (float)(p.scale / s.softcap);
         if (!(bend >= 0x1p-126f) || !std::isfinite(bend)) return GEMM_ERR_DTYPE;
     }
-    // a bias is taken in units of scale: one of up to 2^30 stays finite
-    if (s.softcap == 0.0 && s.slopes && !(p.scale >= 1e-20)) return GEMM_ERR_DTYPE;
     if (s.prefix_lens && !p.causal) return GEMM_ERR_DTYPE;
     return aligned(s.slopes, 4) && aligned(s.prefix_lens, 4) ? GEMM_OK : GEMM_ERR_ALIGN;
 }
@@ -1225,12 +1247,12 @@ Problem device_problem(const attn_problem &a, const attn_scores &s) {
     p.window = a.window < a.tokens ? (int)a.window : 0;  // a wider window hides nothing
     p.first = 0;
     p.factor = (float)a.scale;
-    const double scale = s.softcap > 0.0 ? s.softcap : a.scale;
+    const double times = s.softcap > 0.0 ? s.softcap : a.scale, scale = s.slopes ? 1.0 : times;
     p.scale = (float)scale;
     p.c = folded(scale);
+    p.times = (float)times;
     p.prefix = s.prefix_lens;
     p.bend = s.softcap > 0.0 ? (float)(a.scale / s.softcap) : 0.0f;
-    p.per_scale = (float)(1.0 / scale);
     return p;
 }
 
