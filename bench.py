@@ -90,6 +90,10 @@ def parse():
     ap.add_argument("--attention", action="store_true",
                     help="instead of the step: time attention and the query/key norm with rotation, forward and "
                          "backward, on the seq-512 model's heads and on wider and longer ones")
+    ap.add_argument("--block", action="store_true",
+                    help="instead of the step: time the rest of a transformer block, attention with capped, biased and "
+                         "prefix-masked scores, the norm with a rotation by several axes and the norms around a "
+                         "block, forward and backward")
     ap.add_argument("--distill", action="store_true",
                     help="instead of the step: time distill_cross_entropy (64 teacher logits a row, gradient in a "
                          "buffer of its own) on the seq-512 logits and on 4096 rows of wider vocabularies")
@@ -426,6 +430,92 @@ def time_attention():
                "fwd_GBps": round(2e-3 * nbytes / fwd), "bwd_us": round(bwd, 1), "bwd_GBps": round(3e-3 * nbytes / bwd)}
         rows.append(row)
         print(f"| {label} | {row['heads']} | {fwd:.1f} | {row['fwd_GBps']} | {bwd:.1f} | {row['bwd_GBps']} |", flush=True)
+    return rows
+
+
+# label, sequence lengths, prefixes, query heads, key/value heads, head width
+SCORE_CASES = [("512", [512], [128], 12, 12, 64), ("16 x 512", [512] * 16, [128] * 16, 12, 12, 64),
+               ("6144", [6144], [1024], 12, 4, 64), ("4 x 2048", [2048] * 4, [512] * 4, 16, 4, 128)]
+AXES_CASES = [("23 x 22 patches", 506, 2, 12, 12, 64), ("8 x 34 x 30 patches", 8160, 3, 24, 8, 128),
+              ("16 x 512", 8192, 2, 12, 12, 64)]
+# label, sequences of how many rows, width
+BLOCK_CASES = [("512", 1, 512, 768), ("16 x 512", 16, 512, 768), ("16 x 512", 16, 512, 2048), ("8192", 1, 8192, 1150),
+               ("8 x 1024", 8, 1024, 4096)]
+
+
+def time_block():
+    """attention with each form of scores beside the plain one, qk_norm_rope by
+    several axes, and block_norm, each with its backward pass, through the
+    binding with preallocated results, as time_attention."""
+    import numpy as np
+    import torch
+    from tiled_dense_gemm_matmul_amd import binding
+    dev = torch.device("cuda:0")
+    g = torch.Generator(device="cuda").manual_seed(0)
+
+    def per_call(fn):
+        t0 = time.perf_counter()
+        while time.perf_counter() - t0 < 0.1:
+            fn()
+            torch.cuda.synchronize()
+        return float(np.median([batch_time(fn, 10) for _ in range(5)]))
+
+    rows = []
+    print("| sequences | heads (q/kv x width) | scores | forward us | backward us |\n|---|---|---|---|---|")
+    for label, lengths, prefix, hq, hk, d in SCORE_CASES:
+        T = sum(lengths)
+        qkv = torch.randn((T, (hq + 2 * hk) * d), device=dev, generator=g)
+        qkv[:, :hq * d] *= 4.0
+        q, k, v = (x.unflatten(1, (-1, d)) for x in qkv.split([hq * d, hk * d, hk * d], 1))
+        dq, dk, dv = (x.unflatten(1, (-1, d)) for x in torch.empty_like(qkv).split([hq * d, hk * d, hk * d], 1))
+        cu = torch.tensor([0, *np.cumsum(lengths)], dtype=torch.int32, device=dev)
+        slopes = torch.exp2(-8.0 * (1 + torch.arange(hq, device=dev)) / hq)
+        pre = torch.tensor(prefix, dtype=torch.int32, device=dev)
+        for name, form in (("plain", {}), ("cap 50", {"softcap": 50.0}), ("slopes", {"slopes": slopes}),
+                           ("prefix", {"prefix_lens": pre}),
+                           ("all", {"softcap": 50.0, "slopes": slopes, "prefix_lens": pre})):
+            kw = {"cu_seqlens": cu, **form}
+            out, lse = binding.attention(q, k, v, **kw)
+            dout = torch.randn(out.shape, device=dev, generator=g)
+            ds = {"dslopes": torch.empty_like(slopes)} if "slopes" in form else {}
+            fwd = per_call(lambda: binding.attention(q, k, v, out=out, lse=lse, **kw))
+            bwd = per_call(lambda: binding.attention_backward(dout, q, k, v, out, lse, dq=dq, dk=dk, dv=dv, **kw, **ds))
+            rows.append({"case": label, "heads": f"{hq}/{hk} x {d}", "scores": name, "fwd_us": round(fwd, 1),
+                         "bwd_us": round(bwd, 1)})
+            print(f"| {label} | {hq}/{hk} x {d} | {name} | {fwd:.1f} | {bwd:.1f} |", flush=True)
+    print("\n| tokens | axes | heads (q + k x width) | norm and rotation us | GB/s | backward us | GB/s |\n"
+          "|---|---|---|---|---|---|---|")
+    for label, T, axes, hq, hk, d in AXES_CASES:
+        q, k, gq, gk = (torch.randn((T, h, d), device=dev, generator=g) for h in (hq, hk, hq, hk))
+        w = torch.ones(d, device=dev)
+        common = (w, w, torch.randint(1000, (axes, T), dtype=torch.int32, device=dev, generator=g),
+                  10000.0 ** (-torch.arange(d // 2, device=dev) / (d // 2)))
+        axis = {"pair_axis": (torch.arange(d // 2, device=dev) % axes).int()}
+        a, b, dw = torch.empty_like(q), torch.empty_like(k), torch.empty((2, d), device=dev)
+        fwd = per_call(lambda: binding.qk_norm_rope(q, k, *common, q_out=a, k_out=b, **axis))
+        bwd = per_call(lambda: binding.qk_norm_rope_backward(gq, gk, q, k, *common, dq=a, dk=b, dq_weight=dw[0],
+                                                             dk_weight=dw[1], **axis))
+        nbytes = 4 * T * (hq + hk) * d
+        row = {"case": label, "heads": f"{hq} + {hk} x {d}", "axes": axes, "fwd_us": round(fwd, 1),
+               "fwd_GBps": round(2e-3 * nbytes / fwd), "bwd_us": round(bwd, 1), "bwd_GBps": round(3e-3 * nbytes / bwd)}
+        rows.append(row)
+        print(f"| {label} | {axes} | {row['heads']} | {fwd:.1f} | {row['fwd_GBps']} | {bwd:.1f} | {row['bwd_GBps']} |",
+              flush=True)
+    print("\n| rows | width | norms, gate and residual us | GB/s | backward us | GB/s |\n|---|---|---|---|---|---|")
+    for label, seqs, n, width in BLOCK_CASES:
+        T = seqs * n
+        x, y, dx, dh, a, b = (torch.randn((T, width), device=dev, generator=g) for _ in range(6))
+        w, gate, dgate = torch.ones(width, device=dev), *torch.ones((2, seqs, width), device=dev)
+        cu = (n * torch.arange(seqs + 1, device=dev)).int()
+        kw = {"pre_weight": w, "post_weight": w, "gate": gate, "cu_seqlens": cu}
+        dw = torch.empty((2, width), device=dev)
+        fwd = per_call(lambda: binding.block_norm(x, y, **kw, x_out=a, h_out=b))
+        bwd = per_call(lambda: binding.block_norm_backward(dx, dh, x, y, **kw, dx=a, dy=b, dpre_weight=dw[0],
+                                                           dpost_weight=dw[1], dgate=dgate))
+        row = {"case": label, "width": width, "fwd_us": round(fwd, 1), "fwd_GBps": round(16e-3 * T * width / fwd),
+               "bwd_us": round(bwd, 1), "bwd_GBps": round(24e-3 * T * width / bwd)}
+        rows.append(row)
+        print(f"| {label} | {width} | {fwd:.1f} | {row['fwd_GBps']} | {bwd:.1f} | {row['bwd_GBps']} |", flush=True)
     return rows
 
 
@@ -1269,6 +1359,9 @@ def main():
         return
     if args.attention:
         time_attention()
+        return
+    if args.block:
+        time_block()
         return
     if args.distill:
         time_distill()
