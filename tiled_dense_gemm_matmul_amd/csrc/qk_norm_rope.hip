@@ -134,6 +134,32 @@ __device__ __forceinline__ int64_t axis_row(const Norm &n, int p) {
     return (int64_t)min(max(n.axis[p], 0), n.axes - 1) * n.tokens;
 }
 
+// Cosines and sines of the W pairs from pair p on at a token.  With AXES the
+// 64 / G lanes that hold the same pairs (of other heads) form PER of them each
+// and take the rest from one another, so that a lane loads a position or two,
+// not four (8160 tokens of 32 heads of 128, inputs not in any cache: 58.9 us
+// against 63.1; with one position a token it changed nothing).
+template <int W, int G, bool AXES>
+struct Turns {
+    static constexpr int SLOTS = 64 / G, PER = !AXES ? W : W > SLOTS ? W / SLOTS : 1;
+
+    // The first pair that this lane forms, of the W.
+    static __device__ __forceinline__ int first() { return PER == W ? 0 : (threadIdx.x & 63) / G * PER % W; }
+    // pos(j): the position of pair p + first() + j
+    template <class F>
+    static __device__ __forceinline__ void form(const Norm &n, int p, F pos, float (&c)[W], float (&s)[W]) {
+        const int part = (threadIdx.x & 63) % G;
+        float mc[PER], ms[PER];
+#pragma unroll
+        for (int j = 0; j < PER; ++j) turn(n, pos(j), p + first() + j, mc[j], ms[j]);
+#pragma unroll
+        for (int e = 0; e < W; ++e) {
+            c[e] = PER == W ? mc[e % PER] : __shfl(mc[e % PER], e / PER * G + part, 64);
+            s[e] = PER == W ? ms[e % PER] : __shfl(ms[e % PER], e / PER * G + part, 64);
+        }
+    }
+};
+
 template <int G>
 __device__ __forceinline__ float lanes_sum(float v) {
 #pragma unroll
@@ -161,9 +187,9 @@ __global__ __launch_bounds__(256) void qk_norm_rope_fwd(Norm n, Strided q, Strid
         const int p = (i * G + part) * W;
         in[i] = p < n.d / 2;
         at[i] = place(n, p, W);
-#pragma unroll
-        for (int e = 0; e < W; ++e)
-            turn(n, AXES ? position(n, axis_row<AXES>(n, p + e) + t) : pos, p + e, c[i][e], s[i][e]);
+        Turns<W, G, AXES>::form(
+            n, p, [&](int j) { return AXES ? position(n, axis_row<AXES>(n, p + Turns<W, G, AXES>::first() + j) + t) : pos; },
+            c[i], s[i]);
     }
     const int heads = n.hq + n.hk;
     for (int h = chunk * HW + slot; h < heads; h += chunks * HW) {
@@ -214,14 +240,14 @@ __global__ __launch_bounds__(64 * kWaves) void qk_norm_rope_bwd(Norm n, Strided 
     Place at[NP];
     bool in[NP];
     double sums[2][NP][2 * W];
-    int64_t row[NP][W];  // of the pairs' positions
+    int64_t row[NP][Turns<W, G, AXES>::PER];  // of the positions that this lane turns by
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
         const int p = (i * G + part) * W;
         in[i] = p < n.d / 2;
         at[i] = place(n, p, W);
 #pragma unroll
-        for (int e = 0; e < W; ++e) row[i][e] = axis_row<AXES>(n, p + e);
+        for (int e = 0; e < Turns<W, G, AXES>::PER; ++e) row[i][e] = axis_row<AXES>(n, p + Turns<W, G, AXES>::first() + e);
 #pragma unroll
         for (int e = 0; e < 2 * W; ++e) sums[0][i][e] = sums[1][i][e] = 0.0;
     }
@@ -235,11 +261,10 @@ __global__ __launch_bounds__(64 * kWaves) void qk_norm_rope_bwd(Norm n, Strided 
         float dw[2][NP][2 * W];
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
+            Turns<W, G, AXES>::form(
+                n, (i * G + part) * W, [&](int j) { return AXES ? position(n, row[i][j] + t) : pos; }, c[i], s[i]);
 #pragma unroll
-            for (int e = 0; e < W; ++e) {
-                turn(n, AXES ? position(n, row[i][e] + t) : pos, (i * G + part) * W + e, c[i][e], s[i][e]);
-                dw[0][i][e] = dw[0][i][W + e] = dw[1][i][e] = dw[1][i][W + e] = 0.0f;
-            }
+            for (int e = 0; e < W; ++e) dw[0][i][e] = dw[0][i][W + e] = dw[1][i][e] = dw[1][i][W + e] = 0.0f;
         }
         for (int h = chunk * HW + slot; h < heads; h += chunks * HW) {
             const bool isq = h < n.hq;
