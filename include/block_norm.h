@@ -67,6 +67,7 @@ typedef struct block_norm_problem {
     const float *post_weight;  /* [width], or NULL: no norm behind the block */
     const float *gate;         /* [width] or [num_seqs, width], or NULL */
     int64_t gate_by_sequence;  /* 0 or 1; 1 needs cu_seqlens */
+    int64_t gate_stride;       /* elements from one sequence's gate to the next; ignored otherwise */
     const int32_t *cu_seqlens; /* [num_seqs + 1] device array, or NULL: all rows are one sequence */
     int64_t num_seqs;          /* ignored when cu_seqlens is NULL */
     int64_t tokens;
@@ -82,7 +83,8 @@ typedef struct block_norm_problem {
  *
  * GEMM_ERR_NULL for a missing array (or neither y nor pre_weight),
  * GEMM_ERR_SHAPE for sizes outside the above (tokens < 2^30, num_seqs < 2^24),
- * for strides that are negative or overlap an output's own rows, and for
+ * for strides that are negative, overlap an output's own rows or reach 2^56
+ * elements over all rows, and for
  * arrays that the call has no use for (x_out, post_weight or gate without y, h
  * without pre_weight), GEMM_ERR_ALIGN, GEMM_ERR_DTYPE for a scale, eps or flag
  * outside the above, GEMM_ERR_ALIAS, and GEMM_ERR_LAUNCH when the runtime
@@ -96,7 +98,9 @@ int block_norm(const block_norm_args *args, void *stream);
 
 /*
  * dx, dy (with y) and the gradients of the weights and the gate that the call
- * has, [width], [width] and the gate's shape, dense.  dx_out may be NULL only
+ * has, [width], [width] and the gate's shape, the latter's rows dgate_stride
+ * elements apart (at least width with a gate for each of several sequences).
+ * dx_out may be NULL only
  * with pre_weight.  dx and dy may each be the very same matrix as dx_out, dh,
  * x_out or y; they may not overlap one another or, otherwise, anything else.
  * The workspace holds at least block_norm_backward_workspace_bytes bytes (-1
@@ -108,6 +112,7 @@ typedef struct block_norm_backward_args {
     block_norm_problem p;
     block_rows dx_out, dh, x_out, y, dx, dy;
     float *dpre_weight, *dpost_weight, *dgate;
+    int64_t dgate_stride;
     void *workspace;
     int64_t workspace_bytes;
 } block_norm_backward_args;

@@ -40,7 +40,7 @@ def test_struct_sizes(binding, tmp_path):
     assert sizes == [binding._BLOCK_PROBLEM.size, binding._BLOCK_ARGS.size, binding._BLOCK_BACKWARD_ARGS.size]
 
 
-PROBLEM = {"pre": BASE, "post": BASE + 0x10000, "gate": BASE + 0x20000, "by_seq": 1, "cu": BASE + 0x30000, "nseq": 3,
+PROBLEM = {"pre": BASE, "post": BASE + 0x10000, "gate": BASE + 0x20000, "by_seq": 1, "gate_st": 64, "cu": BASE + 0x30000, "nseq": 3,
            "tokens": 50, "width": 64, "a": 1.0, "b": 1.0, "eps": 1e-6}
 
 
@@ -50,7 +50,7 @@ def _matrices(*names):
 
 FORWARD = {**PROBLEM, **_matrices("x", "y", "x_out", "h")}
 BACKWARD = {**PROBLEM, **_matrices("dx_out", "dh", "x_out", "y", "dx", "dy"), "dpre": BASE + 0x40000,
-            "dpost": BASE + 0x50000, "dgate": BASE + 0x60000, "ws": BASE + 9 * STEP, "wsb": 1 << 20}
+            "dpost": BASE + 0x50000, "dgate": BASE + 0x60000, "dgate_st": 64, "ws": BASE + 9 * STEP, "wsb": 1 << 20}
 
 
 def forward(binding, **kw):
@@ -72,7 +72,8 @@ def workspace(binding, **kw):
 BAD_PROBLEMS = [({"tokens": -1}, SHAPE), ({"tokens": 1 << 30}, SHAPE), ({"width": 0}, SHAPE), ({"width": 8193}, SHAPE),
                 ({"width": -4}, SHAPE), ({"nseq": -1}, SHAPE), ({"nseq": 1 << 24}, SHAPE), ({"by_seq": 2}, DTYPE),
                 ({"a": float("nan")}, DTYPE), ({"a": 1e300}, DTYPE), ({"b": float("inf")}, DTYPE), ({"eps": -1e-9}, DTYPE),
-                ({"eps": float("nan")}, DTYPE), ({"eps": 1e39}, DTYPE), ({"cu": 0}, NULL), ({"pre": BASE + 2}, ALIGN),
+                ({"eps": float("nan")}, DTYPE), ({"eps": 1e39}, DTYPE), ({"cu": 0}, NULL), ({"gate_st": -1}, SHAPE), ({"gate_st": 1 << 56}, SHAPE),
+                ({"pre": BASE + 2}, ALIGN),
                 ({"post": BASE + 0x10001}, ALIGN), ({"gate": BASE + 0x20002}, ALIGN), ({"cu": BASE + 0x30001}, ALIGN)]
 
 
@@ -105,7 +106,8 @@ def test_forward_refuses(binding, kw, status):
     ({"dpost": 0}, NULL), ({"dgate": 0}, NULL), ({"pre": 0, "dpre": 0, "dh": 0, "dx_out": 0}, NULL),
     ({"y": 0}, SHAPE), ({"pre": 0, "dpre": 0}, SHAPE), ({"pre": 0, "dh": 0}, SHAPE), ({"post": 0}, SHAPE),
     ({"gate": 0}, SHAPE), ({**NO_Y, "dpost": 0, "dgate": 0}, SHAPE),
-    ({**NO_Y, "dpost": 0, "dgate": 0, "dy": 0, "b": 2.0}, DTYPE), ({"dx_st": 10}, SHAPE), ({"dy_st": 0}, SHAPE),
+    ({**NO_Y, "dpost": 0, "dgate": 0, "dy": 0, "b": 2.0}, DTYPE), ({"dx_st": 10}, SHAPE), ({"dgate_st": 63}, SHAPE), ({"dgate_st": 1 << 55}, SHAPE),
+    ({"dgate_st": STEP // 4}, ALIAS), ({"dy_st": 0}, SHAPE),
     ({"dh_st": -1}, SHAPE), ({"dx": BASE + 5 * STEP + 2}, ALIGN), ({"dpre": BASE + 0x40001}, ALIGN),
     ({"dgate": BASE + 0x60002}, ALIGN), ({"ws": 0}, WORKSPACE), ({"wsb": 100}, WORKSPACE),
     ({"ws": BASE + 9 * STEP + 8}, ALIGN), ({"dy": BASE + 5 * STEP}, ALIAS), ({"dx": BASE + STEP + 256}, ALIAS),

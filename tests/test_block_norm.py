@@ -303,6 +303,79 @@ def test_offsets_past_32_bits():
     torch.cuda.empty_cache()
 
 
+def test_gates_as_columns_of_a_projection():
+    """Each sequence's gate and its gradient as columns of a wider buffer, and one gate seen by all sequences."""
+    import torch
+    c = Case(8, [30, 0, 41], 96, tail=3)
+    want = c.forward()
+    grads = c.backward(want[0])
+    wide = torch.full((3, 300), float("nan"), device=device())
+    wide[:, 101:197] = c.kw["gate"]
+    kept = torch.full((3, 300), SENTINEL, device=device())
+    c.kw["gate"] = wide[:, 101:197]
+    got = c.forward()
+    back = c.backward(got[0], dgate=kept[:, 7:103])
+    assert all(torch.equal(a, b) for a, b in zip((*want, *grads), (*got, *back)))
+    kept[:, 7:103] = SENTINEL
+    assert bool((kept == SENTINEL).all())
+    c.kw["gate"] = wide[:1, 101:197].expand(3, 96)
+    got = (*c.forward(), *c.backward(want[0]))
+    c.kw["gate"] = c.kw["gate"].contiguous()
+    assert all(torch.equal(a, b) for a, b in zip(got, (*c.forward(), *c.backward(want[0]))))
+
+
+def test_more_rows_than_one_launch_takes():
+    """40 million rows, a wave each forward: both ends against the same rows alone, and the sums in 64 bits."""
+    import torch
+    from tiled_dense_gemm_matmul_amd import binding
+    T, W = 40000003, 4
+    g = torch.Generator(device=device())
+    g.manual_seed(4)
+    x, y, gx, gh = (torch.randn((T, W), generator=g, device=device()) for _ in range(4))
+    w, gate = torch.randn(W, generator=g, device=device()), torch.randn(W, generator=g, device=device())
+    out, h = binding.block_norm(x, y, w, w, gate, 0.9, 0.4)
+    dx, dy, *sums = binding.block_norm_backward(gx, gh, out, y, w, w, gate, 0.9, 0.4)
+    for rows in (slice(0, 500), slice(33554432 - 250, 33554432 + 250), slice(T - 500, T)):
+        part = [t[rows].contiguous() for t in (x, y, gx, gh, out)]
+        o2, h2 = binding.block_norm(part[0], part[1], w, w, gate, 0.9, 0.4)
+        assert torch.equal(out[rows], o2) and torch.equal(h[rows], h2)
+        d2 = binding.block_norm_backward(part[2], part[3], part[4], part[1], w, w, gate, 0.9, 0.4)
+        assert torch.equal(dx[rows], d2[0]) and torch.equal(dy[rows], d2[1])
+    # dpre: sum of dh out r, in slices of 64 bits; a term is off by some 40 u, its sum in fp32 by 70 more
+    total = size = 0.0
+    for rows in torch.arange(T, device=device()).split(4000000):
+        o = out[rows].double()
+        term = gh[rows].double() * o / torch.sqrt((o * o).mean(1, keepdim=True) + 1e-6)
+        total, size = total + term.sum(0), size + term.abs().sum(0)
+    assert bool(((sums[0].double() - total).abs() <= 120 * 2.0 ** -24 * size).all())
+    del x, y, gx, gh, out, h, dx, dy
+    torch.cuda.empty_cache()
+
+
+def test_more_sequences_than_one_launch_takes():
+    """Nine million sequences of one row and none: the gate's gradient has a row for each."""
+    import torch
+    from tiled_dense_gemm_matmul_amd import binding
+    S, W = 9000001, 4
+    g = torch.Generator(device=device())
+    g.manual_seed(5)
+    lengths = torch.randint(0, 2, (S,), generator=g, device=device(), dtype=torch.int32)
+    cu = torch.cat((torch.zeros(1, dtype=torch.int32, device=device()), lengths.cumsum(0, dtype=torch.int32)))
+    T = int(cu[-1])
+    x, y, gx = (torch.randn((T, W), generator=g, device=device()) for _ in range(3))
+    gate = torch.randn((S, W), generator=g, device=device())
+    seq = torch.repeat_interleave(torch.arange(S, device=device()), lengths.long())
+    out, _ = binding.block_norm(x, y, gate=gate, cu_seqlens=cu)
+    assert torch.allclose(out, x + gate[seq] * y, rtol=1e-6, atol=1e-6)
+    dx, dy, _, _, dgate = binding.block_norm_backward(gx, None, out, y, gate=gate, cu_seqlens=cu)
+    assert torch.equal(dx, gx) and torch.equal(dy, gx * gate[seq])
+    want = torch.zeros_like(gate)
+    want[seq] = gx * y
+    assert torch.equal(dgate, want)
+    del x, y, gx, gate, out, dx, dy, dgate, want
+    torch.cuda.empty_cache()
+
+
 def test_refusals_on_the_device():
     import torch
     from tiled_dense_gemm_matmul_amd import binding as B

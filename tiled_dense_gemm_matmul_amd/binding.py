@@ -969,9 +969,9 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, positions, i
 
 # --- norms around a block (include/block_norm.h) ---
 
-_BLOCK_ARGS = struct.Struct("=8q3d 8q")
-_BLOCK_PROBLEM = struct.Struct("=8q3d")
-_BLOCK_BACKWARD_ARGS = struct.Struct("=8q3d 12q 3q 2q")
+_BLOCK_ARGS = struct.Struct("=9q3d 8q")
+_BLOCK_PROBLEM = struct.Struct("=9q3d")
+_BLOCK_BACKWARD_ARGS = struct.Struct("=9q3d 12q 4q 2q")
 
 
 def _rows(t, name, shape, device):
@@ -1001,6 +1001,14 @@ def _out_rows(t, name, shape, like):
     return t, (t.data_ptr(), shape[1])
 
 
+def _gate(t, name, shape, device):
+    """(pointer, row stride) of a [width] or [sequences, width] tensor with contiguous rows."""
+    if not isinstance(t, torch.Tensor) or t.shape != shape or t.device != device or t.dtype != torch.float32 \
+            or (t.stride(-1) != 1 and shape[-1] > 1):
+        raise ValueError(f"{name} must be a float32 tensor of shape {tuple(shape)} on {device} with contiguous rows")
+    return t.data_ptr(), t.stride(0)
+
+
 def _block_problem(rows, name, pre_weight, post_weight, gate, residual_scale, block_scale, cu_seqlens, eps):
     """The fields of block_norm_problem for the [tokens, width] tensor `rows`, and the gate's shape."""
     if not isinstance(rows, torch.Tensor) or rows.dim() != 2:
@@ -1008,7 +1016,7 @@ def _block_problem(rows, name, pre_weight, post_weight, gate, residual_scale, bl
     device = rows.device
     tokens, width = rows.shape
     cu, nseq = _cu_seqlens(cu_seqlens, device)
-    by_seq, shape_gate, pg = 0, None, 0
+    by_seq, shape_gate, pg, gate_st = 0, None, 0, 0
     if gate is not None:
         if not isinstance(gate, torch.Tensor) or gate.dim() not in (1, 2):
             raise TypeError("gate must be a torch.Tensor [width] or [sequences, width]")
@@ -1016,12 +1024,9 @@ def _block_problem(rows, name, pre_weight, post_weight, gate, residual_scale, bl
         if by_seq and cu_seqlens is None:
             raise ValueError("a gate for each sequence needs cu_seqlens")
         shape_gate = torch.Size((nseq, width) if by_seq else (width,))
-        if gate.shape != shape_gate or gate.device != device or gate.dtype != torch.float32 \
-                or not gate.is_contiguous():
-            raise ValueError(f"gate must be a contiguous float32 tensor of shape {tuple(shape_gate)} on {device}")
-        pg = gate.data_ptr()
+        pg, gate_st = _gate(gate, "gate", shape_gate, device)
     fields = (0 if pre_weight is None else _vector(pre_weight, "pre_weight", device, width),
-              0 if post_weight is None else _vector(post_weight, "post_weight", device, width), pg, by_seq, cu, nseq,
+              0 if post_weight is None else _vector(post_weight, "post_weight", device, width), pg, by_seq, gate_st, cu, nseq,
               tokens, width, float(residual_scale), float(block_scale), float(eps))
     return fields, shape_gate
 
@@ -1038,8 +1043,9 @@ def block_norm(x, y=None, pre_weight=None, post_weight=None, gate=None, residual
     where norm divides a row by its root mean square.  x, the residual stream,
     and y, the block's output, are [tokens, width] float32 with contiguous
     rows at any stride, width up to 8192.  gate is [width], or [sequences,
-    width] with cu_seqlens (int32 [sequences + 1] on the device, as for
-    attention; rows of no sequence get x_out and h 0), or None for 1.  Without
+    width], rows at any stride, with cu_seqlens (int32 [sequences + 1] on the
+    device, as for attention; rows of no sequence get x_out and h 0), or None
+    for 1.  Without
     y (in front of the first block, behind the last) x_out is x and only the
     norm is formed.  x_out and h_out may each be x or y.
     Returns (x_out, h)."""
@@ -1084,7 +1090,7 @@ def block_norm_backward(dx_out, dh, x_out, y=None, pre_weight=None, post_weight=
         raise ValueError("dpre_weight, dpost_weight and dgate need pre_weight, post_weight and gate")
     inputs = (*_rows(dx_out, "dx_out", shape, device), *_rows(dh, "dh", shape, device),
               *_rows(x_out, "x_out", shape, device), *_rows(y, "y", shape, device))
-    tdy, ppre, ppost, pgate = (0, 0), 0, 0, 0
+    tdy, ppre, ppost, pgate, dgate_st = (0, 0), 0, 0, 0, 0
     dx, tdx = _out_rows(dx, "dx", shape, x_out)
     if y is not None:
         dy, tdy = _out_rows(dy, "dy", shape, x_out)
@@ -1094,16 +1100,13 @@ def block_norm_backward(dx_out, dh, x_out, y=None, pre_weight=None, post_weight=
         dpost_weight, ppost = _out_vector(dpost_weight, "dpost_weight", post_weight)
     if gate is not None:
         if dgate is None:
-            dgate = torch.empty_like(gate)
-        elif not isinstance(dgate, torch.Tensor) or dgate.shape != shape_gate or dgate.device != device \
-                or dgate.dtype != torch.float32 or not dgate.is_contiguous():
-            raise ValueError(f"dgate must be a contiguous float32 tensor of shape {tuple(shape_gate)} on {device}")
-        pgate = dgate.data_ptr()
+            dgate = gate.new_empty(shape_gate)
+        pgate, dgate_st = _gate(dgate, "dgate", shape_gate, device)
     nbytes = load_library().block_norm_backward_workspace_bytes(_BLOCK_PROBLEM.pack(*fields))
     # scratch of this call's own: two captured graphs share nothing (none for
     # a problem that the call below refuses, with the reason)
     scratch = x_out.new_empty((nbytes // 4,)) if nbytes > 0 else None
     _call_packed("block_norm_backward",
-                 _BLOCK_BACKWARD_ARGS.pack(*fields, *inputs, *tdx, *tdy, ppre, ppost, pgate,
+                 _BLOCK_BACKWARD_ARGS.pack(*fields, *inputs, *tdx, *tdy, ppre, ppost, pgate, dgate_st,
                                            scratch.data_ptr() if nbytes > 0 else 0, max(0, nbytes)), device)
     return dx, dy, dpre_weight, dpost_weight, dgate

@@ -44,6 +44,7 @@ struct Matrix {
 struct Problem {
     const float *pre, *post, *gate;
     const int *cu;
+    int64_t gate_st;  // from one sequence's gate to the next
     int by_seq, nseq, tokens, width;
     float a, b, eps, inv_width;  // a, b: residual_scale, block_scale
 };
@@ -226,7 +227,7 @@ __global__ __launch_bounds__(LANES < 256 ? 256 : LANES) void block_norm_fwd(Prob
             for (int i = 0; i < NV; ++i) n.x[i] = n.x[i] * r * w.x[i];
         }
         if (p.gate) {
-            w.load(p.gate + (p.by_seq ? (int64_t)sequence_of(p, t) * p.width : 0), p.width);
+            w.load(p.gate + (p.by_seq ? sequence_of(p, t) * p.gate_st : 0), p.width);
 #pragma unroll
             for (int i = 0; i < NV; ++i) n.x[i] *= w.x[i];
         }
@@ -312,7 +313,7 @@ __global__ __launch_bounds__(LANES < 256 ? 256 : LANES, 2) void block_norm_bwd(P
                 int behind;
                 sequences.find(p, row, seq, behind);
                 end = min(end, max(row + 1, behind));
-                gate.load(p.gate + (int64_t)seq * p.width, p.width);
+                gate.load(p.gate + seq * p.gate_st, p.width);
             }
         }
         // a workgroup's rows go to its waves in turn
@@ -396,6 +397,7 @@ __global__ __launch_bounds__(LANES < 256 ? 256 : LANES, 2) void block_norm_bwd(P
 struct Sums {
     const float *pre_parts, *post_parts, *gate_parts;
     float *dpre, *dpost, *dgate;
+    int64_t dgate_st;
     int pitch, groups, chunk;
 };
 template <int EACH>
@@ -414,7 +416,7 @@ __global__ __launch_bounds__(16 * EACH) void block_norm_sums(Problem p, Sums a, 
         to = a.dpost;
     } else {
         parts = a.gate_parts;
-        to = a.dgate + job * p.width;
+        to = a.dgate + job * a.dgate_st;
         if (p.by_seq) {
             const int s0 = max(bound(p, (int)job), bound(p, 0)), s1 = min(bound(p, (int)job + 1), bound(p, p.nseq));
             lo = s0 / a.chunk + job;
@@ -445,6 +447,7 @@ __global__ __launch_bounds__(16 * EACH) void block_norm_sums(Problem p, Sums a, 
 
 // --- host ---
 
+constexpr int64_t kMost = (int64_t)1 << 56;  // elements from the first to the last
 constexpr int64_t kMaxTokens = (int64_t)1 << 30, kMaxWidth = 8192, kMaxSeqs = (int64_t)1 << 24;
 
 int check_problem(const block_norm_problem &p) {
@@ -454,6 +457,8 @@ int check_problem(const block_norm_problem &p) {
         !std::isfinite((float)p.block_scale) || !(p.eps >= 0.0) || !std::isfinite((float)p.eps))
         return GEMM_ERR_DTYPE;
     if (p.gate && p.gate_by_sequence && !p.cu_seqlens) return GEMM_ERR_NULL;
+    if (p.gate && p.gate_by_sequence && p.num_seqs > 1 && (p.gate_stride < 0 || p.gate_stride > kMost / p.num_seqs))
+        return GEMM_ERR_SHAPE;
     if (!aligned(p.pre_weight, 4) || !aligned(p.post_weight, 4) || !aligned(p.gate, 4) || !aligned(p.cu_seqlens, 4))
         return GEMM_ERR_ALIGN;
     return GEMM_OK;
@@ -469,15 +474,17 @@ struct Rows {
 };
 
 int check_rows(const Rows &r, int64_t tokens, int64_t width) {
-    const int64_t most = (int64_t)1 << 56;  // elements from the first to the last
-    if (r.t.token_stride < 0 || r.t.token_stride > most / std::max<int64_t>(tokens, 1)) return GEMM_ERR_SHAPE;
+    if (r.t.token_stride < 0 || r.t.token_stride > kMost / std::max<int64_t>(tokens, 1)) return GEMM_ERR_SHAPE;
     if (r.output && !rows_apart(r.view(), tokens, width)) return GEMM_ERR_SHAPE;
     return aligned(r.t.data, 4) ? GEMM_OK : GEMM_ERR_ALIGN;
 }
 
 int64_t cu_bytes(const block_norm_problem &p) { return p.cu_seqlens ? (p.num_seqs + 1) * 4 : 0; }
-int64_t gate_bytes(const block_norm_problem &p) {
-    return p.gate ? (p.gate_by_sequence ? p.num_seqs : 1) * p.width * 4 : 0;
+// Rows of the gate, and what they span `stride` elements apart.
+int64_t gate_rows(const block_norm_problem &p) { return !p.gate ? 0 : p.gate_by_sequence ? p.num_seqs : 1; }
+int64_t gate_bytes(const block_norm_problem &p, int64_t stride) {
+    const int64_t rows = gate_rows(p);
+    return rows > 0 ? ((rows - 1) * stride + p.width) * 4 : 0;
 }
 
 // Whether an output overlaps what all rows share.
@@ -485,7 +492,7 @@ bool covers_shared(const Rows &o, const block_norm_problem &p) {
     const View v = o.view();
     const int64_t T = p.tokens, W = p.width;
     return in_range(v, p.pre_weight, W * 4, T, W) || in_range(v, p.post_weight, W * 4, T, W) ||
-           in_range(v, p.gate, gate_bytes(p), T, W) || in_range(v, p.cu_seqlens, cu_bytes(p), T, W);
+           in_range(v, p.gate, gate_bytes(p, p.gate_stride), T, W) || in_range(v, p.cu_seqlens, cu_bytes(p), T, W);
 }
 
 // Whether an output overlaps an input without being the very same matrix.
@@ -504,6 +511,7 @@ Problem device_problem(const block_norm_problem &a) {
     p.gate = a.gate;
     p.cu = a.cu_seqlens;
     p.by_seq = (int)a.gate_by_sequence;
+    p.gate_st = a.gate_stride;
     p.nseq = a.cu_seqlens ? (int)a.num_seqs : 1;
     p.tokens = (int)a.tokens;
     p.width = (int)a.width;
@@ -626,7 +634,8 @@ int block_norm_backward(const block_norm_backward_args *args, void *stream) {
         (!a.p.gate && a.dgate))
         return GEMM_ERR_SHAPE;
     if (!y.there() && T > 0 && (a.p.residual_scale != 1.0 || a.p.block_scale != 1.0)) return GEMM_ERR_DTYPE;
-    const int64_t gates = gate_bytes(a.p);
+    const int64_t gates = gate_rows(a.p);
+    if (gates > 1 && (a.dgate_stride < W || a.dgate_stride > kMost / gates)) return GEMM_ERR_SHAPE;
     if ((a.p.pre_weight && !a.dpre_weight) || (a.p.post_weight && !a.dpost_weight) || (gates > 0 && !a.dgate))
         return GEMM_ERR_NULL;
     if (T > 0 && (!dx.there() || (y.there() && !dy.there()) || (a.p.pre_weight && (!dh.there() || !xo.there())) ||
@@ -638,8 +647,8 @@ int block_norm_backward(const block_norm_backward_args *args, void *stream) {
     if (need > 0 && (a.workspace == nullptr || a.workspace_bytes < need)) return GEMM_ERR_WORKSPACE;
     if (!aligned(a.workspace, 16)) return GEMM_ERR_ALIGN;
     // the sums and the scratch apart from one another and from everything else
-    const Span sums[4] = {{a.dpre_weight, W * 4}, {a.dpost_weight, W * 4}, {a.dgate, gates}, {a.workspace, need}};
-    const Span shared[4] = {{a.p.pre_weight, W * 4}, {a.p.post_weight, W * 4}, {a.p.gate, gates},
+    const Span sums[4] = {{a.dpre_weight, W * 4}, {a.dpost_weight, W * 4}, {a.dgate, gate_bytes(a.p, a.dgate_stride)}, {a.workspace, need}};
+    const Span shared[4] = {{a.p.pre_weight, W * 4}, {a.p.post_weight, W * 4}, {a.p.gate, gate_bytes(a.p, a.p.gate_stride)},
                             {a.p.cu_seqlens, cu_bytes(a.p)}};
     const Rows *all[6] = {&dxo, &dh, &xo, &y, &dx, &dy};
     if (T > 0) {
@@ -681,8 +690,8 @@ int block_norm_backward(const block_norm_backward_args *args, void *stream) {
 #undef BWD
     if (st != GEMM_OK) return st;
     const Sums s = {b.pre_parts, b.post_parts, b.gate_parts, a.dpre_weight, a.dpost_weight, a.dgate,
-                    (int)parts.pitch, (int)parts.groups, (int)parts.chunk};
-    const int64_t jobs = (p.pre ? 1 : 0) + (p.post ? 1 : 0) + gates / (W * 4), tiles = (W + 63) / 64;
+                    a.dgate_stride, (int)parts.pitch, (int)parts.groups, (int)parts.chunk};
+    const int64_t jobs = (p.pre ? 1 : 0) + (p.post ? 1 : 0) + gates, tiles = (W + 63) / 64;
     // Many parts of few results: four times the threads, each with its loads in
     // flight at once (8192 rows of 768: 30.2 us for the whole pass and 31.3; 512
     // rows, 128 parts: 9.0 and 8.5; gates of 2048 sequences: 132 and 56).
