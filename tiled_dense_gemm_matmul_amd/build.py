@@ -21,6 +21,7 @@ NORM_SRC = os.path.join(PKG, "csrc", "qk_norm_rope.hip")
 BLOCK_SRC = os.path.join(PKG, "csrc", "block_norm.hip")
 SRCS = [SRC, LOSS_SRC, ACT_SRC, ATTN_SRC, *SCORES_SRCS, NORM_SRC, BLOCK_SRC]
 INCLUDE = os.path.join(ROOT, "include")
+BUILD = os.path.join(ROOT, "_build")  # objects, for the time of a build
 LIB = os.path.join(PKG, "libgemmfwd.so")
 SYNC_LIB = os.path.join(PKG, "libgemmfwd_sync.so")
 PROBE_SRC = os.path.join(PKG, "csrc", "mfma_probe.hip")
@@ -41,7 +42,8 @@ def _hipcc(srcs, lib: str, verbose: bool, defines=()) -> str:
             print(" ".join(cmd), flush=True)
         subprocess.run(cmd, check=True)
 
-    with tempfile.TemporaryDirectory() as tmp, ThreadPoolExecutor(len(srcs)) as pool:
+    os.makedirs(BUILD, exist_ok=True)
+    with tempfile.TemporaryDirectory(dir=BUILD) as tmp, ThreadPoolExecutor(len(srcs)) as pool:
         objects = [os.path.join(tmp, os.path.basename(src) + ".o") for src in srcs]
         jobs = [pool.submit(run, [hipcc, *HIPCC_FLAGS, *[f"-D{d}" for d in defines], "-I", INCLUDE, "-c", src, "-o", o])
                 for src, o in zip(srcs, objects)]
