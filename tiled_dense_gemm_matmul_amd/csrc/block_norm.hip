@@ -5,7 +5,7 @@
 // x and y in, x_out and h out; backward: dx_out, dh, x_out and y in, dx and dy
 // out), and a row stays in registers between its sums.  7992 rows of 4096
 // forward run at 5.3 TB/s, where a large copy on this card reaches 5.1; 8192
-// rows of 768 backward take 30 us, 5.0 TB/s with the kernel behind it.  LANES lanes own a row,
+// rows of 768 backward take 31 us, 4.9 TB/s with the kernel behind it.  LANES lanes own a row,
 // each NV groups of 4 consecutive values: a wave rows of up to 1024 values,
 // four rows a workgroup, and a workgroup of 256 or 512 threads wider ones.
 //  * Accesses are 16 bytes wide at any 4-byte alignment; where the width is no
