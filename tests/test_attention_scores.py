@@ -125,6 +125,29 @@ def test_plans(plan, d, form, window):
 
 
 @pytest.mark.parametrize("plan", PLANS)
+@pytest.mark.parametrize("form", FORMS)
+def test_results_inside_one_buffer(plan, form):
+    """out over q inside the projection's output, and the gradients as columns
+    of one buffer, have the bits of results of their own; what lies beside
+    them stays."""
+    import torch
+    c = Case(6, form=form, d=64, **PLANS[plan])
+    out, lse = call(c)
+    want = call_backward(c, out, lse)
+    w = [s[1] * s[2] for s in c.shapes]
+    buf = torch.full((c.T, sum(w) + 4), SENTINEL, device=device())
+    views = [x.unflatten(1, s[1:]) for x, s in zip(buf[:, :-4].split(w, 1), c.shapes)]
+    got = call_backward(c, out, lse, dq=views[0], dk=views[1], dv=views[2])
+    assert all(torch.equal(x, y) for x, y in zip(want, got))
+    assert bool((buf[:, -4:] == SENTINEL).all())
+    k, v = c.k.clone(), c.v.clone()
+    over, lse2 = call(c, out=c.q)
+    assert over.data_ptr() == c.q.data_ptr() and torch.equal(over, out) and torch.equal(lse2, lse)
+    assert torch.equal(c.k.view(torch.int32), k.view(torch.int32))
+    assert torch.equal(c.v.view(torch.int32), v.view(torch.int32))
+
+
+@pytest.mark.parametrize("plan", PLANS)
 @pytest.mark.parametrize("form", ["cap", "slopes"])
 def test_both_ways(plan, form):
     """Without a causal mask: distances ahead count as those behind."""
