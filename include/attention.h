@@ -155,7 +155,9 @@ int attn_backward(const attn_backward_args *args, void *stream);
  *   dslopes[h] = - sum_{i,j} ds_ij |i - j|,
  *
  * with ds_ij (1 - tanh^2) in the place of ds_ij in dq and dk.  Distances are
- * fp32, slopes finite (others spread NaN over their head).
+ * fp32, slopes finite (others spread NaN over their head).  A key whose final
+ * score is below -2^30, as a bias by far distances makes it, has probability
+ * zero; a row's largest final score is less than 2^30 in magnitude, as above.
  */
 typedef struct attn_scores {
     double softcap;             /* 0: none; 1e-6 to 1e6, with scale / softcap normal in fp32 */

@@ -80,6 +80,13 @@ constexpr float kLn2 = 0.69314718055994530942f;
 // The running maximum of a row that has seen no key yet: low enough that any
 // score replaces it, finite so that differences with it are not NaN.
 constexpr float kNoMax = -3.0e38f;
+// The same with a bias, which pushes keys below any score: -2^30 log2(e), the
+// least score that is served.  Keys below it never become the reference and
+// add exp2 of a large negative number, which is zero.  (As a reference, rounded
+// to fp32, such a key was off by up to half an ulp of its score from the
+// exponent that it was taken from, 128 from 2^30 on: its exponential and the
+// sums were infinite, and NaN once they were rescaled by zero.)
+constexpr float kNoBiasedMax = -0x1p30f * kLog2e;
 
 struct Problem {
     const int *cu;
@@ -636,7 +643,7 @@ __global__ __launch_bounds__(256, DP > 64 ? 2 : DP == 64 && RB == 2 && FORM > kP
     for (int b = 0; b < RB; ++b) {
         Q[b].template load<EX>(rows_rsrc(q.p + h * q.sh, q.st, r0 + 16 * b, s1, p.d), q.st, p.d);
         O[b].clear();
-        top[b] = kNoMax;
+        top[b] = FORM & kBias ? kNoBiasedMax : kNoMax;
         sum[b] = 0.0f;
         largest[b] = -INFINITY;
     }
