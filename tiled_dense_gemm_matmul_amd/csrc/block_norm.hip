@@ -557,21 +557,25 @@ Parts parts_of(const block_norm_problem &p) {
     return r;
 }
 
-#define BLOCK_BY_WIDTH(LAUNCH)                                           \
-    do {                                                                 \
-        const int lanes_ = lanes_of(W);                                  \
-        const int nv_ = (int)((W + 4 * lanes_ - 1) / (4 * lanes_));      \
-        if (lanes_ == 64) BLOCK_BY_GROUPS(LAUNCH, 64);                   \
-        else if (lanes_ == 256) BLOCK_BY_GROUPS(LAUNCH, 256);            \
-        else if (nv_ == 3) BLOCK_BY_ODD(LAUNCH, 512, 3);                 \
-        else BLOCK_BY_ODD(LAUNCH, 512, 4);                               \
-    } while (0)
-#define BLOCK_BY_GROUPS(LAUNCH, LANES)              \
-    do {                                            \
-        if (nv_ == 1) BLOCK_BY_ODD(LAUNCH, LANES, 1);      \
-        else if (nv_ == 2) BLOCK_BY_ODD(LAUNCH, LANES, 2); \
-        else if (nv_ == 3) BLOCK_BY_ODD(LAUNCH, LANES, 3); \
-        else BLOCK_BY_ODD(LAUNCH, LANES, 4);        \
+// Groups of 4 values a lane: 1 to 4 of 64 lanes, and as many as the widths of
+// more lanes, which begin where fewer are full, need.
+#define BLOCK_BY_WIDTH(LAUNCH)                                      \
+    do {                                                            \
+        const int lanes_ = lanes_of(W);                             \
+        const int nv_ = (int)((W + 4 * lanes_ - 1) / (4 * lanes_)); \
+        if (lanes_ == 64) {                                         \
+            if (nv_ == 1) BLOCK_BY_ODD(LAUNCH, 64, 1);              \
+            else if (nv_ == 2) BLOCK_BY_ODD(LAUNCH, 64, 2);         \
+            else if (nv_ == 3) BLOCK_BY_ODD(LAUNCH, 64, 3);         \
+            else BLOCK_BY_ODD(LAUNCH, 64, 4);                       \
+        } else if (lanes_ == 256) {                                 \
+            if (nv_ == 2) BLOCK_BY_ODD(LAUNCH, 256, 2);             \
+            else if (nv_ == 3) BLOCK_BY_ODD(LAUNCH, 256, 3);        \
+            else BLOCK_BY_ODD(LAUNCH, 256, 4);                      \
+        } else {                                                    \
+            if (nv_ == 3) BLOCK_BY_ODD(LAUNCH, 512, 3);             \
+            else BLOCK_BY_ODD(LAUNCH, 512, 4);                      \
+        }                                                           \
     } while (0)
 #define BLOCK_BY_ODD(LAUNCH, LANES, NV)             \
     do {                                            \
