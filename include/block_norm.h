@@ -38,9 +38,10 @@
  * of a row in elements; a row's values are contiguous, addresses multiples of
  * 4 bytes.  All device pointers are owned by the caller; a call allocates
  * nothing and only enqueues work on `stream` (a hipStream_t, NULL for the null
- * stream).  A row's sums are fp32, the sums over rows fp32 over at most 64
- * rows and fp64 from there, each in a fixed order: results are bitwise
- * reproducible.
+ * stream).  A row's sums are fp32.  The sums over rows are fp32 over at most 64
+ * rows of a wave or workgroup, joined in fp32 over four waves for widths up to
+ * 1024 (256 rows), and fp64 from there.  Each has a fixed order: results are
+ * bitwise reproducible.
  *
  * Errors are returned synchronously, before anything is enqueued, except
  * GEMM_ERR_LAUNCH from a later one of a call's launches (the status values are
@@ -84,11 +85,11 @@ typedef struct block_norm_problem {
  * GEMM_ERR_NULL for a missing array (or neither y nor pre_weight),
  * GEMM_ERR_SHAPE for sizes outside the above (tokens < 2^30, num_seqs < 2^24),
  * for strides that are negative, overlap an output's own rows or reach 2^56
- * elements over all rows, and for
- * arrays that the call has no use for (x_out, post_weight or gate without y, h
- * without pre_weight), GEMM_ERR_ALIGN, GEMM_ERR_DTYPE for a scale, eps or flag
- * outside the above, GEMM_ERR_ALIAS, and GEMM_ERR_LAUNCH when the runtime
- * rejects the launch.  tokens == 0 enqueues nothing.
+ * elements over all rows, and for arrays that the call has no use for (x_out,
+ * post_weight or gate without y, h without pre_weight), GEMM_ERR_ALIGN,
+ * GEMM_ERR_DTYPE for a scale, eps or flag outside the above, GEMM_ERR_ALIAS,
+ * and GEMM_ERR_LAUNCH when the runtime rejects the launch.  tokens == 0
+ * enqueues nothing.
  */
 typedef struct block_norm_args {
     block_norm_problem p;
@@ -100,9 +101,9 @@ int block_norm(const block_norm_args *args, void *stream);
  * dx, dy (with y) and the gradients of the weights and the gate that the call
  * has, [width], [width] and the gate's shape, the latter's rows dgate_stride
  * elements apart (at least width with a gate for each of several sequences).
- * dx_out may be NULL only
- * with pre_weight.  dx and dy may each be the very same matrix as dx_out, dh,
- * x_out or y; they may not overlap one another or, otherwise, anything else.
+ * dx_out may be NULL only with pre_weight.  dx and dy may each be the very same
+ * matrix as dx_out, dh, x_out or y; they may not overlap one another or,
+ * otherwise, anything else.
  * The workspace holds at least block_norm_backward_workspace_bytes bytes (-1
  * for sizes the call refuses), 16-byte aligned, of any contents; calls that
  * may run at the same time need one each (GEMM_ERR_WORKSPACE when it is too

@@ -3,21 +3,26 @@
 //
 // The work is bound by memory: every value is read and written once (forward:
 // x and y in, x_out and h out; backward: dx_out, dh, x_out and y in, dx and dy
-// out), and a row stays in registers between its sums.  7992 rows of 4096
-// forward run at 5.3 TB/s, where a large copy on this card reaches 5.1; 8192
-// rows of 768 backward take 31 us, 4.9 TB/s with the kernel behind it.  LANES lanes own a row,
-// each NV groups of 4 consecutive values: a wave rows of up to 1024 values,
-// four rows a workgroup, and a workgroup of 256 or 512 threads wider ones.
+// out), and a row stays in registers between its sums.  With inputs in no cache
+// 7992 rows of 4096 forward run at 5.3 TB/s, where a large copy on this card
+// reaches 5.1, and 8192 rows of 768 backward take 36 us, 4.2 TB/s with the
+// kernel behind it.  (Other times below are of calls repeated on the same
+// arrays, part of which the last-level cache holds: 31 us, 4.9 TB/s, for
+// these.)  LANES lanes own a row, each NV groups of 4 consecutive values: a
+// wave rows of up to 1024 values, four rows a workgroup, and a workgroup of 256
+// or 512 threads wider ones.
 //  * Accesses are 16 bytes wide at any 4-byte alignment; where the width is no
 //    multiple of 4, one lane takes a row's last values one by one (EX false),
 //    behind the loads of all others (8192 rows of 1150 backward 49 us; 69 with
 //    the choice inside every load).
 //  * The backward pass sums over rows for the weights and the gate.  A
 //    workgroup owns a run of rows and keeps its sums in registers (fp32, 64
-//    rows a lane at most), the gate's until the sequence ends; it writes them
-//    to parts of its own, and a second kernel adds the parts in fp64.  Part w +
-//    b holds workgroup w's sum over sequence b, which no other pair shares: b
-//    does not fall as w grows, so w + b grows with every step of either.
+//    rows a lane at most), the gate's until the sequence ends; it adds those of
+//    its four waves, where each has rows of its own, in fp32 (one part a wave
+//    would be four times the parts), writes them to parts of its own, and a
+//    second kernel adds the parts in fp64.  Part w + b holds workgroup w's sum
+//    over sequence b, which no other pair shares: b does not fall as w grows, so
+//    w + b grows with every step of either.
 
 #include <hip/hip_runtime.h>
 #include <stddef.h>
@@ -534,7 +539,8 @@ int lanes_of(int64_t width) { return width <= 1024 ? 64 : width <= 4096 ? 256 : 
 // 64 rows a lane at most, which bounds the fp32 sums.  Narrow rows take more of
 // them, wide ones, of 512 threads, fewer: us with 256, 512 and 1024, 16384 rows
 // of 128: -, 18.5, 16.6 (2048: 20.0); 8192 rows of 768: -, 30.2, 32.8; 4096
-// rows of 8192: 172, 182, -.
+// rows of 2048: 43.5, 38.7, -; of 4096: 89.1, 93.1, -; of 4100: 94.5, 99.4, -;
+// of 8192: 172, 181, -.
 int64_t chunk_of(const block_norm_problem &p) {
     const int64_t rows = std::max<int64_t>(1, 256 / lanes_of(p.width));
     const int64_t most = p.width <= 256 ? 1024 : p.width <= 4096 ? 512 : 256;
