@@ -1,6 +1,5 @@
-// Attention whose scores are capped by a tanh, with or
-// without a prefix that all rows see (definitions in attention.h, kernels in
-// attention_kernels.h).
+// Attention whose scores are capped by a tanh, with or without a prefix that
+// all rows see (definitions in attention.h, kernels in attention_kernels.h).
 
 #include "attention_kernels.h"
 #include "attention_scores.h"
