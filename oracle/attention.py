@@ -235,8 +235,9 @@ def _final_scores(q, k, scale, softcap, slope):
     away = np.abs(np.arange(n)[:, None] - np.arange(n)[None, :]).astype(np.float64)
     s, steep = raw, np.ones((n, n))
     if softcap:
-        t = np.tanh(raw / softcap)
-        s, steep = softcap * t, 1.0 - t * t
+        x = raw / softcap
+        # 1 - tanh^2 without the cancellation that leaves nothing of it from |x| = 19 on
+        s, steep = softcap * np.tanh(x), 1.0 / np.cosh(np.minimum(np.abs(x), 350.0)) ** 2
         # what the argument is off by, which the cap's slope shrinks, and the tanh's own 8 u
         err = steep * (err + 2 * U * np.abs(raw)) + 8 * U * np.abs(s) + err * err / softcap
     if slope:

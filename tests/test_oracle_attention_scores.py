@@ -133,3 +133,20 @@ def test_an_fp32_evaluation_stays_inside_the_bounds():
             s = 4.0 * torch.tanh(x @ y.T * np.float32(d ** -0.5) / 4.0) - float(form["slopes"][h]) * (i[:, None] - i).abs()
             p = torch.softmax(s.masked_fill(~see, -np.inf), 1)
             assert OA.compare((p @ z).numpy(), ro[a:e, h], eo[a:e, h])["fails"] == 0
+
+
+def test_the_cap_keeps_its_derivative_where_it_saturates():
+    """1 - tanh^2 is 4 e / (1 + e)^2, e = exp(-2 |x|): far below what is left of 1 - t t in 64 bits, and not zero.
+    A row that sees one key alone has ds = 0, which fp32 forms to some roundings of dout . v; times that derivative
+    they are what dq may be off by."""
+    from decimal import Decimal
+    for x in (0.0, 0.3, -2.0, 9.0, 18.0, -19.5, 25.0, 100.0, 300.0):
+        steep = OA._final_scores(np.array([[x]]), np.array([[1.0]]), 1.0, 1.0, 0.0)[1][0, 0]
+        e = (Decimal(-2) * abs(Decimal(x))).exp()
+        assert abs(Decimal(steep) / (4 * e / (1 + e) ** 2) - 1) < Decimal(1e-13), x
+    assert OA._final_scores(np.array([[1e30]]), np.array([[1.0]]), 1.0, 1.0, 0.0)[1][0, 0] < 1e-300
+    q, k, v, g = np.full((1, 1, 4), 12.5), np.ones((1, 1, 4)), np.full((1, 1, 4), 0.5), np.ones((1, 1, 4))
+    out, lse, _, _ = OA.scored_attention(q, k, v, softcap=1.0)
+    dq, _, _, _, e_dq = OA.scored_attention_backward(g, q, k, v, out, lse, softcap=1.0)[:5]
+    # ds of three roundings of dout . v = 2, the derivative at x = 25, scale 1/2
+    assert not dq.any() and (e_dq > 0.5 * 4 * np.exp(-50.0) * 3 * 2.0 ** -24 * 2).all() and (e_dq < 1e-25).all()
