@@ -142,7 +142,7 @@ def _angles(positions, inv_freq, axis=None):
     if axis is not None and np.abs(np.asarray(positions)).max(initial=0) > 1 << 32:
         pos = np.asarray(positions)
         cols = [_reduced(pos[a], np.asarray(inv_freq)[p:p + 1]) for p, a in enumerate(np.asarray(axis))]
-        return np.concatenate(cols, 1)
+        return np.concatenate([np.empty((pos.shape[1], 0), dtype=np.longdouble), *cols], 1)
     pos, freq = np.asarray(positions).astype(np.longdouble), np.asarray(inv_freq).astype(np.longdouble)
     if axis is None:
         return pos[:, None] * freq[None, :]

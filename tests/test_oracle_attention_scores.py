@@ -150,3 +150,12 @@ def test_the_cap_keeps_its_derivative_where_it_saturates():
     dq, _, _, _, e_dq = OA.scored_attention_backward(g, q, k, v, out, lse, softcap=1.0)[:5]
     # ds of three roundings of dout . v = 2, the derivative at x = 25, scale 1/2
     assert not dq.any() and (e_dq > 0.5 * 4 * np.exp(-50.0) * 3 * 2.0 ** -24 * 2).all() and (e_dq < 1e-25).all()
+
+
+@pytest.mark.parametrize("axes", [1, 3])
+def test_far_positions_without_a_rotated_pair(axes):
+    """Heads that are normed and not turned, at positions of any size."""
+    r = np.random.default_rng(0)
+    x, w, pos = r.standard_normal((5, 2, 8)), r.standard_normal(8), np.full((axes, 5), 1 << 50)
+    y = OA.qk_norm_rope(x, w, pos, np.zeros(0), axis=np.zeros(0, np.int32))[0]
+    assert np.array_equal(y, OA.qk_norm_rope(x, w, pos[0] * 0, np.zeros(0))[0])
